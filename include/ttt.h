@@ -90,11 +90,14 @@ typedef enum {
   TTT_ERR_ALLOC = -8,       /* stream-ordered scratch allocation failed */
   TTT_ERR_ARG = -9,         /* scalar argument out of range (chunk, enums) */
   TTT_ERR_SCRATCH = -10,    /* scratch need exceeds lact_swiglu_fwd_noalloc's fixed pool */
-  TTT_ERR_BOUNDS = -11      /* debug-bounds build only: a kernel index check failed (the
-                               access was skipped); reported by ttt_get_device_status */
+  TTT_ERR_BOUNDS = -11      /* reported by ttt_get_device_status: an entry of a cu_seqlens or
+                               slots tensor was out of range (what it names was skipped), or,
+                               in the debug-bounds build, a kernel index check failed */
 } ttt_status;
 
-typedef enum { TTT_F32 = 0, TTT_BF16 = 1 } ttt_dtype;
+/* TTT_I32 and TTT_E4M3 appear only where an entry point names them (sequence
+ * offsets, state slots, 8-bit norm outputs). */
+typedef enum { TTT_F32 = 0, TTT_BF16 = 1, TTT_I32 = 2, TTT_E4M3 = 3 } ttt_dtype;
 
 typedef enum { TTT_LOSS_MSE = 0, TTT_LOSS_NEG_DOT = 1 } ttt_loss;
 
@@ -367,6 +370,170 @@ ttt_status lact_swiglu_window_fwd(const ttt_tensor* q, const ttt_tensor* k, cons
                                   const ttt_tensor* W2, const ttt_tensor* W3, int32_t chunk,
                                   int32_t update_rule, int32_t window, const ttt_tensor* out,
                                   void* stream);
+
+/*
+ * ---- The recurrent block around the layers above: norm, convolution, scan ----
+ *
+ * Tokens are [B,H,T,d] under the conventions at the top of this file; a block
+ * of width D with [B,T,D] storage passes H = 1, d = D, and heads that lie
+ * beside one another in storage are described by strides. One element type
+ * (fp32 or bf16) for all token tensors of a call; parameters are fp32.
+ * Arithmetic, sums and states are fp32; a 16-bit output is rounded once.
+ *
+ * Packed sequences: with cu_seqlens (TTT_I32, contiguous, [S+1], on the
+ * device) B is 1 and sequence i is the tokens cu_seqlens[i] ..
+ * cu_seqlens[i+1]-1 of the T packed ones; it may be empty. Sequences share
+ * nothing: each starts from its own row of the [S,...] state tensors. Token
+ * rows behind the last sequence are neither read nor written. The offsets
+ * must not decrease and lie in [0, T]. Where they break this nothing outside
+ * the tensors is touched and ttt_get_device_status reports TTT_ERR_BOUNDS,
+ * but which of the call's sequences are computed is not specified.
+ * Without cu_seqlens there are S = B sequences of T tokens.
+ *
+ * Slots: the single-token forms keep the states of many sequences in a pool
+ * of S places. slots (TTT_I32, contiguous, [B], on the device) gives each
+ * row's place; NULL means row b has place b (S = B). A row with slot -1 (a
+ * padded batch) does nothing: its output row is left as it was. Any other
+ * value outside [0, S) does nothing either and is reported as TTT_ERR_BOUNDS.
+ * Rows that name the same place are applied one after another in row order,
+ * as consecutive tokens of that sequence. The state is updated in place.
+ *
+ * Workspaces come stream-ordered from the library's pool (failure ->
+ * TTT_ERR_ALLOC). Results do not depend on scheduling: no atomics in sums.
+ */
+
+/*
+ * Root-mean-square norm over d, optionally of the sum with a residual:
+ *   s = x (+ residual),  out = s * (mean(s^2) + eps)^(-1/2) * weight.
+ * With weight = 1/sqrt(d) and eps = 0 this is the L2 normalisation per head
+ * that ttt_linear_fwd and the LaCT layers expect of q and k.
+ *  x, residual  [B,H,T,d]; residual NULLable
+ *  weight       [d] or [H,d] fp32 contiguous
+ *  eps          finite, >= 0 (a row of zeros with eps = 0 gives zeros)
+ *  out          [B,H,T,d] of x's type, or TTT_E4M3: then per token
+ *               scale = max_d |out| / 448 and the stored 8-bit values are
+ *               out / scale rounded to the nearest (ties to even); a token
+ *               of zeros has scale 0
+ *  scale        [B,H,T] fp32, any strides; required for a TTT_E4M3 out and
+ *               NULL otherwise
+ *  residual_out NULL or [B,H,T,d] of x's type: s (requires residual)
+ * d <= 16384 (TTT_ERR_UNSUPPORTED otherwise).
+ */
+ttt_status rms_norm_fwd(const ttt_tensor* x, const ttt_tensor* residual,
+                        const ttt_tensor* weight, float eps, const ttt_tensor* out,
+                        const ttt_tensor* scale, const ttt_tensor* residual_out, void* stream);
+
+/*
+ * Backward of rms_norm_fwd, from the summed input h = x (+ residual) (the
+ * forward's residual_out, or x): with r = (mean(h^2) + eps)^(-1/2),
+ *   dh = r (dy w - h r mean(dy w h r)) + dres,  dweight = sum dy h r.
+ * dh is the gradient of x and of the residual alike.
+ *  h, dy   [B,H,T,d]; dres NULL or [B,H,T,d]: the gradient that reaches h
+ *          through residual_out; dh [B,H,T,d]; all of h's type
+ *  dweight weight's shape, fp32 contiguous (summed over what shares it)
+ */
+ttt_status rms_norm_bwd(const ttt_tensor* h, const ttt_tensor* weight, const ttt_tensor* dy,
+                        const ttt_tensor* dres, float eps, const ttt_tensor* dh,
+                        const ttt_tensor* dweight, void* stream);
+
+/*
+ * Short causal depthwise convolution along T:
+ *   p_t = bias + sum_{j<K} weight[j] x_{t-K+1+j},  out_t = silu(p_t) or p_t,
+ * each sequence preceded by its state0 (its last K-1 inputs so far), or zeros.
+ *  x, out   [B,H,T,d]
+ *  weight   [H,d,K] fp32 contiguous, 1 <= K <= 8; bias NULL or [H,d]
+ *  state0   NULL or [S,H,K-1,d] of x's type, token strides (rows in time order)
+ *  cu_seqlens NULL or [S+1] (see above); silu 0 or 1
+ *  state_final NULL or [S,H,K-1,d] of x's type: the last K-1 inputs, for the
+ *           next call's state0 or causal_conv_step
+ */
+ttt_status causal_conv_fwd(const ttt_tensor* x, const ttt_tensor* weight, const ttt_tensor* bias,
+                           const ttt_tensor* state0, const ttt_tensor* cu_seqlens, int32_t silu,
+                           const ttt_tensor* out, const ttt_tensor* state_final, void* stream);
+
+/*
+ * Backward of causal_conv_fwd: with dp_t = dy_t silu'(p_t) (dy_t without silu),
+ *   dx_s = sum_j weight[j] dp_{s+K-1-j}, dweight[j] = sum_t dp_t x_{t-K+1+j},
+ *   dbias = sum_t dp_t, dstate0 like dx; dstate_final adds to the inputs that
+ *   state_final holds.
+ *  dy, dx   [B,H,T,d]; dstate_final NULL or as state_final
+ *  dweight  [H,d,K], dbias [H,d] (required iff bias is given): fp32 contiguous
+ *  dstate0  NULL or as state0 (requires state0)
+ */
+ttt_status causal_conv_bwd(const ttt_tensor* x, const ttt_tensor* weight, const ttt_tensor* bias,
+                           const ttt_tensor* state0, const ttt_tensor* cu_seqlens, int32_t silu,
+                           const ttt_tensor* dy, const ttt_tensor* dstate_final,
+                           const ttt_tensor* dx, const ttt_tensor* dweight,
+                           const ttt_tensor* dbias, const ttt_tensor* dstate0, void* stream);
+
+/*
+ * One token of causal_conv_fwd for each of B sequences, from a pool of states.
+ *  x, out  [B,H,1,d]; state [S,H,K-1,d] of x's type, updated in place
+ *  slots   NULL or [B] (see above)
+ */
+ttt_status causal_conv_step(const ttt_tensor* x, const ttt_tensor* state, const ttt_tensor* slots,
+                            const ttt_tensor* weight, const ttt_tensor* bias, int32_t silu,
+                            const ttt_tensor* out, void* stream);
+
+/*
+ * Selective state space scan, a recurrence with a diagonal, input-dependent
+ * decay beside the inner-product layer of ttt_linear_fwd (whose state never
+ * decays). Per channel (h, c), with N states and D_t = softplus(dt_t +
+ * dt_bias) (or dt_t + dt_bias without softplus):
+ *   s_t = exp(D_t A) s_{t-1} + D_t x_t B_t,   y_t = <C_t, s_t> + D x_t,
+ *   out_t = y_t silu(z_t)  (out_t = y_t without z).
+ *  x, dt, out [B,H,T,d]; z NULL or [B,H,T,d]
+ *  A       [H,d,N] fp32 contiguous, 1 <= N <= 64 (negative in a stable layer)
+ *  Bm, Cm  [B,G,T,N], H a multiple of G: head h reads group h / (H/G)
+ *  D, dt_bias  NULL or [H,d] fp32 contiguous
+ *  h0      NULL (zero) or [S,H,d,N] fp32 contiguous; cu_seqlens as above
+ *  softplus 0 or 1
+ *  h_final NULL or [S,H,d,N] fp32 contiguous: the state after the last token
+ */
+ttt_status selective_scan_fwd(const ttt_tensor* x, const ttt_tensor* dt, const ttt_tensor* A,
+                              const ttt_tensor* Bm, const ttt_tensor* Cm, const ttt_tensor* D,
+                              const ttt_tensor* z, const ttt_tensor* dt_bias,
+                              const ttt_tensor* h0, const ttt_tensor* cu_seqlens,
+                              int32_t softplus, const ttt_tensor* out,
+                              const ttt_tensor* h_final, void* stream);
+
+/*
+ * Backward of selective_scan_fwd: with e_t the gradient of y_t and
+ * g_t = C_t e_t + exp(D_{t+1} A) g_{t+1} (dh_final at a sequence's end),
+ *   dC_t = sum_c e_t s_t, dB_t = sum_c g_t D_t x_t,
+ *   dx_t = D_t <g_t, B_t> + D e_t,
+ *   dD_t = <g_t, A exp(D_t A) s_{t-1}> + x_t <g_t, B_t>, ddt_t = dD_t softplus',
+ *   dA = sum_t g_t D_t exp(D_t A) s_{t-1}, dh0 = exp(D_0 A) g_0.
+ * The states are computed again from the inputs.
+ *  dy      [B,H,T,d]; dh_final NULL or as h_final
+ *  dx, ddt [B,H,T,d]; dz as z (required iff z is given)
+ *  dA [H,d,N] fp32; dBm, dCm [B,G,T,N] of x's type, summed over the channels
+ *  that share them; dD, ddt_bias [H,d] fp32 (each required iff its input is
+ *  given); dh0 NULL or as h0 (requires h0)
+ * Workspace: at most 12 bytes x B*H*T*d*ceil(N/16), plus 1 MB or so.
+ */
+ttt_status selective_scan_bwd(const ttt_tensor* x, const ttt_tensor* dt, const ttt_tensor* A,
+                              const ttt_tensor* Bm, const ttt_tensor* Cm, const ttt_tensor* D,
+                              const ttt_tensor* z, const ttt_tensor* dt_bias,
+                              const ttt_tensor* h0, const ttt_tensor* cu_seqlens,
+                              int32_t softplus, const ttt_tensor* dy,
+                              const ttt_tensor* dh_final, const ttt_tensor* dx,
+                              const ttt_tensor* ddt, const ttt_tensor* dA,
+                              const ttt_tensor* dBm, const ttt_tensor* dCm,
+                              const ttt_tensor* dD, const ttt_tensor* dz,
+                              const ttt_tensor* ddt_bias, const ttt_tensor* dh0, void* stream);
+
+/*
+ * One token of selective_scan_fwd for each of B sequences, from a pool of
+ * states.
+ *  x, dt, out [B,H,1,d], z NULL or [B,H,1,d], Bm, Cm [B,G,1,N]
+ *  state [S,H,d,N] fp32 contiguous, updated in place; slots NULL or [B]
+ */
+ttt_status selective_scan_step(const ttt_tensor* x, const ttt_tensor* dt, const ttt_tensor* A,
+                               const ttt_tensor* Bm, const ttt_tensor* Cm, const ttt_tensor* D,
+                               const ttt_tensor* z, const ttt_tensor* dt_bias,
+                               const ttt_tensor* state, const ttt_tensor* slots,
+                               int32_t softplus, const ttt_tensor* out, void* stream);
 
 /* Static description of a status code (never NULL). */
 const char* ttt_status_string(int32_t status);

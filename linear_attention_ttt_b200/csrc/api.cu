@@ -1,6 +1,9 @@
 // C ABI of libttt_b200: argument validation and dispatch (see include/ttt.h).
+#include <algorithm>
+#include <cmath>
 #include <mutex>
 
+#include "block.cuh"
 #include "common.cuh"
 #include "lact.cuh"
 
@@ -26,7 +29,7 @@ int* device_status_ptr() {
   return g_status_ptr[dev];
 }
 
-size_t elem_size(int32_t dtype) { return dtype == TTT_BF16 ? 2 : 4; }
+size_t elem_size(int32_t dtype) { return dtype == TTT_BF16 ? 2 : dtype == TTT_E4M3 ? 1 : 4; }
 
 // Sizes the kernels index with 32-bit integers: tokens per sequence (tile
 // starts plus one tile stay below 2^31) and (batch, head) pairs (grids of a
@@ -175,7 +178,7 @@ const char* ttt_status_string(int32_t s) {
     case TTT_ERR_ALLOC: return "stream-ordered scratch allocation failed";
     case TTT_ERR_ARG: return "scalar argument out of range";
     case TTT_ERR_SCRATCH: return "scratch need exceeds the fixed pool of lact_swiglu_fwd_noalloc";
-    case TTT_ERR_BOUNDS: return "a kernel index check of the debug-bounds build failed";
+    case TTT_ERR_BOUNDS: return "a sequence offset, a slot or (debug-bounds build) a kernel index was out of range";
     default: return "unknown status";
   }
 }
@@ -811,6 +814,573 @@ ttt_status lact_swiglu_bwd(const ttt_tensor* q, const ttt_tensor* k, const ttt_t
   g.dW3 = static_cast<float*>(dW3->data);
   if ((st = ttt::lact_attach_status(&a)) != TTT_OK) return st;
   return ttt::lact_backward(a, g, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
+
+// ---- the recurrent block: norm, convolution, scan ----------------------------
+
+namespace {
+
+// Sizes of a block call's tokens.
+struct Dims {
+  int64_t B, H, T, d;
+};
+
+// Channel tiles of 32 that the scan's grids count with 32-bit integers.
+constexpr int64_t kMaxTiles = (int64_t)1 << 24;
+constexpr int64_t kMaxBlockWidth = (int64_t)1 << 20;
+
+ttt_status token_dims(const ttt_tensor* x, Dims* n) {
+  if (x->ndim != 4) return TTT_ERR_SHAPE;
+  *n = {x->shape[0], x->shape[1], x->shape[2], x->shape[3]};
+  if (n->B < 1 || n->H < 1 || n->T < 0 || n->d < 1) return TTT_ERR_SHAPE;
+  if (n->B > kMaxHeads || n->H > kMaxHeads || n->B * n->H > kMaxHeads || n->T > kMaxT ||
+      n->d > kMaxBlockWidth || n->B * n->H * ((n->d + 31) / 32) > kMaxTiles ||
+      n->B * n->H * n->T > ((int64_t)1 << 40))
+    return TTT_ERR_UNSUPPORTED;
+  if (x->dtype != TTT_F32 && x->dtype != TTT_BF16) return TTT_ERR_DTYPE;
+  return TTT_OK;
+}
+
+// Whether no two elements of a tensor share an address (by strides, smallest first).
+bool distinct(const ttt_tensor* t) {
+  if (empty(t)) return true;
+  int64_t st[4], sh[4];
+  int n = 0;
+  for (int i = 0; i < t->ndim; ++i) {
+    if (t->shape[i] == 1) continue;
+    st[n] = t->stride[i];
+    sh[n++] = t->shape[i];
+  }
+  for (int i = 0; i < n; ++i)
+    for (int j = i + 1; j < n; ++j)
+      if (st[j] < st[i]) {
+        std::swap(st[i], st[j]);
+        std::swap(sh[i], sh[j]);
+      }
+  int64_t reach = 1;
+  for (int i = 0; i < n; ++i) {
+    if (st[i] < reach) return false;
+    reach += (sh[i] - 1) * st[i];
+  }
+  return true;
+}
+
+ttt_status check_out_tokens(const ttt_tensor* t, const Dims& n, int64_t d, int32_t dtype) {
+  const ttt_status st = check_tokens(t, n.B, n.H, n.T, d, dtype);
+  if (st != TTT_OK) return st;
+  return distinct(t) ? TTT_OK : TTT_ERR_LAYOUT;
+}
+
+// Contiguous fp32 tensor of the given shape; NULL passes when optional.
+ttt_status check_f32(const ttt_tensor* t, int ndim, const int64_t* shape, bool optional) {
+  if (!t) return optional ? TTT_OK : TTT_ERR_NULL;
+  if (t->ndim != ndim) return TTT_ERR_SHAPE;
+  for (int i = 0; i < ndim; ++i)
+    if (t->shape[i] != shape[i]) return TTT_ERR_SHAPE;
+  if (t->dtype != TTT_F32) return TTT_ERR_DTYPE;
+  if (empty(t)) return TTT_OK;
+  if (!t->data) return TTT_ERR_NULL;
+  if (!contiguous(t) || !aligned16(t->data)) return TTT_ERR_LAYOUT;
+  return TTT_OK;
+}
+
+// Contiguous int32 vector (sequence offsets, slots); *n gets its length.
+ttt_status check_i32(const ttt_tensor* t, int64_t* n) {
+  if (t->ndim != 1) return TTT_ERR_SHAPE;
+  if (t->dtype != TTT_I32) return TTT_ERR_DTYPE;
+  *n = t->shape[0];
+  if (*n < 1) return TTT_ERR_SHAPE;
+  if (!t->data) return TTT_ERR_NULL;
+  if ((t->stride[0] != 1 && *n > 1) || (reinterpret_cast<uintptr_t>(t->data) & 3u)) return TTT_ERR_LAYOUT;
+  return TTT_OK;
+}
+
+// cu_seqlens against the tokens: S sequences.
+ttt_status check_seqs(const ttt_tensor* cu, const Dims& n, ttt::Seqs* q) {
+  *q = {nullptr, (int)n.B};
+  if (!cu) return TTT_OK;
+  int64_t len = 0;
+  const ttt_status st = check_i32(cu, &len);
+  if (st != TTT_OK) return st;
+  if (n.B != 1 || len < 2) return TTT_ERR_SHAPE;
+  if (len - 1 > kMaxHeads || (len - 1) * n.H > kMaxHeads) return TTT_ERR_UNSUPPORTED;
+  *q = {static_cast<const int32_t*>(cu->data), (int)(len - 1)};
+  return TTT_OK;
+}
+
+ttt_status check_slots(const ttt_tensor* slots, const Dims& n, int64_t S, const int32_t** p) {
+  *p = nullptr;
+  if (S > kMaxHeads || S * n.H > kMaxHeads || n.B > 65535) return TTT_ERR_UNSUPPORTED;
+  if (!slots) return S == n.B ? TTT_OK : TTT_ERR_SHAPE;
+  int64_t len = 0;
+  const ttt_status st = check_i32(slots, &len);
+  if (st != TTT_OK) return st;
+  if (len != n.B) return TTT_ERR_SHAPE;
+  *p = static_cast<const int32_t*>(slots->data);
+  return TTT_OK;
+}
+
+template <size_t NI, size_t NO>
+bool clash(const ttt_tensor* const (&ins)[NI], const ttt_tensor* const (&outs)[NO]) {
+  for (size_t i = 0; i < NO; ++i) {
+    for (const ttt_tensor* in : ins)
+      if (overlaps(outs[i], in)) return true;
+    for (size_t j = i + 1; j < NO; ++j)
+      if (overlaps(outs[i], outs[j])) return true;
+  }
+  return false;
+}
+
+ttt::TokView view_or_null(const ttt_tensor* t) {
+  return t ? view(t) : ttt::TokView{nullptr, 0, 0, 0};
+}
+ttt::TokViewMut view_mut(const ttt_tensor* t) {
+  return t ? ttt::TokViewMut{t->data, t->stride[0], t->stride[1], t->stride[2]}
+           : ttt::TokViewMut{nullptr, 0, 0, 0};
+}
+ttt::RowsView rows_view(const ttt_tensor* t) {
+  return t ? ttt::RowsView{t->data, t->stride[0], t->stride[1], t->stride[2]}
+           : ttt::RowsView{nullptr, 0, 0, 0};
+}
+template <typename T = float>
+T* ptr(const ttt_tensor* t) {
+  return t ? static_cast<T*>(t->data) : nullptr;
+}
+
+// Runs `launch(workspace)` with `bytes` of stream-ordered scratch (none for 0).
+template <typename F>
+ttt_status with_scratch(size_t bytes, cudaStream_t s, F launch) {
+  void* ws = nullptr;
+  if (bytes && ttt::scratch_alloc(&ws, bytes, s) != cudaSuccess) return TTT_ERR_ALLOC;
+  cudaError_t e = launch(static_cast<float*>(ws));
+  if (ws && cudaFreeAsync(ws, s) != cudaSuccess && e == cudaSuccess) e = cudaErrorUnknown;
+  return e == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
+}
+
+ttt_status norm_check(const ttt_tensor* x, const ttt_tensor* weight, float eps, Dims* n,
+                      int64_t* w_sh) {
+  ttt_status st;
+  if ((st = token_dims(x, n)) != TTT_OK) return st;
+  if (n->d > 16384) return TTT_ERR_UNSUPPORTED;
+  if (!std::isfinite(eps) || eps < 0.f) return TTT_ERR_ARG;
+  if ((st = check_tokens(x, n->B, n->H, n->T, n->d, x->dtype)) != TTT_OK) return st;
+  const int64_t shape[2] = {n->H, n->d};
+  *w_sh = weight->ndim == 2 ? n->d : 0;
+  return weight->ndim == 2 ? check_f32(weight, 2, shape, false) : check_f32(weight, 1, shape + 1, false);
+}
+
+}  // namespace
+
+extern "C" {
+
+ttt_status rms_norm_fwd(const ttt_tensor* x, const ttt_tensor* residual,
+                        const ttt_tensor* weight, float eps, const ttt_tensor* out,
+                        const ttt_tensor* scale, const ttt_tensor* residual_out, void* stream) {
+  if (!x || !weight || !out) return TTT_ERR_NULL;
+  Dims n;
+  ttt::NormArgs a;
+  ttt_status st;
+  if ((st = norm_check(x, weight, eps, &n, &a.w_sh)) != TTT_OK) return st;
+  if (residual && (st = check_tokens(residual, n.B, n.H, n.T, n.d, x->dtype)) != TTT_OK) return st;
+  if (residual_out && !residual) return TTT_ERR_ARG;
+  if (residual_out && (st = check_out_tokens(residual_out, n, n.d, x->dtype)) != TTT_OK) return st;
+  const bool quant = out->dtype == TTT_E4M3;
+  if ((st = check_out_tokens(out, n, n.d, quant ? TTT_E4M3 : x->dtype)) != TTT_OK) return st;
+  if (quant != (scale != nullptr)) return quant ? TTT_ERR_NULL : TTT_ERR_ARG;
+  if (scale) {
+    if (scale->ndim != 3 || scale->shape[0] != n.B || scale->shape[1] != n.H ||
+        scale->shape[2] != n.T)
+      return TTT_ERR_SHAPE;
+    if (scale->dtype != TTT_F32) return TTT_ERR_DTYPE;
+    if (n.T > 0) {
+      if (!scale->data) return TTT_ERR_NULL;
+      for (int i = 0; i < 3; ++i)
+        if (scale->stride[i] < 0) return TTT_ERR_LAYOUT;
+      if (!aligned16(scale->data) || !distinct(scale)) return TTT_ERR_LAYOUT;
+    }
+    a.sc_sb = scale->stride[0];
+    a.sc_sh = scale->stride[1];
+    a.sc_st = scale->stride[2];
+  }
+  const ttt_tensor* const ins[] = {x, residual, weight};
+  const ttt_tensor* const outs[] = {out, scale, residual_out};
+  if (clash(ins, outs)) return TTT_ERR_ARG;
+  if (n.T == 0) return TTT_OK;
+  a.x = view(x);
+  a.r = view_or_null(residual);
+  a.w = ptr<const float>(weight);
+  a.eps = eps;
+  a.out = rows_view(out);
+  a.rout = rows_view(residual_out);
+  a.scale = ptr(scale);
+  a.B = (int)n.B, a.H = (int)n.H, a.T = (int)n.T, a.d = (int)n.d;
+  return ttt::launch_rms_norm_fwd(a, x->dtype == TTT_BF16, static_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
+             ? TTT_OK
+             : TTT_ERR_CUDA;
+}
+
+ttt_status rms_norm_bwd(const ttt_tensor* h, const ttt_tensor* weight, const ttt_tensor* dy,
+                        const ttt_tensor* dres, float eps, const ttt_tensor* dh,
+                        const ttt_tensor* dweight, void* stream) {
+  if (!h || !weight || !dy || !dh || !dweight) return TTT_ERR_NULL;
+  Dims n;
+  ttt::NormBwdArgs a;
+  ttt_status st;
+  if ((st = norm_check(h, weight, eps, &n, &a.w_sh)) != TTT_OK) return st;
+  if ((st = check_tokens(dy, n.B, n.H, n.T, n.d, h->dtype)) != TTT_OK) return st;
+  if (dres && (st = check_tokens(dres, n.B, n.H, n.T, n.d, h->dtype)) != TTT_OK) return st;
+  if ((st = check_out_tokens(dh, n, n.d, h->dtype)) != TTT_OK) return st;
+  if (dweight->ndim != weight->ndim) return TTT_ERR_SHAPE;
+  if ((st = check_f32(dweight, weight->ndim, weight->shape, false)) != TTT_OK) return st;
+  const ttt_tensor* const ins[] = {h, weight, dy, dres};
+  const ttt_tensor* const outs[] = {dh, dweight};
+  if (clash(ins, outs)) return TTT_ERR_ARG;
+  a.h = view(h);
+  a.dy = view(dy);
+  a.dres = view_or_null(dres);
+  a.w = ptr<const float>(weight);
+  a.eps = eps;
+  a.dh = view_mut(dh);
+  a.dw = ptr(dweight);
+  a.B = (int)n.B, a.H = (int)n.H, a.T = (int)n.T, a.d = (int)n.d;
+  const bool bf16 = h->dtype == TTT_BF16;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return with_scratch(ttt::rms_norm_bwd_workspace(a, bf16), s, [&](float* ws) {
+    a.ws = ws;
+    return ttt::launch_rms_norm_bwd(a, bf16, s);
+  });
+}
+
+}  // extern "C"
+
+namespace {
+
+// What the three convolution calls share: x, weight, bias.
+ttt_status conv_check(const ttt_tensor* x, const ttt_tensor* weight, const ttt_tensor* bias,
+                      int32_t silu, Dims* n, int64_t* K) {
+  ttt_status st;
+  if ((st = token_dims(x, n)) != TTT_OK) return st;
+  if (silu != 0 && silu != 1) return TTT_ERR_ARG;
+  if ((st = check_tokens(x, n->B, n->H, n->T, n->d, x->dtype)) != TTT_OK) return st;
+  if (weight->ndim != 3) return TTT_ERR_SHAPE;
+  *K = weight->shape[2];
+  if (*K < 1) return TTT_ERR_SHAPE;
+  if (*K > 8) return TTT_ERR_UNSUPPORTED;
+  const int64_t shape[3] = {n->H, n->d, *K};
+  if ((st = check_f32(weight, 3, shape, false)) != TTT_OK) return st;
+  return check_f32(bias, 2, shape, true);
+}
+
+// A convolution's state tensor [S,H,K-1,d].
+ttt_status conv_state(const ttt_tensor* t, int64_t S, const Dims& n, int64_t K, int32_t dtype,
+                      bool written) {
+  if (!t) return TTT_OK;
+  const Dims m = {S, n.H, K - 1, n.d};
+  return written ? check_out_tokens(t, m, n.d, dtype)
+                 : check_tokens(t, S, n.H, K - 1, n.d, dtype);
+}
+
+}  // namespace
+
+extern "C" {
+
+ttt_status causal_conv_fwd(const ttt_tensor* x, const ttt_tensor* weight, const ttt_tensor* bias,
+                           const ttt_tensor* state0, const ttt_tensor* cu_seqlens, int32_t silu,
+                           const ttt_tensor* out, const ttt_tensor* state_final, void* stream) {
+  if (!x || !weight || !out) return TTT_ERR_NULL;
+  Dims n;
+  int64_t K;
+  ttt::ConvArgs a;
+  ttt_status st;
+  if ((st = conv_check(x, weight, bias, silu, &n, &K)) != TTT_OK) return st;
+  if ((st = check_seqs(cu_seqlens, n, &a.seqs)) != TTT_OK) return st;
+  if ((st = conv_state(state0, a.seqs.S, n, K, x->dtype, false)) != TTT_OK) return st;
+  if ((st = conv_state(state_final, a.seqs.S, n, K, x->dtype, true)) != TTT_OK) return st;
+  if ((st = check_out_tokens(out, n, n.d, x->dtype)) != TTT_OK) return st;
+  const ttt_tensor* const ins[] = {x, weight, bias, state0, cu_seqlens};
+  const ttt_tensor* const outs[] = {out, state_final};
+  if (clash(ins, outs)) return TTT_ERR_ARG;
+  a.x = view(x);
+  a.state0 = K > 1 ? view_or_null(state0) : ttt::TokView{nullptr, 0, 0, 0};
+  a.w = ptr<const float>(weight);
+  a.bias = ptr<const float>(bias);
+  a.out = rows_view(out);
+  a.fin = K > 1 ? rows_view(state_final) : ttt::RowsView{nullptr, 0, 0, 0};
+  a.B = (int)n.B, a.H = (int)n.H, a.T = (int)n.T, a.d = (int)n.d, a.K = (int)K, a.silu = silu;
+  a.status = device_status_ptr();
+  if (!a.status) return TTT_ERR_CUDA;
+  return ttt::launch_causal_conv_fwd(a, x->dtype == TTT_BF16, static_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
+             ? TTT_OK
+             : TTT_ERR_CUDA;
+}
+
+ttt_status causal_conv_bwd(const ttt_tensor* x, const ttt_tensor* weight, const ttt_tensor* bias,
+                           const ttt_tensor* state0, const ttt_tensor* cu_seqlens, int32_t silu,
+                           const ttt_tensor* dy, const ttt_tensor* dstate_final,
+                           const ttt_tensor* dx, const ttt_tensor* dweight,
+                           const ttt_tensor* dbias, const ttt_tensor* dstate0, void* stream) {
+  if (!x || !weight || !dy || !dx || !dweight) return TTT_ERR_NULL;
+  if (!bias != !dbias) return bias ? TTT_ERR_NULL : TTT_ERR_ARG;
+  if (dstate0 && !state0) return TTT_ERR_ARG;
+  Dims n;
+  int64_t K;
+  ttt::ConvBwdArgs a;
+  ttt_status st;
+  if ((st = conv_check(x, weight, bias, silu, &n, &K)) != TTT_OK) return st;
+  if ((st = check_seqs(cu_seqlens, n, &a.seqs)) != TTT_OK) return st;
+  if ((st = conv_state(state0, a.seqs.S, n, K, x->dtype, false)) != TTT_OK) return st;
+  if ((st = conv_state(dstate_final, a.seqs.S, n, K, x->dtype, false)) != TTT_OK) return st;
+  if ((st = conv_state(dstate0, a.seqs.S, n, K, x->dtype, true)) != TTT_OK) return st;
+  if ((st = check_tokens(dy, n.B, n.H, n.T, n.d, x->dtype)) != TTT_OK) return st;
+  if ((st = check_out_tokens(dx, n, n.d, x->dtype)) != TTT_OK) return st;
+  const int64_t shape[3] = {n.H, n.d, K};
+  if ((st = check_f32(dweight, 3, shape, false)) != TTT_OK) return st;
+  if ((st = check_f32(dbias, 2, shape, true)) != TTT_OK) return st;
+  const ttt_tensor* const ins[] = {x, weight, bias, state0, cu_seqlens, dy, dstate_final};
+  const ttt_tensor* const outs[] = {dx, dweight, dbias, dstate0};
+  if (clash(ins, outs)) return TTT_ERR_ARG;
+  const ttt::TokView none = {nullptr, 0, 0, 0};
+  a.x = view(x);
+  a.state0 = K > 1 ? view_or_null(state0) : none;
+  a.dy = view(dy);
+  a.dfin = K > 1 ? view_or_null(dstate_final) : none;
+  a.w = ptr<const float>(weight);
+  a.bias = ptr<const float>(bias);
+  a.dx = view_mut(dx);
+  a.dstate0 = view_mut(K > 1 ? dstate0 : nullptr);
+  a.dw = ptr(dweight);
+  a.dbias = ptr(dbias);
+  a.B = (int)n.B, a.H = (int)n.H, a.T = (int)n.T, a.d = (int)n.d, a.K = (int)K, a.silu = silu;
+  a.status = device_status_ptr();
+  if (!a.status) return TTT_ERR_CUDA;
+  const bool bf16 = x->dtype == TTT_BF16;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return with_scratch(ttt::causal_conv_bwd_workspace(a, bf16), s, [&](float* ws) {
+    a.ws = ws;
+    return ttt::launch_causal_conv_bwd(a, bf16, s);
+  });
+}
+
+ttt_status causal_conv_step(const ttt_tensor* x, const ttt_tensor* state, const ttt_tensor* slots,
+                            const ttt_tensor* weight, const ttt_tensor* bias, int32_t silu,
+                            const ttt_tensor* out, void* stream) {
+  if (!x || !state || !weight || !out) return TTT_ERR_NULL;
+  Dims n;
+  int64_t K;
+  ttt::ConvStepArgs a;
+  ttt_status st;
+  if ((st = conv_check(x, weight, bias, silu, &n, &K)) != TTT_OK) return st;
+  if (n.T != 1 || state->ndim != 4 || state->shape[0] < 1) return TTT_ERR_SHAPE;
+  const int64_t S = state->shape[0];
+  if ((st = check_slots(slots, n, S, &a.slots)) != TTT_OK) return st;
+  if ((st = conv_state(state, S, n, K, x->dtype, true)) != TTT_OK) return st;
+  if ((st = check_out_tokens(out, n, n.d, x->dtype)) != TTT_OK) return st;
+  const ttt_tensor* const ins[] = {x, weight, bias, slots};
+  const ttt_tensor* const outs[] = {out, state};
+  if (clash(ins, outs)) return TTT_ERR_ARG;
+  a.x = view(x);
+  a.state = view_mut(state);
+  a.out = view_mut(out);
+  a.w = ptr<const float>(weight);
+  a.bias = ptr<const float>(bias);
+  a.B = (int)n.B, a.S = (int)S, a.H = (int)n.H, a.d = (int)n.d, a.K = (int)K, a.silu = silu;
+  a.status = device_status_ptr();
+  if (!a.status) return TTT_ERR_CUDA;
+  return ttt::launch_causal_conv_step(a, x->dtype == TTT_BF16, static_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
+             ? TTT_OK
+             : TTT_ERR_CUDA;
+}
+
+}  // extern "C"
+
+namespace {
+
+// What the three scan calls share: every input but the state.
+ttt_status scan_check(const ttt_tensor* x, const ttt_tensor* dt, const ttt_tensor* A,
+                      const ttt_tensor* Bm, const ttt_tensor* Cm, const ttt_tensor* D,
+                      const ttt_tensor* z, const ttt_tensor* dt_bias, int32_t softplus, Dims* n,
+                      int64_t* N, int64_t* G) {
+  ttt_status st;
+  if ((st = token_dims(x, n)) != TTT_OK) return st;
+  if (softplus != 0 && softplus != 1) return TTT_ERR_ARG;
+  const int32_t ty = x->dtype;
+  if ((st = check_tokens(x, n->B, n->H, n->T, n->d, ty)) != TTT_OK) return st;
+  if ((st = check_tokens(dt, n->B, n->H, n->T, n->d, ty)) != TTT_OK) return st;
+  if (z && (st = check_tokens(z, n->B, n->H, n->T, n->d, ty)) != TTT_OK) return st;
+  if (A->ndim != 3 || Bm->ndim != 4) return TTT_ERR_SHAPE;
+  *N = A->shape[2];
+  *G = Bm->shape[1];
+  if (*N < 1 || *G < 1) return TTT_ERR_SHAPE;
+  if (*N > 64) return TTT_ERR_UNSUPPORTED;
+  if (n->H % *G != 0) return TTT_ERR_SHAPE;
+  const int64_t shape[3] = {n->H, n->d, *N};
+  if ((st = check_f32(A, 3, shape, false)) != TTT_OK) return st;
+  if ((st = check_f32(D, 2, shape, true)) != TTT_OK) return st;
+  if ((st = check_f32(dt_bias, 2, shape, true)) != TTT_OK) return st;
+  if ((st = check_tokens(Bm, n->B, *G, n->T, *N, ty)) != TTT_OK) return st;
+  return check_tokens(Cm, n->B, *G, n->T, *N, ty);
+}
+
+void scan_args(ttt::ScanArgs* a, const ttt_tensor* x, const ttt_tensor* dt, const ttt_tensor* A,
+               const ttt_tensor* Bm, const ttt_tensor* Cm, const ttt_tensor* D,
+               const ttt_tensor* z, const ttt_tensor* dt_bias, const ttt_tensor* h0,
+               int32_t softplus, const Dims& n, int64_t N, int64_t G) {
+  a->x = view(x);
+  a->dt = view(dt);
+  a->z = view_or_null(z);
+  a->Bm = view(Bm);
+  a->Cm = view(Cm);
+  a->A = ptr<const float>(A);
+  a->D = ptr<const float>(D);
+  a->dt_bias = ptr<const float>(dt_bias);
+  a->h0 = ptr<const float>(h0);
+  a->out = {nullptr, 0, 0, 0};
+  a->h_final = nullptr;
+  a->ws = nullptr;
+  a->B = (int)n.B, a->H = (int)n.H, a->T = (int)n.T, a->d = (int)n.d;
+  a->N = (int)N, a->G = (int)G, a->softplus = softplus;
+}
+
+}  // namespace
+
+extern "C" {
+
+ttt_status selective_scan_fwd(const ttt_tensor* x, const ttt_tensor* dt, const ttt_tensor* A,
+                              const ttt_tensor* Bm, const ttt_tensor* Cm, const ttt_tensor* D,
+                              const ttt_tensor* z, const ttt_tensor* dt_bias,
+                              const ttt_tensor* h0, const ttt_tensor* cu_seqlens,
+                              int32_t softplus, const ttt_tensor* out,
+                              const ttt_tensor* h_final, void* stream) {
+  if (!x || !dt || !A || !Bm || !Cm || !out) return TTT_ERR_NULL;
+  Dims n;
+  int64_t N, G;
+  ttt::ScanArgs a;
+  ttt_status st;
+  if ((st = scan_check(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, &n, &N, &G)) != TTT_OK) return st;
+  if ((st = check_seqs(cu_seqlens, n, &a.seqs)) != TTT_OK) return st;
+  const int64_t hs[4] = {a.seqs.S, n.H, n.d, N};
+  if ((st = check_f32(h0, 4, hs, true)) != TTT_OK) return st;
+  if ((st = check_f32(h_final, 4, hs, true)) != TTT_OK) return st;
+  if ((st = check_out_tokens(out, n, n.d, x->dtype)) != TTT_OK) return st;
+  const ttt_tensor* const ins[] = {x, dt, A, Bm, Cm, D, z, dt_bias, h0, cu_seqlens};
+  const ttt_tensor* const outs[] = {out, h_final};
+  if (clash(ins, outs)) return TTT_ERR_ARG;
+  scan_args(&a, x, dt, A, Bm, Cm, D, z, dt_bias, h0, softplus, n, N, G);
+  a.out = view_mut(out);
+  a.h_final = ptr(h_final);
+  a.status = device_status_ptr();
+  if (!a.status) return TTT_ERR_CUDA;
+  const bool bf16 = x->dtype == TTT_BF16;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return with_scratch(ttt::selective_scan_workspace(a), s, [&](float* ws) {
+    a.ws = ws;
+    return ttt::launch_selective_scan_fwd(a, bf16, s);
+  });
+}
+
+ttt_status selective_scan_bwd(const ttt_tensor* x, const ttt_tensor* dt, const ttt_tensor* A,
+                              const ttt_tensor* Bm, const ttt_tensor* Cm, const ttt_tensor* D,
+                              const ttt_tensor* z, const ttt_tensor* dt_bias,
+                              const ttt_tensor* h0, const ttt_tensor* cu_seqlens,
+                              int32_t softplus, const ttt_tensor* dy,
+                              const ttt_tensor* dh_final, const ttt_tensor* dx,
+                              const ttt_tensor* ddt, const ttt_tensor* dA,
+                              const ttt_tensor* dBm, const ttt_tensor* dCm,
+                              const ttt_tensor* dD, const ttt_tensor* dz,
+                              const ttt_tensor* ddt_bias, const ttt_tensor* dh0, void* stream) {
+  if (!x || !dt || !A || !Bm || !Cm || !dy || !dx || !ddt || !dA || !dBm || !dCm)
+    return TTT_ERR_NULL;
+  if ((D && !dD) || (z && !dz) || (dt_bias && !ddt_bias)) return TTT_ERR_NULL;
+  if ((!D && dD) || (!z && dz) || (!dt_bias && ddt_bias) || (dh0 && !h0)) return TTT_ERR_ARG;
+  Dims n;
+  int64_t N, G;
+  ttt::ScanBwdArgs g;
+  ttt_status st;
+  if ((st = scan_check(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, &n, &N, &G)) != TTT_OK) return st;
+  if ((st = check_seqs(cu_seqlens, n, &g.f.seqs)) != TTT_OK) return st;
+  const int32_t ty = x->dtype;
+  const int64_t hs[4] = {g.f.seqs.S, n.H, n.d, N};
+  const Dims gn = {n.B, G, n.T, N};
+  if ((st = check_f32(h0, 4, hs, true)) != TTT_OK) return st;
+  if ((st = check_f32(dh_final, 4, hs, true)) != TTT_OK) return st;
+  if ((st = check_f32(dh0, 4, hs, true)) != TTT_OK) return st;
+  if ((st = check_tokens(dy, n.B, n.H, n.T, n.d, ty)) != TTT_OK) return st;
+  if ((st = check_out_tokens(dx, n, n.d, ty)) != TTT_OK) return st;
+  if ((st = check_out_tokens(ddt, n, n.d, ty)) != TTT_OK) return st;
+  if (dz && (st = check_out_tokens(dz, n, n.d, ty)) != TTT_OK) return st;
+  if ((st = check_out_tokens(dBm, gn, N, ty)) != TTT_OK) return st;
+  if ((st = check_out_tokens(dCm, gn, N, ty)) != TTT_OK) return st;
+  if ((st = check_f32(dA, 3, hs + 1, false)) != TTT_OK) return st;
+  if ((st = check_f32(dD, 2, hs + 1, true)) != TTT_OK) return st;
+  if ((st = check_f32(ddt_bias, 2, hs + 1, true)) != TTT_OK) return st;
+  const ttt_tensor* const ins[] = {x, dt, A, Bm, Cm, D, z, dt_bias, h0, cu_seqlens, dy, dh_final};
+  const ttt_tensor* const outs[] = {dx, ddt, dA, dBm, dCm, dD, dz, ddt_bias, dh0};
+  if (clash(ins, outs)) return TTT_ERR_ARG;
+  scan_args(&g.f, x, dt, A, Bm, Cm, D, z, dt_bias, h0, softplus, n, N, G);
+  g.dy = view(dy);
+  g.dh_final = ptr<const float>(dh_final);
+  g.dx = view_mut(dx);
+  g.ddt = view_mut(ddt);
+  g.dz = view_mut(dz);
+  g.dBm = view_mut(dBm);
+  g.dCm = view_mut(dCm);
+  g.dA = ptr(dA);
+  g.dD = ptr(dD);
+  g.ddt_bias = ptr(ddt_bias);
+  g.dh0 = ptr(dh0);
+  g.f.status = device_status_ptr();
+  if (!g.f.status) return TTT_ERR_CUDA;
+  const bool bf16 = ty == TTT_BF16;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return with_scratch(ttt::selective_scan_bwd_workspace(g), s, [&](float* ws) {
+    g.ws = ws;
+    return ttt::launch_selective_scan_bwd(g, bf16, s);
+  });
+}
+
+ttt_status selective_scan_step(const ttt_tensor* x, const ttt_tensor* dt, const ttt_tensor* A,
+                               const ttt_tensor* Bm, const ttt_tensor* Cm, const ttt_tensor* D,
+                               const ttt_tensor* z, const ttt_tensor* dt_bias,
+                               const ttt_tensor* state, const ttt_tensor* slots,
+                               int32_t softplus, const ttt_tensor* out, void* stream) {
+  if (!x || !dt || !A || !Bm || !Cm || !state || !out) return TTT_ERR_NULL;
+  Dims n;
+  int64_t N, G;
+  ttt::ScanStepArgs a;
+  ttt_status st;
+  if ((st = scan_check(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, &n, &N, &G)) != TTT_OK) return st;
+  if (n.T != 1 || state->ndim != 4 || state->shape[0] < 1) return TTT_ERR_SHAPE;
+  const int64_t S = state->shape[0];
+  if ((st = check_slots(slots, n, S, &a.slots)) != TTT_OK) return st;
+  const int64_t hs[4] = {S, n.H, n.d, N};
+  if ((st = check_f32(state, 4, hs, false)) != TTT_OK) return st;
+  if ((st = check_out_tokens(out, n, n.d, x->dtype)) != TTT_OK) return st;
+  const ttt_tensor* const ins[] = {x, dt, A, Bm, Cm, D, z, dt_bias, slots};
+  const ttt_tensor* const outs[] = {out, state};
+  if (clash(ins, outs)) return TTT_ERR_ARG;
+  a.x = view(x);
+  a.dt = view(dt);
+  a.z = view_or_null(z);
+  a.Bm = view(Bm);
+  a.Cm = view(Cm);
+  a.A = ptr<const float>(A);
+  a.D = ptr<const float>(D);
+  a.dt_bias = ptr<const float>(dt_bias);
+  a.state = ptr(state);
+  a.out = view_mut(out);
+  a.B = (int)n.B, a.S = (int)S, a.H = (int)n.H, a.d = (int)n.d;
+  a.N = (int)N, a.G = (int)G, a.softplus = softplus;
+  a.status = device_status_ptr();
+  if (!a.status) return TTT_ERR_CUDA;
+  return ttt::launch_selective_scan_step(a, x->dtype == TTT_BF16,
+                                         static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? TTT_OK
+             : TTT_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -1,0 +1,311 @@
+// Arguments and shared device code of the recurrent block's operators: RMS
+// norm, short causal convolution, selective scan (see include/ttt.h).
+#pragma once
+
+#include "common.cuh"
+
+namespace ttt {
+
+// ---- host-side arguments ------------------------------------------------------
+
+struct RowsView {  // like TokView, also for 8-bit elements
+  void* p;
+  int64_t sb, sh, st;
+};
+
+struct NormArgs {
+  TokView x, r;            // r.p null: no residual
+  const float* w;
+  int64_t w_sh;            // 0: one weight for all heads
+  float eps;
+  RowsView out, rout;      // rout.p null: the sum is not wanted
+  float* scale;            // non-null: out is e4m3
+  int64_t sc_sb, sc_sh, sc_st;
+  int B, H, T, d;
+};
+cudaError_t launch_rms_norm_fwd(const NormArgs& a, bool bf16, cudaStream_t s);
+
+struct NormBwdArgs {
+  TokView h, dy, dres;     // dres.p null: none
+  const float* w;
+  int64_t w_sh;
+  float eps;
+  TokViewMut dh;
+  float* dw;
+  float* ws;
+  int B, H, T, d;
+};
+size_t rms_norm_bwd_workspace(const NormBwdArgs& a, bool bf16);
+cudaError_t launch_rms_norm_bwd(const NormBwdArgs& a, bool bf16, cudaStream_t s);
+
+// A call's sequences: S packed ones (cu non-null, B = 1), or B of T tokens.
+struct Seqs {
+  const int32_t* cu;
+  int S;
+};
+
+struct ConvArgs {
+  TokView x, state0;       // state0.p null: zeros
+  const float *w, *bias;   // bias may be null
+  Seqs seqs;
+  RowsView out, fin;       // fin.p null: not wanted
+  int B, H, T, d, K, silu;
+  int* status;
+};
+cudaError_t launch_causal_conv_fwd(const ConvArgs& a, bool bf16, cudaStream_t s);
+
+struct ConvBwdArgs {
+  TokView x, state0, dy, dfin;
+  const float *w, *bias;
+  Seqs seqs;
+  TokViewMut dx, dstate0;  // dstate0.p null: not wanted
+  float *dw, *dbias;       // dbias may be null
+  float* ws;
+  int B, H, T, d, K, silu;
+  int* status;
+};
+size_t causal_conv_bwd_workspace(const ConvBwdArgs& a, bool bf16);
+cudaError_t launch_causal_conv_bwd(const ConvBwdArgs& a, bool bf16, cudaStream_t s);
+
+struct ConvStepArgs {
+  TokView x;
+  TokViewMut state, out;
+  const int32_t* slots;    // may be null
+  const float *w, *bias;
+  int B, S, H, d, K, silu;
+  int* status;
+};
+cudaError_t launch_causal_conv_step(const ConvStepArgs& a, bool bf16, cudaStream_t s);
+
+struct ScanArgs {
+  TokView x, dt, z, Bm, Cm;   // z.p may be null; Bm, Cm: sh is the group stride
+  const float *A, *D, *dt_bias, *h0;   // D, dt_bias, h0 may be null
+  Seqs seqs;
+  TokViewMut out;
+  float* h_final;          // may be null
+  float* ws;
+  int B, H, T, d, N, G, softplus;
+  int* status;
+};
+size_t selective_scan_workspace(const ScanArgs& a);
+cudaError_t launch_selective_scan_fwd(const ScanArgs& a, bool bf16, cudaStream_t s);
+
+struct ScanBwdArgs {
+  ScanArgs f;              // the forward's inputs (out, h_final, ws unused)
+  TokView dy;
+  const float* dh_final;   // may be null
+  TokViewMut dx, ddt, dz, dBm, dCm;   // dz.p may be null
+  float *dA, *dD, *ddt_bias, *dh0;    // all but dA may be null
+  float* ws;
+};
+size_t selective_scan_bwd_workspace(const ScanBwdArgs& a);
+cudaError_t launch_selective_scan_bwd(const ScanBwdArgs& a, bool bf16, cudaStream_t s);
+
+struct ScanStepArgs {
+  TokView x, dt, z, Bm, Cm;
+  const float *A, *D, *dt_bias;
+  float* state;
+  const int32_t* slots;
+  TokViewMut out;
+  int B, S, H, d, N, G, softplus;
+  int* status;
+};
+cudaError_t launch_selective_scan_step(const ScanStepArgs& a, bool bf16, cudaStream_t s);
+
+// ---- device code --------------------------------------------------------------
+
+// 16 bytes of a token row: 8 bf16 or 4 fp32 channels.
+template <typename T>
+struct Vec {
+  static constexpr int n = 16 / sizeof(T);
+  uint4 v;
+};
+
+template <typename T>
+__device__ __forceinline__ void unpack(const Vec<T>& a, float (&f)[Vec<T>::n]);
+template <>
+__device__ __forceinline__ void unpack<float>(const Vec<float>& a, float (&f)[4]) {
+  f[0] = __uint_as_float(a.v.x);
+  f[1] = __uint_as_float(a.v.y);
+  f[2] = __uint_as_float(a.v.z);
+  f[3] = __uint_as_float(a.v.w);
+}
+template <>
+__device__ __forceinline__ void unpack<__nv_bfloat16>(const Vec<__nv_bfloat16>& a, float (&f)[8]) {
+  const uint32_t w[4] = {a.v.x, a.v.y, a.v.z, a.v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {  // a bf16 is the upper half of its fp32
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+template <typename T>
+__device__ __forceinline__ Vec<T> pack(const float (&f)[Vec<T>::n]);
+template <>
+__device__ __forceinline__ Vec<float> pack<float>(const float (&f)[4]) {
+  return {make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                     __float_as_uint(f[3]))};
+}
+template <>
+__device__ __forceinline__ Vec<__nv_bfloat16> pack<__nv_bfloat16>(const float (&f)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&p);
+  }
+  return {make_uint4(w[0], w[1], w[2], w[3])};
+}
+
+// The first `n` elements (n may be <= 0) of the row piece at p, which is
+// 16-byte aligned; the rest reads as zero. A piece that ends inside the vector
+// is read element by element: nothing behind the row's end is touched.
+template <typename T>
+__device__ __forceinline__ Vec<T> load_vec(const T* p, int n) {
+  Vec<T> r;
+  if (n >= Vec<T>::n) {
+    r.v = *reinterpret_cast<const uint4*>(p);
+  } else {
+    float f[Vec<T>::n];
+#pragma unroll
+    for (int i = 0; i < Vec<T>::n; ++i) f[i] = i < n ? to_f32(p[i]) : 0.f;
+    r = pack<T>(f);
+  }
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
+  return __float2bfloat16_rn(x);
+}
+template <typename T>
+__device__ __forceinline__ void store_vec(T* p, int n, const float (&f)[Vec<T>::n]) {
+  if (n >= Vec<T>::n) {
+    *reinterpret_cast<uint4*>(p) = pack<T>(f).v;
+  } else {
+#pragma unroll
+    for (int i = 0; i < Vec<T>::n; ++i)
+      if (i < n) p[i] = from_f32<T>(f[i]);
+  }
+}
+
+// 1 / (1 + exp(-x)). __fdividef gives 0 for a denominator above 2^126, where
+// the quotient is below 2^-126 anyway; NaN stays NaN.
+__device__ __forceinline__ float sigmoid_f(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// x sigmoid(x); left of -88 it is below fp32's normal range, and -inf * 0 is avoided.
+__device__ __forceinline__ float silu_f(float x) { return x < -88.f ? 0.f : x * sigmoid_f(x); }
+// d silu / dx = s (1 + x (1 - s)); right of 88 it is 1 in fp32 (inf * 0 is avoided).
+__device__ __forceinline__ float dsilu_f(float x) {
+  const float s = sigmoid_f(x);
+  return x < -88.f ? 0.f : x > 88.f ? 1.f : s * (1.f + x * (1.f - s));
+}
+// log(1 + exp(x)); above 20 the difference to x is below half an fp32 step.
+// log1p keeps the relative accuracy for very negative x, where the small
+// step sizes of a trained layer lie.
+__device__ __forceinline__ float softplus_f(float x) {
+  return x > 20.f ? x : log1pf(__expf(x));
+}
+
+// Sequence i of a packed call, its offsets clamped into [0, T]; empty (lo =
+// hi) where they decrease or leave the range, which is recorded.
+__device__ __forceinline__ void packed_seq(const int32_t* cu, int i, int T, int* status, int* lo,
+                                           int* hi) {
+  int a = cu[i], b = cu[i + 1];
+  if (a < 0 || b < a || b > T) {
+    record_error(status, DEV_BOUNDS);
+    a = b = 0;
+  }
+  *lo = a;
+  *hi = b;
+}
+
+// The first sequence whose end lies behind token t (S if none).
+__device__ __forceinline__ int first_seq_behind(const int32_t* cu, int S, int t) {
+  int lo = 0, hi = S;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (cu[mid + 1] > t)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  return lo;
+}
+
+// A row's place in a pool of states (slots null: row b has place b), for a
+// block that works on row b alone. False: nothing to do here. Rows that name
+// one place are all done by the block of the first of them, in row order: it
+// calls next_row() after each row until that returns false.
+struct SlotRows {
+  const int32_t* slots;
+  int b, B, slot;
+  bool more;
+  __device__ __forceinline__ bool begin(const int32_t* s, int row, int rows, int S, int* status) {
+    slots = s;
+    b = row;
+    B = rows;
+    slot = s ? s[row] : row;
+    more = false;
+    if (slot < 0 || slot >= S) {
+      if (slot != -1 && threadIdx.x == 0) record_error(status, DEV_BOUNDS);
+      return false;
+    }
+    if (!s) return true;
+    int earlier = 0, later = 0;
+    for (int i = threadIdx.x; i < B; i += blockDim.x)
+      if (s[i] == slot) {
+        earlier |= i < b;
+        later |= i > b;
+      }
+    if (__syncthreads_or(earlier)) return false;
+    more = __syncthreads_or(later);
+    return true;
+  }
+  __device__ __forceinline__ bool next_row() {
+    if (!more) return false;
+    __shared__ int s_next;
+    __syncthreads();
+    if (threadIdx.x == 0) s_next = B;
+    __syncthreads();
+    for (int i = b + 1 + threadIdx.x; i < B; i += blockDim.x)
+      if (slots[i] == slot) {
+        atomicMin(&s_next, i);
+        break;
+      }
+    __syncthreads();
+    b = s_next;
+    return b < B;
+  }
+};
+
+// out(col, sum over p of ws[p * cols + col]): 32 columns a block, 16 threads a
+// column, each summing every 16th part in order, then the 16 in order: the
+// result does not depend on scheduling.
+constexpr int kSumCols = 32, kSumRows = 16;
+template <typename Out>
+__global__ void __launch_bounds__(kSumCols * kSumRows)
+    sum_parts_kernel(const float* __restrict__ ws, int64_t parts, int64_t cols, Out out) {
+  __shared__ float part[kSumRows][kSumCols];
+  const int c = threadIdx.x % kSumCols, r = threadIdx.x / kSumCols;
+  const int64_t col = (int64_t)blockIdx.x * kSumCols + c;
+  float s = 0.f;
+  if (col < cols)
+    for (int64_t p = r; p < parts; p += kSumRows) s += ws[p * cols + col];
+  part[r][c] = s;
+  __syncthreads();
+  if (r == 0 && col < cols) {
+    for (int i = 1; i < kSumRows; ++i) s += part[i][c];
+    out(col, s);
+  }
+}
+template <typename Out>
+cudaError_t sum_parts(const float* ws, int64_t parts, int64_t cols, Out out, cudaStream_t s) {
+  sum_parts_kernel<<<(unsigned)((cols + kSumCols - 1) / kSumCols), kSumCols * kSumRows, 0, s>>>(
+      ws, parts, cols, out);
+  return cudaGetLastError();
+}
+
+}  // namespace ttt

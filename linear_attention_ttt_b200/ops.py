@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -19,7 +20,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("TTT_B200_LIB") or os.path.join(_PKG, "libttt_b200.so")
 DEBUG_LIB_PATH = os.path.join(_PKG, "libttt_b200_dbg.so")
 
-TTT_F32, TTT_BF16 = 0, 1
+TTT_F32, TTT_BF16, TTT_I32, TTT_E4M3 = 0, 1, 2, 3
 TTT_LOSS_MSE, TTT_LOSS_NEG_DOT = 0, 1
 LACT_UPDATE_GD, LACT_UPDATE_MUON = 0, 1
 
@@ -81,6 +82,15 @@ SIGNATURES = {
                            ctypes.c_int32),
     "lact_swiglu_bwd": ([P, P, P, P, P, P, P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                          P, P, P, P, P, P, P, P, P, P, P, ctypes.c_void_p], ctypes.c_int32),
+    **{name: ([ctypes.c_void_p] * n + scalars + [ctypes.c_void_p] * m + [ctypes.c_void_p],
+              ctypes.c_int32)
+       for name, n, scalars, m in (
+           ("rms_norm_fwd", 3, [ctypes.c_float], 3), ("rms_norm_bwd", 4, [ctypes.c_float], 2),
+           ("causal_conv_fwd", 5, [ctypes.c_int32], 2), ("causal_conv_bwd", 5, [ctypes.c_int32], 6),
+           ("causal_conv_step", 5, [ctypes.c_int32], 1),
+           ("selective_scan_fwd", 10, [ctypes.c_int32], 2),
+           ("selective_scan_bwd", 10, [ctypes.c_int32], 11),
+           ("selective_scan_step", 10, [ctypes.c_int32], 1))},
     "ttt_status_string": ([ctypes.c_int32], ctypes.c_char_p),
     "ttt_get_device_status": ([ctypes.c_void_p], ctypes.c_int32),
     "ttt_version": ([], ctypes.c_int32),
@@ -301,6 +311,199 @@ def lact_swiglu_window_fwd(q, k, v, eta, W1, W2, W3, chunk: int, update_rule: in
     code = load().lact_swiglu_window_fwd(*r[:7], int(chunk), int(update_rule), int(window), r[7],
                                          _stream(stream))
     _check(code, "lact_swiglu_window_fwd")
+    return out
+
+
+# ---- the recurrent block: RMS norm, short convolution, selective scan ---------
+
+_DTYPES = {torch.float32: TTT_F32, torch.bfloat16: TTT_BF16, torch.int32: TTT_I32,
+           torch.float8_e4m3fn: TTT_E4M3}
+_PACK = struct.Struct("=Qii4q4q").pack_into  # one TTTTensor
+_DESC = ctypes.sizeof(TTTTensor)
+_ZEROS = (0, 0, 0, 0)
+
+
+def _block_call(name, tensors, split, scalar, stream):
+    """Calls entry point `name` with the descriptors of `tensors` (None -> NULL), the
+    scalar argument behind the first `split` of them. All tensors have to be on one
+    CUDA device; the call is made with that device current, on `stream` or its current
+    stream."""
+    lib = load()
+    n = len(tensors)
+    buf = ctypes.create_string_buffer(n * _DESC)
+    base = ctypes.addressof(buf)
+    args = [None] * n
+    device = tensors[0].device
+    for i, t in enumerate(tensors):
+        if t is None:
+            continue
+        if t.device != device or device.type != "cuda":
+            raise ValueError(f"{name}: tensors have to be on one CUDA device, got {t.device}")
+        dt = _DTYPES.get(t.dtype)
+        if dt is None:
+            raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+        shape, stride, nd = t.shape, t.stride(), t.dim()
+        if nd > 4:
+            raise ValueError(f"{name}: at most 4 dims")
+        _PACK(buf, i * _DESC, t.data_ptr(), dt, nd, *shape, *_ZEROS[nd:], *stride, *_ZEROS[nd:])
+        args[i] = base + i * _DESC
+    index = device.index
+    if index == torch.cuda.current_device():
+        code = getattr(lib, name)(*args[:split], scalar, *args[split:],
+                                  _block_stream(stream, index))
+    else:
+        with torch.cuda.device(index):
+            code = getattr(lib, name)(*args[:split], scalar, *args[split:],
+                                      _block_stream(stream, index))
+    _check(code, name)
+
+
+def _block_stream(stream, index):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _like_tokens(x, d=None, dtype=None, zero=False):
+    """A new token tensor [B,H,T,d] with x's order of storage (heads before or behind
+    tokens) and rows of a multiple of 16 bytes."""
+    B, H, T = x.shape[:3]
+    d = x.shape[3] if d is None else d
+    dtype = dtype or x.dtype
+    pad = -d % (16 // dtype.itemsize)
+    make = torch.zeros if zero else torch.empty
+    if H > 1 and T > 1 and x.stride(1) < x.stride(2):
+        t = make((B, T, H, d + pad), dtype=dtype, device=x.device).transpose(1, 2)
+    else:
+        t = make((B, H, T, d + pad), dtype=dtype, device=x.device)
+    return t[..., :d] if pad else t
+
+
+def _conv_state(x, S, K):
+    B, H, T, d = x.shape
+    pad = -d % (16 // x.dtype.itemsize)
+    return torch.empty((S, H, K - 1, d + pad), dtype=x.dtype, device=x.device)[..., :d]
+
+
+def _sequences(x, cu_seqlens):
+    return x.shape[0] if cu_seqlens is None else cu_seqlens.shape[0] - 1
+
+
+def rms_norm_fwd(x, weight, eps: float = 1e-6, residual=None, quant: bool = False, out=None,
+                 scale=None, residual_out=None, stream=None):
+    """RMS norm over the last dimension of x [B,H,T,d], or of x + residual, times weight
+    ([d] or [H,d], fp32). Returns (out, scale, summed): with quant=True out holds 8-bit
+    (e4m3) values and scale [B,H,T] what they are multiplied with, else scale is None;
+    summed is x + residual, or None without a residual. weight = 1/sqrt(d) with eps = 0
+    is the L2 normalisation that ttt_linear_fwd and the LaCT layers expect of q and k."""
+    if out is None:
+        out = _like_tokens(x, dtype=torch.float8_e4m3fn if quant else None)
+    if quant and scale is None:
+        scale = torch.empty(x.shape[:3], dtype=torch.float32, device=x.device)
+    if residual is not None and residual_out is None:
+        residual_out = _like_tokens(x)
+    _block_call("rms_norm_fwd", (x, residual, weight, out, scale, residual_out), 3, float(eps),
+                stream)
+    return out, scale, residual_out
+
+
+def rms_norm_bwd(h, weight, dy, eps: float = 1e-6, dres=None, stream=None):
+    """Backward of rms_norm_fwd from its normalised input h (its `summed`, or x): returns
+    (dh, dweight). dres is the gradient that reaches h past the norm. dh is the gradient
+    of x and of the residual alike."""
+    dh = _like_tokens(h)
+    dw = torch.empty(weight.shape, dtype=torch.float32, device=h.device)
+    _block_call("rms_norm_bwd", (h, weight, dy, dres, dh, dw), 4, float(eps), stream)
+    return dh, dw
+
+
+def causal_conv_fwd(x, weight, bias=None, silu: bool = True, state0=None, cu_seqlens=None,
+                    out=None, state_final=None, want_final: bool = True, stream=None):
+    """Short causal depthwise convolution of x [B,H,T,d] along T (weight [H,d,K], bias
+    [H,d]), followed by silu. Returns (out, state_final): the last K-1 inputs of every
+    sequence [S,H,K-1,d], which state0 of a later call or causal_conv_step continues
+    from. cu_seqlens (int32 [S+1]) packs S sequences along T of one batch row."""
+    if out is None:
+        out = _like_tokens(x, zero=cu_seqlens is not None)
+    if state_final is None and want_final:
+        state_final = _conv_state(x, _sequences(x, cu_seqlens), weight.shape[-1])
+    _block_call("causal_conv_fwd", (x, weight, bias, state0, cu_seqlens, out, state_final), 5,
+                int(bool(silu)), stream)
+    return out, state_final
+
+
+def causal_conv_bwd(x, weight, dy, bias=None, silu: bool = True, state0=None, dstate_final=None,
+                    cu_seqlens=None, stream=None):
+    """Backward of causal_conv_fwd: returns (dx, dweight, dbias, dstate0), None for the
+    gradient of what was not given."""
+    dx = _like_tokens(x, zero=cu_seqlens is not None)
+    dw = torch.empty(weight.shape, dtype=torch.float32, device=x.device)
+    db = None if bias is None else torch.empty(bias.shape, dtype=torch.float32, device=x.device)
+    ds = None if state0 is None else _conv_state(x, state0.shape[0], weight.shape[-1])
+    _block_call("causal_conv_bwd", (x, weight, bias, state0, cu_seqlens, dy, dstate_final, dx, dw,
+                                    db, ds), 5, int(bool(silu)), stream)
+    return dx, dw, db, ds
+
+
+def causal_conv_step(x, state, weight, bias=None, silu: bool = True, slots=None, out=None,
+                     stream=None):
+    """One token of causal_conv_fwd for each of B sequences: x [B,H,1,d]; state
+    [S,H,K-1,d] is updated in place. slots (int32 [B]) names each row's place in the
+    state pool (-1: a padded row, left alone). Returns out."""
+    if out is None:
+        out = _like_tokens(x, zero=slots is not None)
+    _block_call("causal_conv_step", (x, state, slots, weight, bias, out), 5, int(bool(silu)),
+                stream)
+    return out
+
+
+def selective_scan_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, softplus: bool = True,
+                       h0=None, cu_seqlens=None, out=None, h_final=None, want_final: bool = True,
+                       stream=None):
+    """Selective state space scan: per channel, with step = softplus(dt + dt_bias),
+    s <- exp(step A) s + step x Bm, y = <Cm, s> + D x, out = y silu(z). x, dt, z
+    [B,H,T,d]; A [H,d,N] fp32; Bm, Cm [B,G,T,N] shared by H/G heads each; D, dt_bias
+    [H,d] fp32. Returns (out, h_final): the states [S,H,d,N] (fp32) behind each sequence,
+    which h0 of a later call or selective_scan_step continues from."""
+    if out is None:
+        out = _like_tokens(x, zero=cu_seqlens is not None)
+    if h_final is None and want_final:
+        h_final = torch.empty((_sequences(x, cu_seqlens), *A.shape), dtype=torch.float32,
+                              device=x.device)
+    _block_call("selective_scan_fwd", (x, dt, A, Bm, Cm, D, z, dt_bias, h0, cu_seqlens, out,
+                                       h_final), 10, int(bool(softplus)), stream)
+    return out, h_final
+
+
+def selective_scan_bwd(x, dt, A, Bm, Cm, dy, D=None, z=None, dt_bias=None, softplus: bool = True,
+                       h0=None, dh_final=None, cu_seqlens=None, stream=None):
+    """Backward of selective_scan_fwd: returns (dx, ddt, dA, dBm, dCm, dD, dz, ddt_bias,
+    dh0), None for the gradient of what was not given. The states are computed again
+    from the inputs."""
+    packed = cu_seqlens is not None
+    f32 = dict(dtype=torch.float32, device=x.device)
+    dx, ddt = _like_tokens(x, zero=packed), _like_tokens(x, zero=packed)
+    dBm, dCm = _like_tokens(Bm, zero=packed), _like_tokens(Cm, zero=packed)
+    dA = torch.empty(A.shape, **f32)
+    dD = None if D is None else torch.empty(D.shape, **f32)
+    dz = None if z is None else _like_tokens(x, zero=packed)
+    dbias = None if dt_bias is None else torch.empty(dt_bias.shape, **f32)
+    dh0 = None if h0 is None else torch.empty(h0.shape, **f32)
+    _block_call("selective_scan_bwd", (x, dt, A, Bm, Cm, D, z, dt_bias, h0, cu_seqlens, dy,
+                                       dh_final, dx, ddt, dA, dBm, dCm, dD, dz, dbias, dh0), 10,
+                int(bool(softplus)), stream)
+    return dx, ddt, dA, dBm, dCm, dD, dz, dbias, dh0
+
+
+def selective_scan_step(x, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None,
+                        softplus: bool = True, slots=None, out=None, stream=None):
+    """One token of selective_scan_fwd for each of B sequences: x, dt, z [B,H,1,d], Bm, Cm
+    [B,G,1,N]; state [S,H,d,N] (fp32) is updated in place; slots as in causal_conv_step.
+    Returns out."""
+    if out is None:
+        out = _like_tokens(x, zero=slots is not None)
+    _block_call("selective_scan_step", (x, dt, A, Bm, Cm, D, z, dt_bias, state, slots, out), 10,
+                int(bool(softplus)), stream)
     return out
 
 
