@@ -377,7 +377,10 @@ ttt_status lact_swiglu_window_fwd(const ttt_tensor* q, const ttt_tensor* k, cons
  * Tokens are [B,H,T,d] under the conventions at the top of this file; a block
  * of width D with [B,T,D] storage passes H = 1, d = D, and heads that lie
  * beside one another in storage are described by strides. One element type
- * (fp32 or bf16) for all token tensors of a call; parameters are fp32.
+ * (fp32 or bf16) for all token tensors of a call; parameters are fp32. The
+ * 16-byte rule does not apply to these calls: pointers need the alignment of
+ * their element, and rows may start anywhere. Where all token rows of a call
+ * are 16-byte aligned they move 16 bytes at a time, else one by one.
  * Arithmetic, sums and states are fp32; a 16-bit output is rounded once.
  *
  * Packed sequences: with cu_seqlens (TTT_I32, contiguous, [S+1], on the

@@ -10,7 +10,9 @@ Each translation unit is compiled to an object under csrc/_build/ and the
 objects are linked into linear_attention_ttt_b200/libttt_b200.so (cudart
 linked statically, so the library shares the CUDA driver context of whatever
 process loads it). A unit is rebuilt when it, or any header it may include,
-is newer than its object.
+is newer than its object. csrc/binding.cpp, the native half of the Python
+binding, is compiled with g++ against torch's headers into
+linear_attention_ttt_b200/_binding.so.
 """
 from __future__ import annotations
 
@@ -28,6 +30,8 @@ BUILD = os.path.join(CSRC, "_build")
 LIB = os.path.join(PKG, "libttt_b200.so")
 BUILD_DBG = os.path.join(CSRC, "_build_dbg")
 LIB_DBG = os.path.join(PKG, "libttt_b200_dbg.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O3", "--expt-relaxed-constexpr",
@@ -45,7 +49,32 @@ def _headers():
     return glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(ROOT, "include", "*.h"))
 
 
+def build_binding(force: bool = False) -> str:
+    """_binding.so (see csrc/binding.cpp). Only torch's headers and libraries are used."""
+    newest = max(os.path.getmtime(f) for f in (BINDING_SRC, os.path.join(ROOT, "include", "ttt.h")))
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
+        return BINDING
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    inc = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    lib = os.path.join(base, "lib")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-I{i}" for i in inc), BINDING_SRC, "-o", BINDING, f"-L{lib}", f"-Wl,-rpath,{lib}",
+           "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("g++ failed on binding.cpp")
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False, extra=(), debug_bounds: bool = False) -> str:
+    build_binding(force)
     build_dir, lib = (BUILD_DBG, LIB_DBG) if debug_bounds else (BUILD, LIB)
     if debug_bounds:
         extra = (*extra, "-DTTT_DEBUG_BOUNDS")

@@ -843,6 +843,27 @@ ttt_status token_dims(const ttt_tensor* x, Dims* n) {
   return TTT_OK;
 }
 
+// Token tensor [B,H,T,d] of a block call. Rows may start at any element;
+// *wide becomes false where they are not all 16-byte aligned.
+ttt_status check_rows(const ttt_tensor* t, int64_t B, int64_t H, int64_t T, int64_t d, int32_t dtype,
+                      bool* wide) {
+  if (t->ndim != 4) return TTT_ERR_SHAPE;
+  if (t->shape[0] != B || t->shape[1] != H || t->shape[2] != T || t->shape[3] != d)
+    return TTT_ERR_SHAPE;
+  if (t->dtype != dtype) return TTT_ERR_DTYPE;
+  if (empty(t)) return TTT_OK;
+  if (!t->data) return TTT_ERR_NULL;
+  const int64_t es = (int64_t)elem_size(dtype);
+  if ((t->stride[3] != 1 && d > 1) || reinterpret_cast<uintptr_t>(t->data) % es != 0)
+    return TTT_ERR_LAYOUT;
+  *wide &= aligned16(t->data);
+  for (int i = 0; i < 3; ++i) {
+    if (t->stride[i] < 0) return TTT_ERR_LAYOUT;
+    *wide &= t->shape[i] == 1 || t->stride[i] * es % 16 == 0;
+  }
+  return TTT_OK;
+}
+
 // Whether no two elements of a tensor share an address (by strides, smallest first).
 bool distinct(const ttt_tensor* t) {
   if (empty(t)) return true;
@@ -867,8 +888,8 @@ bool distinct(const ttt_tensor* t) {
   return true;
 }
 
-ttt_status check_out_tokens(const ttt_tensor* t, const Dims& n, int64_t d, int32_t dtype) {
-  const ttt_status st = check_tokens(t, n.B, n.H, n.T, d, dtype);
+ttt_status check_out_rows(const ttt_tensor* t, const Dims& n, int64_t d, int32_t dtype, bool* wide) {
+  const ttt_status st = check_rows(t, n.B, n.H, n.T, d, dtype, wide);
   if (st != TTT_OK) return st;
   return distinct(t) ? TTT_OK : TTT_ERR_LAYOUT;
 }
@@ -882,7 +903,7 @@ ttt_status check_f32(const ttt_tensor* t, int ndim, const int64_t* shape, bool o
   if (t->dtype != TTT_F32) return TTT_ERR_DTYPE;
   if (empty(t)) return TTT_OK;
   if (!t->data) return TTT_ERR_NULL;
-  if (!contiguous(t) || !aligned16(t->data)) return TTT_ERR_LAYOUT;
+  if (!contiguous(t) || reinterpret_cast<uintptr_t>(t->data) % 4 != 0) return TTT_ERR_LAYOUT;
   return TTT_OK;
 }
 
@@ -960,12 +981,13 @@ ttt_status with_scratch(size_t bytes, cudaStream_t s, F launch) {
 }
 
 ttt_status norm_check(const ttt_tensor* x, const ttt_tensor* weight, float eps, Dims* n,
-                      int64_t* w_sh) {
+                      int64_t* w_sh, bool* wide) {
+  *wide = true;
   ttt_status st;
   if ((st = token_dims(x, n)) != TTT_OK) return st;
   if (n->d > 16384) return TTT_ERR_UNSUPPORTED;
   if (!std::isfinite(eps) || eps < 0.f) return TTT_ERR_ARG;
-  if ((st = check_tokens(x, n->B, n->H, n->T, n->d, x->dtype)) != TTT_OK) return st;
+  if ((st = check_rows(x, n->B, n->H, n->T, n->d, x->dtype, wide)) != TTT_OK) return st;
   const int64_t shape[2] = {n->H, n->d};
   *w_sh = weight->ndim == 2 ? n->d : 0;
   return weight->ndim == 2 ? check_f32(weight, 2, shape, false) : check_f32(weight, 1, shape + 1, false);
@@ -982,12 +1004,12 @@ ttt_status rms_norm_fwd(const ttt_tensor* x, const ttt_tensor* residual,
   Dims n;
   ttt::NormArgs a;
   ttt_status st;
-  if ((st = norm_check(x, weight, eps, &n, &a.w_sh)) != TTT_OK) return st;
-  if (residual && (st = check_tokens(residual, n.B, n.H, n.T, n.d, x->dtype)) != TTT_OK) return st;
+  if ((st = norm_check(x, weight, eps, &n, &a.w_sh, &a.wide)) != TTT_OK) return st;
+  if (residual && (st = check_rows(residual, n.B, n.H, n.T, n.d, x->dtype, &a.wide)) != TTT_OK) return st;
   if (residual_out && !residual) return TTT_ERR_ARG;
-  if (residual_out && (st = check_out_tokens(residual_out, n, n.d, x->dtype)) != TTT_OK) return st;
+  if (residual_out && (st = check_out_rows(residual_out, n, n.d, x->dtype, &a.wide)) != TTT_OK) return st;
   const bool quant = out->dtype == TTT_E4M3;
-  if ((st = check_out_tokens(out, n, n.d, quant ? TTT_E4M3 : x->dtype)) != TTT_OK) return st;
+  if ((st = check_out_rows(out, n, n.d, quant ? TTT_E4M3 : x->dtype, &a.wide)) != TTT_OK) return st;
   if (quant != (scale != nullptr)) return quant ? TTT_ERR_NULL : TTT_ERR_ARG;
   if (scale) {
     if (scale->ndim != 3 || scale->shape[0] != n.B || scale->shape[1] != n.H ||
@@ -998,7 +1020,8 @@ ttt_status rms_norm_fwd(const ttt_tensor* x, const ttt_tensor* residual,
       if (!scale->data) return TTT_ERR_NULL;
       for (int i = 0; i < 3; ++i)
         if (scale->stride[i] < 0) return TTT_ERR_LAYOUT;
-      if (!aligned16(scale->data) || !distinct(scale)) return TTT_ERR_LAYOUT;
+      if (reinterpret_cast<uintptr_t>(scale->data) % 4 != 0 || !distinct(scale))
+        return TTT_ERR_LAYOUT;
     }
     a.sc_sb = scale->stride[0];
     a.sc_sh = scale->stride[1];
@@ -1029,10 +1052,10 @@ ttt_status rms_norm_bwd(const ttt_tensor* h, const ttt_tensor* weight, const ttt
   Dims n;
   ttt::NormBwdArgs a;
   ttt_status st;
-  if ((st = norm_check(h, weight, eps, &n, &a.w_sh)) != TTT_OK) return st;
-  if ((st = check_tokens(dy, n.B, n.H, n.T, n.d, h->dtype)) != TTT_OK) return st;
-  if (dres && (st = check_tokens(dres, n.B, n.H, n.T, n.d, h->dtype)) != TTT_OK) return st;
-  if ((st = check_out_tokens(dh, n, n.d, h->dtype)) != TTT_OK) return st;
+  if ((st = norm_check(h, weight, eps, &n, &a.w_sh, &a.wide)) != TTT_OK) return st;
+  if ((st = check_rows(dy, n.B, n.H, n.T, n.d, h->dtype, &a.wide)) != TTT_OK) return st;
+  if (dres && (st = check_rows(dres, n.B, n.H, n.T, n.d, h->dtype, &a.wide)) != TTT_OK) return st;
+  if ((st = check_out_rows(dh, n, n.d, h->dtype, &a.wide)) != TTT_OK) return st;
   if (dweight->ndim != weight->ndim) return TTT_ERR_SHAPE;
   if ((st = check_f32(dweight, weight->ndim, weight->shape, false)) != TTT_OK) return st;
   const ttt_tensor* const ins[] = {h, weight, dy, dres};
@@ -1060,11 +1083,12 @@ namespace {
 
 // What the three convolution calls share: x, weight, bias.
 ttt_status conv_check(const ttt_tensor* x, const ttt_tensor* weight, const ttt_tensor* bias,
-                      int32_t silu, Dims* n, int64_t* K) {
+                      int32_t silu, Dims* n, int64_t* K, bool* wide) {
+  *wide = true;
   ttt_status st;
   if ((st = token_dims(x, n)) != TTT_OK) return st;
   if (silu != 0 && silu != 1) return TTT_ERR_ARG;
-  if ((st = check_tokens(x, n->B, n->H, n->T, n->d, x->dtype)) != TTT_OK) return st;
+  if ((st = check_rows(x, n->B, n->H, n->T, n->d, x->dtype, wide)) != TTT_OK) return st;
   if (weight->ndim != 3) return TTT_ERR_SHAPE;
   *K = weight->shape[2];
   if (*K < 1) return TTT_ERR_SHAPE;
@@ -1076,11 +1100,11 @@ ttt_status conv_check(const ttt_tensor* x, const ttt_tensor* weight, const ttt_t
 
 // A convolution's state tensor [S,H,K-1,d].
 ttt_status conv_state(const ttt_tensor* t, int64_t S, const Dims& n, int64_t K, int32_t dtype,
-                      bool written) {
+                      bool written, bool* wide) {
   if (!t) return TTT_OK;
   const Dims m = {S, n.H, K - 1, n.d};
-  return written ? check_out_tokens(t, m, n.d, dtype)
-                 : check_tokens(t, S, n.H, K - 1, n.d, dtype);
+  return written ? check_out_rows(t, m, n.d, dtype, wide)
+                 : check_rows(t, S, n.H, K - 1, n.d, dtype, wide);
 }
 
 }  // namespace
@@ -1095,11 +1119,11 @@ ttt_status causal_conv_fwd(const ttt_tensor* x, const ttt_tensor* weight, const 
   int64_t K;
   ttt::ConvArgs a;
   ttt_status st;
-  if ((st = conv_check(x, weight, bias, silu, &n, &K)) != TTT_OK) return st;
+  if ((st = conv_check(x, weight, bias, silu, &n, &K, &a.wide)) != TTT_OK) return st;
   if ((st = check_seqs(cu_seqlens, n, &a.seqs)) != TTT_OK) return st;
-  if ((st = conv_state(state0, a.seqs.S, n, K, x->dtype, false)) != TTT_OK) return st;
-  if ((st = conv_state(state_final, a.seqs.S, n, K, x->dtype, true)) != TTT_OK) return st;
-  if ((st = check_out_tokens(out, n, n.d, x->dtype)) != TTT_OK) return st;
+  if ((st = conv_state(state0, a.seqs.S, n, K, x->dtype, false, &a.wide)) != TTT_OK) return st;
+  if ((st = conv_state(state_final, a.seqs.S, n, K, x->dtype, true, &a.wide)) != TTT_OK) return st;
+  if ((st = check_out_rows(out, n, n.d, x->dtype, &a.wide)) != TTT_OK) return st;
   const ttt_tensor* const ins[] = {x, weight, bias, state0, cu_seqlens};
   const ttt_tensor* const outs[] = {out, state_final};
   if (clash(ins, outs)) return TTT_ERR_ARG;
@@ -1130,13 +1154,13 @@ ttt_status causal_conv_bwd(const ttt_tensor* x, const ttt_tensor* weight, const 
   int64_t K;
   ttt::ConvBwdArgs a;
   ttt_status st;
-  if ((st = conv_check(x, weight, bias, silu, &n, &K)) != TTT_OK) return st;
+  if ((st = conv_check(x, weight, bias, silu, &n, &K, &a.wide)) != TTT_OK) return st;
   if ((st = check_seqs(cu_seqlens, n, &a.seqs)) != TTT_OK) return st;
-  if ((st = conv_state(state0, a.seqs.S, n, K, x->dtype, false)) != TTT_OK) return st;
-  if ((st = conv_state(dstate_final, a.seqs.S, n, K, x->dtype, false)) != TTT_OK) return st;
-  if ((st = conv_state(dstate0, a.seqs.S, n, K, x->dtype, true)) != TTT_OK) return st;
-  if ((st = check_tokens(dy, n.B, n.H, n.T, n.d, x->dtype)) != TTT_OK) return st;
-  if ((st = check_out_tokens(dx, n, n.d, x->dtype)) != TTT_OK) return st;
+  if ((st = conv_state(state0, a.seqs.S, n, K, x->dtype, false, &a.wide)) != TTT_OK) return st;
+  if ((st = conv_state(dstate_final, a.seqs.S, n, K, x->dtype, false, &a.wide)) != TTT_OK) return st;
+  if ((st = conv_state(dstate0, a.seqs.S, n, K, x->dtype, true, &a.wide)) != TTT_OK) return st;
+  if ((st = check_rows(dy, n.B, n.H, n.T, n.d, x->dtype, &a.wide)) != TTT_OK) return st;
+  if ((st = check_out_rows(dx, n, n.d, x->dtype, &a.wide)) != TTT_OK) return st;
   const int64_t shape[3] = {n.H, n.d, K};
   if ((st = check_f32(dweight, 3, shape, false)) != TTT_OK) return st;
   if ((st = check_f32(dbias, 2, shape, true)) != TTT_OK) return st;
@@ -1173,12 +1197,12 @@ ttt_status causal_conv_step(const ttt_tensor* x, const ttt_tensor* state, const 
   int64_t K;
   ttt::ConvStepArgs a;
   ttt_status st;
-  if ((st = conv_check(x, weight, bias, silu, &n, &K)) != TTT_OK) return st;
+  if ((st = conv_check(x, weight, bias, silu, &n, &K, &a.wide)) != TTT_OK) return st;
   if (n.T != 1 || state->ndim != 4 || state->shape[0] < 1) return TTT_ERR_SHAPE;
   const int64_t S = state->shape[0];
   if ((st = check_slots(slots, n, S, &a.slots)) != TTT_OK) return st;
-  if ((st = conv_state(state, S, n, K, x->dtype, true)) != TTT_OK) return st;
-  if ((st = check_out_tokens(out, n, n.d, x->dtype)) != TTT_OK) return st;
+  if ((st = conv_state(state, S, n, K, x->dtype, true, &a.wide)) != TTT_OK) return st;
+  if ((st = check_out_rows(out, n, n.d, x->dtype, &a.wide)) != TTT_OK) return st;
   const ttt_tensor* const ins[] = {x, weight, bias, slots};
   const ttt_tensor* const outs[] = {out, state};
   if (clash(ins, outs)) return TTT_ERR_ARG;
@@ -1204,14 +1228,15 @@ namespace {
 ttt_status scan_check(const ttt_tensor* x, const ttt_tensor* dt, const ttt_tensor* A,
                       const ttt_tensor* Bm, const ttt_tensor* Cm, const ttt_tensor* D,
                       const ttt_tensor* z, const ttt_tensor* dt_bias, int32_t softplus, Dims* n,
-                      int64_t* N, int64_t* G) {
+                      int64_t* N, int64_t* G, bool* wide) {
+  *wide = true;
   ttt_status st;
   if ((st = token_dims(x, n)) != TTT_OK) return st;
   if (softplus != 0 && softplus != 1) return TTT_ERR_ARG;
   const int32_t ty = x->dtype;
-  if ((st = check_tokens(x, n->B, n->H, n->T, n->d, ty)) != TTT_OK) return st;
-  if ((st = check_tokens(dt, n->B, n->H, n->T, n->d, ty)) != TTT_OK) return st;
-  if (z && (st = check_tokens(z, n->B, n->H, n->T, n->d, ty)) != TTT_OK) return st;
+  if ((st = check_rows(x, n->B, n->H, n->T, n->d, ty, wide)) != TTT_OK) return st;
+  if ((st = check_rows(dt, n->B, n->H, n->T, n->d, ty, wide)) != TTT_OK) return st;
+  if (z && (st = check_rows(z, n->B, n->H, n->T, n->d, ty, wide)) != TTT_OK) return st;
   if (A->ndim != 3 || Bm->ndim != 4) return TTT_ERR_SHAPE;
   *N = A->shape[2];
   *G = Bm->shape[1];
@@ -1222,8 +1247,8 @@ ttt_status scan_check(const ttt_tensor* x, const ttt_tensor* dt, const ttt_tenso
   if ((st = check_f32(A, 3, shape, false)) != TTT_OK) return st;
   if ((st = check_f32(D, 2, shape, true)) != TTT_OK) return st;
   if ((st = check_f32(dt_bias, 2, shape, true)) != TTT_OK) return st;
-  if ((st = check_tokens(Bm, n->B, *G, n->T, *N, ty)) != TTT_OK) return st;
-  return check_tokens(Cm, n->B, *G, n->T, *N, ty);
+  if ((st = check_rows(Bm, n->B, *G, n->T, *N, ty, wide)) != TTT_OK) return st;
+  return check_rows(Cm, n->B, *G, n->T, *N, ty, wide);
 }
 
 void scan_args(ttt::ScanArgs* a, const ttt_tensor* x, const ttt_tensor* dt, const ttt_tensor* A,
@@ -1261,12 +1286,13 @@ ttt_status selective_scan_fwd(const ttt_tensor* x, const ttt_tensor* dt, const t
   int64_t N, G;
   ttt::ScanArgs a;
   ttt_status st;
-  if ((st = scan_check(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, &n, &N, &G)) != TTT_OK) return st;
+  if ((st = scan_check(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, &n, &N, &G,
+                       &a.wide)) != TTT_OK) return st;
   if ((st = check_seqs(cu_seqlens, n, &a.seqs)) != TTT_OK) return st;
   const int64_t hs[4] = {a.seqs.S, n.H, n.d, N};
   if ((st = check_f32(h0, 4, hs, true)) != TTT_OK) return st;
   if ((st = check_f32(h_final, 4, hs, true)) != TTT_OK) return st;
-  if ((st = check_out_tokens(out, n, n.d, x->dtype)) != TTT_OK) return st;
+  if ((st = check_out_rows(out, n, n.d, x->dtype, &a.wide)) != TTT_OK) return st;
   const ttt_tensor* const ins[] = {x, dt, A, Bm, Cm, D, z, dt_bias, h0, cu_seqlens};
   const ttt_tensor* const outs[] = {out, h_final};
   if (clash(ins, outs)) return TTT_ERR_ARG;
@@ -1301,7 +1327,8 @@ ttt_status selective_scan_bwd(const ttt_tensor* x, const ttt_tensor* dt, const t
   int64_t N, G;
   ttt::ScanBwdArgs g;
   ttt_status st;
-  if ((st = scan_check(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, &n, &N, &G)) != TTT_OK) return st;
+  if ((st = scan_check(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, &n, &N, &G,
+                       &g.f.wide)) != TTT_OK) return st;
   if ((st = check_seqs(cu_seqlens, n, &g.f.seqs)) != TTT_OK) return st;
   const int32_t ty = x->dtype;
   const int64_t hs[4] = {g.f.seqs.S, n.H, n.d, N};
@@ -1309,12 +1336,12 @@ ttt_status selective_scan_bwd(const ttt_tensor* x, const ttt_tensor* dt, const t
   if ((st = check_f32(h0, 4, hs, true)) != TTT_OK) return st;
   if ((st = check_f32(dh_final, 4, hs, true)) != TTT_OK) return st;
   if ((st = check_f32(dh0, 4, hs, true)) != TTT_OK) return st;
-  if ((st = check_tokens(dy, n.B, n.H, n.T, n.d, ty)) != TTT_OK) return st;
-  if ((st = check_out_tokens(dx, n, n.d, ty)) != TTT_OK) return st;
-  if ((st = check_out_tokens(ddt, n, n.d, ty)) != TTT_OK) return st;
-  if (dz && (st = check_out_tokens(dz, n, n.d, ty)) != TTT_OK) return st;
-  if ((st = check_out_tokens(dBm, gn, N, ty)) != TTT_OK) return st;
-  if ((st = check_out_tokens(dCm, gn, N, ty)) != TTT_OK) return st;
+  if ((st = check_rows(dy, n.B, n.H, n.T, n.d, ty, &g.f.wide)) != TTT_OK) return st;
+  if ((st = check_out_rows(dx, n, n.d, ty, &g.f.wide)) != TTT_OK) return st;
+  if ((st = check_out_rows(ddt, n, n.d, ty, &g.f.wide)) != TTT_OK) return st;
+  if (dz && (st = check_out_rows(dz, n, n.d, ty, &g.f.wide)) != TTT_OK) return st;
+  if ((st = check_out_rows(dBm, gn, N, ty, &g.f.wide)) != TTT_OK) return st;
+  if ((st = check_out_rows(dCm, gn, N, ty, &g.f.wide)) != TTT_OK) return st;
   if ((st = check_f32(dA, 3, hs + 1, false)) != TTT_OK) return st;
   if ((st = check_f32(dD, 2, hs + 1, true)) != TTT_OK) return st;
   if ((st = check_f32(ddt_bias, 2, hs + 1, true)) != TTT_OK) return st;
@@ -1352,17 +1379,20 @@ ttt_status selective_scan_step(const ttt_tensor* x, const ttt_tensor* dt, const 
   Dims n;
   int64_t N, G;
   ttt::ScanStepArgs a;
+  bool rows_wide;  // single values are read: no difference
   ttt_status st;
-  if ((st = scan_check(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, &n, &N, &G)) != TTT_OK) return st;
+  if ((st = scan_check(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, &n, &N, &G,
+                       &rows_wide)) != TTT_OK) return st;
   if (n.T != 1 || state->ndim != 4 || state->shape[0] < 1) return TTT_ERR_SHAPE;
   const int64_t S = state->shape[0];
   if ((st = check_slots(slots, n, S, &a.slots)) != TTT_OK) return st;
   const int64_t hs[4] = {S, n.H, n.d, N};
   if ((st = check_f32(state, 4, hs, false)) != TTT_OK) return st;
-  if ((st = check_out_tokens(out, n, n.d, x->dtype)) != TTT_OK) return st;
+  if ((st = check_out_rows(out, n, n.d, x->dtype, &rows_wide)) != TTT_OK) return st;
   const ttt_tensor* const ins[] = {x, dt, A, Bm, Cm, D, z, dt_bias, slots};
   const ttt_tensor* const outs[] = {out, state};
   if (clash(ins, outs)) return TTT_ERR_ARG;
+  a.wide = aligned16(state->data) && aligned16(A->data);
   a.x = view(x);
   a.dt = view(dt);
   a.z = view_or_null(z);

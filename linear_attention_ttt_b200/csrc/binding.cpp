@@ -1,0 +1,133 @@
+// Native half of the Python binding for the recurrent block's entry points
+// (include/ttt.h): fills the ttt_tensor descriptors from torch tensors and
+// calls the C function, about 1 us instead of the 15 us that building a dozen
+// descriptors in Python takes. A single-token step's kernel runs 3 to 6 us.
+//
+// call(function, tensors, split, scalar, stream, name) -> status. `function` is the
+// C function's address (from the loaded library), `tensors` a tuple of tensors
+// or None, the scalar argument goes behind the first `split` of them. `stream`
+// is None for the tensors' device's current stream, or a stream's handle.
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <c10/cuda/CUDAGuard.h>
+#include <c10/cuda/CUDAStream.h>
+
+#include <utility>
+
+#include "../../include/ttt.h"
+
+namespace {
+
+constexpr size_t kMost = 24;
+
+template <size_t NA, size_t NB, typename S, size_t... A, size_t... B>
+ttt_status invoke(void* f, ttt_tensor* const* t, S scalar, void* stream, std::index_sequence<A...>,
+                  std::index_sequence<B...>) {
+  using At = const ttt_tensor*;
+  using F = ttt_status (*)(decltype((void)A, At())..., S, decltype((void)B, At())..., void*);
+  return reinterpret_cast<F>(f)(t[A]..., scalar, t[NA + B]..., stream);
+}
+template <size_t NA, size_t NB, typename S>
+ttt_status invoke(void* f, ttt_tensor* const* t, S scalar, void* stream) {
+  return invoke<NA, NB, S>(f, t, scalar, stream, std::make_index_sequence<NA>(), std::make_index_sequence<NB>());
+}
+
+PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+  if (nargs != 6 || !PyTuple_Check(args[1])) {
+    PyErr_SetString(PyExc_TypeError, "call(function, tensors, split, scalar, stream, name)");
+    return nullptr;
+  }
+  void* fn = PyLong_AsVoidPtr(args[0]);
+  const Py_ssize_t n = PyTuple_GET_SIZE(args[1]);
+  const long split = PyLong_AsLong(args[2]);
+  const bool real = PyFloat_Check(args[3]);
+  const double fs = real ? PyFloat_AS_DOUBLE(args[3]) : 0.0;
+  const long is = real ? 0 : PyLong_AsLong(args[3]);
+  void* given = args[4] == Py_None ? nullptr : PyLong_AsVoidPtr(args[4]);
+  const char* name = PyUnicode_AsUTF8(args[5]);
+  if (PyErr_Occurred()) return nullptr;
+  if (!name || !fn || n > (Py_ssize_t)kMost) {
+    if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "no such call");
+    return nullptr;
+  }
+  ttt_tensor desc[kMost];
+  ttt_tensor* t[kMost] = {};
+  int device = -1;
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    PyObject* o = PyTuple_GET_ITEM(args[1], i);
+    if (o == Py_None) continue;
+    if (!THPVariable_Check(o)) {
+      PyErr_Format(PyExc_TypeError, "%s: argument %zd is not a tensor", name, i);
+      return nullptr;
+    }
+    const at::Tensor& v = THPVariable_Unpack(o);
+    const int on = v.is_cuda() ? v.get_device() : -1;
+    if (on < 0 || (device >= 0 && on != device)) {
+      PyErr_Format(PyExc_ValueError, "%s: tensors have to be on one CUDA device", name);
+      return nullptr;
+    }
+    device = on;
+    if (v.layout() != at::kStrided || v.dim() > 4) {
+      PyErr_Format(PyExc_ValueError, "%s: tensors have to be strided, of at most 4 dimensions", name);
+      return nullptr;
+    }
+    ttt_tensor& d = desc[i];
+    switch (v.scalar_type()) {
+      case at::kFloat: d.dtype = TTT_F32; break;
+      case at::kBFloat16: d.dtype = TTT_BF16; break;
+      case at::kInt: d.dtype = TTT_I32; break;
+      case at::kFloat8_e4m3fn: d.dtype = TTT_E4M3; break;
+      default:
+        PyErr_Format(PyExc_TypeError, "%s: unsupported dtype (argument %zd)", name, i);
+        return nullptr;
+    }
+    d.data = v.numel() ? v.data_ptr() : nullptr;
+    d.ndim = (int32_t)v.dim();
+    for (int k = 0; k < 4; ++k) {
+      d.shape[k] = k < d.ndim ? v.size(k) : 0;
+      d.stride[k] = k < d.ndim ? v.stride(k) : 0;
+    }
+    t[i] = &d;
+  }
+  if (device < 0) {
+    PyErr_Format(PyExc_TypeError, "%s: no tensor", name);
+    return nullptr;
+  }
+  ttt_status st = TTT_ERR_ARG;
+  bool known = true;
+  try {
+    const c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, (c10::DeviceIndex)device));
+    void* s = args[4] == Py_None ? (void*)c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream() : given;
+    Py_BEGIN_ALLOW_THREADS
+    const float f = (float)fs;
+    const int32_t k = (int32_t)is;
+    if (real && split == 3 && n == 6) st = invoke<3, 3>(fn, t, f, s);
+    else if (real && split == 4 && n == 6) st = invoke<4, 2>(fn, t, f, s);
+    else if (!real && split == 5 && n == 6) st = invoke<5, 1>(fn, t, k, s);
+    else if (!real && split == 5 && n == 7) st = invoke<5, 2>(fn, t, k, s);
+    else if (!real && split == 5 && n == 11) st = invoke<5, 6>(fn, t, k, s);
+    else if (!real && split == 10 && n == 11) st = invoke<10, 1>(fn, t, k, s);
+    else if (!real && split == 10 && n == 12) st = invoke<10, 2>(fn, t, k, s);
+    else if (!real && split == 10 && n == 21) st = invoke<10, 11>(fn, t, k, s);
+    else known = false;
+    Py_END_ALLOW_THREADS
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+    return nullptr;
+  }
+  if (!known) {
+    PyErr_Format(PyExc_ValueError, "%s: no such call", name);
+    return nullptr;
+  }
+  return PyLong_FromLong(st);
+}
+
+PyMethodDef methods[] = {
+    {"call", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(call)), METH_FASTCALL,
+     "call(function, tensors, split, scalar, stream, name) -> status"},
+    {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&module); }

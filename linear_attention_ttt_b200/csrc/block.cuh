@@ -22,6 +22,7 @@ struct NormArgs {
   float* scale;            // non-null: out is e4m3
   int64_t sc_sb, sc_sh, sc_st;
   int B, H, T, d;
+  bool wide;               // every token tensor's rows are 16-byte aligned
 };
 cudaError_t launch_rms_norm_fwd(const NormArgs& a, bool bf16, cudaStream_t s);
 
@@ -34,6 +35,7 @@ struct NormBwdArgs {
   float* dw;
   float* ws;
   int B, H, T, d;
+  bool wide;
 };
 size_t rms_norm_bwd_workspace(const NormBwdArgs& a, bool bf16);
 cudaError_t launch_rms_norm_bwd(const NormBwdArgs& a, bool bf16, cudaStream_t s);
@@ -50,6 +52,7 @@ struct ConvArgs {
   Seqs seqs;
   RowsView out, fin;       // fin.p null: not wanted
   int B, H, T, d, K, silu;
+  bool wide;
   int* status;
 };
 cudaError_t launch_causal_conv_fwd(const ConvArgs& a, bool bf16, cudaStream_t s);
@@ -62,6 +65,7 @@ struct ConvBwdArgs {
   float *dw, *dbias;       // dbias may be null
   float* ws;
   int B, H, T, d, K, silu;
+  bool wide;
   int* status;
 };
 size_t causal_conv_bwd_workspace(const ConvBwdArgs& a, bool bf16);
@@ -73,6 +77,7 @@ struct ConvStepArgs {
   const int32_t* slots;    // may be null
   const float *w, *bias;
   int B, S, H, d, K, silu;
+  bool wide;
   int* status;
 };
 cudaError_t launch_causal_conv_step(const ConvStepArgs& a, bool bf16, cudaStream_t s);
@@ -85,6 +90,7 @@ struct ScanArgs {
   float* h_final;          // may be null
   float* ws;
   int B, H, T, d, N, G, softplus;
+  bool wide;
   int* status;
 };
 size_t selective_scan_workspace(const ScanArgs& a);
@@ -108,6 +114,7 @@ struct ScanStepArgs {
   const int32_t* slots;
   TokViewMut out;
   int B, S, H, d, N, G, softplus;
+  bool wide;               // state and A are 16-byte aligned
   int* status;
 };
 cudaError_t launch_selective_scan_step(const ScanStepArgs& a, bool bf16, cudaStream_t s);
@@ -157,13 +164,14 @@ __device__ __forceinline__ Vec<__nv_bfloat16> pack<__nv_bfloat16>(const float (&
   return {make_uint4(w[0], w[1], w[2], w[3])};
 }
 
-// The first `n` elements (n may be <= 0) of the row piece at p, which is
-// 16-byte aligned; the rest reads as zero. A piece that ends inside the vector
-// is read element by element: nothing behind the row's end is touched.
+// The first `n` elements (n may be <= 0) of the row piece at p; the rest reads
+// as zero. A piece that ends inside the vector is read element by element, so
+// that nothing behind the row's end is touched, and so is every piece where
+// the call's rows are not all 16-byte aligned (wide is false).
 template <typename T>
-__device__ __forceinline__ Vec<T> load_vec(const T* p, int n) {
+__device__ __forceinline__ Vec<T> load_vec(const T* p, int n, bool wide) {
   Vec<T> r;
-  if (n >= Vec<T>::n) {
+  if (wide && n >= Vec<T>::n) {
     r.v = *reinterpret_cast<const uint4*>(p);
   } else {
     float f[Vec<T>::n];
@@ -182,8 +190,8 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
   return __float2bfloat16_rn(x);
 }
 template <typename T>
-__device__ __forceinline__ void store_vec(T* p, int n, const float (&f)[Vec<T>::n]) {
-  if (n >= Vec<T>::n) {
+__device__ __forceinline__ void store_vec(T* p, int n, bool wide, const float (&f)[Vec<T>::n]) {
+  if (wide && n >= Vec<T>::n) {
     *reinterpret_cast<uint4*>(p) = pack<T>(f).v;
   } else {
 #pragma unroll

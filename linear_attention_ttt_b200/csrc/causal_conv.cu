@@ -15,11 +15,11 @@ constexpr int kThreads = 128;
 // V channels of a token row, in fp32: 16 bytes of bf16 (V = 8) or fp32 (V = 4),
 // or 8 bytes of bf16 (V = 4).
 template <typename T, int V>
-__device__ __forceinline__ void load_row(const T* p, int n, float (&f)[V]) {
+__device__ __forceinline__ void load_row(const T* p, int n, bool wide, float (&f)[V]) {
   if constexpr (V * sizeof(T) == 16) {
-    unpack<T>(load_vec(p, n), f);
+    unpack<T>(load_vec(p, n, wide), f);
   } else {
-    if (n >= V) {
+    if (wide && n >= V) {
       const uint2 v = *reinterpret_cast<const uint2*>(p);
       f[0] = __uint_as_float(v.x << 16);
       f[1] = __uint_as_float(v.x & 0xffff0000u);
@@ -32,11 +32,11 @@ __device__ __forceinline__ void load_row(const T* p, int n, float (&f)[V]) {
   }
 }
 template <typename T, int V>
-__device__ __forceinline__ void store_row(T* p, int n, const float (&f)[V]) {
+__device__ __forceinline__ void store_row(T* p, int n, bool wide, const float (&f)[V]) {
   if constexpr (V * sizeof(T) == 16) {
-    store_vec<T>(p, n, f);
+    store_vec<T>(p, n, wide, f);
   } else {
-    if (n >= V) {
+    if (wide && n >= V) {
       const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
       *reinterpret_cast<uint2*>(p) =
           make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
@@ -103,15 +103,15 @@ __device__ __forceinline__ bool next_piece(const Seqs& q, const Run& r, int T, i
 // state before it.
 template <typename T, int K, int V>
 __device__ __forceinline__ void fill_window(const T* x, int64_t st, const TokView& state0, const Run& r,
-                                            const Piece& p, int t, float (&win)[K][V]) {
+                                            const Piece& p, int t, bool wide, float (&win)[K][V]) {
 #pragma unroll
   for (int i = 0; i < K - 1; ++i) {
     const int src = t - (K - 1) + i;
     if (src >= p.lo) {
-      load_row<T, V>(x + src * st, r.n, win[i]);
+      load_row<T, V>(x + src * st, r.n, wide, win[i]);
     } else if (state0.p) {
       const T* s0 = static_cast<const T*>(state0.p) + p.seq * state0.sb + r.h * state0.sh + r.c;
-      load_row<T, V>(s0 + (int64_t)(K - 1 + src - p.lo) * state0.st, r.n, win[i]);
+      load_row<T, V>(s0 + (int64_t)(K - 1 + src - p.lo) * state0.st, r.n, wide, win[i]);
     } else {
 #pragma unroll
       for (int j = 0; j < V; ++j) win[i][j] = 0.f;
@@ -148,12 +148,12 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(ConvArgs a, int len)
   do {
     const int t0 = max(p.lo, r.r0), t1 = min(p.hi, r.r1);
     float win[K][V];
-    fill_window<T, K, V>(x, a.x.st, a.state0, r, p, t0, win);
+    fill_window<T, K, V>(x, a.x.st, a.state0, r, p, t0, a.wide, win);
     for (int tb = t0; tb < t1; tb += kBatch) {
       Vec<T> in[kBatch];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i)
-        if (tb + i < t1) in[i] = load_vec(x + (tb + i) * a.x.st, r.n);
+        if (tb + i < t1) in[i] = load_vec(x + (tb + i) * a.x.st, r.n, a.wide);
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         if (tb + i >= t1) break;
@@ -168,13 +168,13 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(ConvArgs a, int len)
 #pragma unroll
           for (int k = 0; k < K - 1; ++k) win[k][j] = win[k + 1][j];
         }
-        store_vec<T>(out + (tb + i) * a.out.st, r.n, y);
+        store_vec<T>(out + (tb + i) * a.out.st, r.n, a.wide, y);
       }
     }
     if (a.fin.p && t1 == p.hi) {
       T* f = static_cast<T*>(a.fin.p) + p.seq * a.fin.sb + r.h * a.fin.sh + r.c;
 #pragma unroll
-      for (int k = 0; k < K - 1; ++k) store_vec<T>(f + k * a.fin.st, r.n, win[k]);
+      for (int k = 0; k < K - 1; ++k) store_vec<T>(f + k * a.fin.st, r.n, a.wide, win[k]);
     }
   } while (next_piece(a.seqs, r, a.T, a.status, &p));
 }
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(ConvBwdArgs a, int l
     const int t0 = max(p.lo, r.r0), t1 = min(p.hi, r.r1);
     const int first = t0 == p.lo ? p.lo - (K - 1) : t0;  // the state's inputs belong to the first run
     float win[K][V], dp[K][V];
-    fill_window<T, K, V>(x, a.x.st, a.state0, r, p, t0, win);
+    fill_window<T, K, V>(x, a.x.st, a.state0, r, p, t0, a.wide, win);
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
@@ -247,8 +247,8 @@ __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(ConvBwdArgs a, int l
         for (int j = 0; j < V; ++j) dp[k][j] = dp[k + 1][j];
       if (t < p.hi) {
         float g[V];
-        load_row<T, V>(x + t * a.x.st, r.n, win[K - 1]);
-        load_row<T, V>(dy + t * a.dy.st, r.n, g);
+        load_row<T, V>(x + t * a.x.st, r.n, a.wide, win[K - 1]);
+        load_row<T, V>(dy + t * a.dy.st, r.n, a.wide, g);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           if (a.silu) {
@@ -282,15 +282,15 @@ __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(ConvBwdArgs a, int l
       if (a.dfin.p && s >= p.hi - (K - 1)) {  // state_final holds this input
         float f[V];
         const T* df = static_cast<const T*>(a.dfin.p) + p.seq * a.dfin.sb + r.h * a.dfin.sh + r.c;
-        load_row<T, V>(df + (int64_t)(K - 1 + s - p.hi) * a.dfin.st, r.n, f);
+        load_row<T, V>(df + (int64_t)(K - 1 + s - p.hi) * a.dfin.st, r.n, a.wide, f);
 #pragma unroll
         for (int j = 0; j < V; ++j) o[j] += f[j];
       }
       if (s >= p.lo) {
-        store_row<T, V>(dx + s * a.dx.st, r.n, o);
+        store_row<T, V>(dx + s * a.dx.st, r.n, a.wide, o);
       } else if (a.dstate0.p) {
         T* d0 = static_cast<T*>(a.dstate0.p) + p.seq * a.dstate0.sb + r.h * a.dstate0.sh + r.c;
-        store_row<T, V>(d0 + (int64_t)(K - 1 + s - p.lo) * a.dstate0.st, r.n, o);
+        store_row<T, V>(d0 + (int64_t)(K - 1 + s - p.lo) * a.dstate0.st, r.n, a.wide, o);
       }
     }
   } while (next_piece(a.seqs, r, a.T, a.status, &p));
@@ -329,11 +329,11 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(ConvStepArgs a) {
   T* st = static_cast<T*>(a.state.p) + rows.slot * a.state.sb + r.h * a.state.sh + r.c;
   float win[K][V];
 #pragma unroll
-  for (int k = 0; k < K - 1; ++k) load_row<T, V>(st + k * a.state.st, r.n, win[k]);
+  for (int k = 0; k < K - 1; ++k) load_row<T, V>(st + k * a.state.st, r.n, a.wide, win[k]);
   do {
     const T* x = static_cast<const T*>(a.x.p) + rows.b * a.x.sb + r.h * a.x.sh + r.c;
     T* out = static_cast<T*>(a.out.p) + rows.b * a.out.sb + r.h * a.out.sh + r.c;
-    load_row<T, V>(x, r.n, win[K - 1]);
+    load_row<T, V>(x, r.n, a.wide, win[K - 1]);
     float y[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -344,10 +344,10 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(ConvStepArgs a) {
 #pragma unroll
       for (int k = 0; k < K - 1; ++k) win[k][j] = win[k + 1][j];
     }
-    store_row<T, V>(out, r.n, y);
+    store_row<T, V>(out, r.n, a.wide, y);
   } while (rows.next_row());
 #pragma unroll
-  for (int k = 0; k < K - 1; ++k) store_row<T, V>(st + k * a.state.st, r.n, win[k]);
+  for (int k = 0; k < K - 1; ++k) store_row<T, V>(st + k * a.state.st, r.n, a.wide, win[k]);
 }
 
 // f(integral constant K) for the call's K.

@@ -80,7 +80,7 @@ __device__ __forceinline__ float inv_rms(float sumsq, int d, float eps) {
   return m > 0.f || m != m ? rsqrtf(m) : 0.f;
 }
 
-__device__ __forceinline__ void store_e4m3(uint8_t* p, int n, const float* y, int count) {
+__device__ __forceinline__ void store_e4m3(uint8_t* p, int n, bool wide, const float* y, int count) {
 #pragma unroll
   for (int i = 0; i < 8; i += 4) {
     if (i >= count) break;
@@ -88,7 +88,7 @@ __device__ __forceinline__ void store_e4m3(uint8_t* p, int n, const float* y, in
     const uint32_t hi =
         __nv_cvt_float2_to_fp8x2(make_float2(y[i + 2], y[i + 3]), __NV_SATFINITE, __NV_E4M3);
     const uint32_t w = lo | hi << 16;
-    if (i + 4 <= n) {
+    if (wide && i + 4 <= n) {
       *reinterpret_cast<uint32_t*>(p + i) = w;
     } else {
 #pragma unroll
@@ -112,14 +112,14 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_kernel(NormArgs a, int l
   float s[VPT][V];
   float sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) unpack<T>(load_vec(x + (i * lanes + lane) * V, a.d - (i * lanes + lane) * V), s[i]);
+  for (int i = 0; i < VPT; ++i) unpack<T>(load_vec(x + (i * lanes + lane) * V, a.d - (i * lanes + lane) * V, a.wide), s[i]);
   if (a.r.p) {
     const T* res = static_cast<const T*>(a.r.p) + at.b * a.r.sb + at.h * a.r.sh + at.t * a.r.st;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = (i * lanes + lane) * V;
       float f[V];
-      unpack<T>(load_vec(res + c, a.d - c), f);
+      unpack<T>(load_vec(res + c, a.d - c, a.wide), f);
 #pragma unroll
       for (int j = 0; j < V; ++j) s[i][j] += f[j];
     }
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_kernel(NormArgs a, int l
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = (i * lanes + lane) * V;
-      store_vec<T>(ro + c, a.d - c, s[i]);
+      store_vec<T>(ro + c, a.d - c, a.wide, s[i]);
     }
   }
   const float rs = inv_rms(row_reduce<false>(sum, lanes, red), a.d, a.eps);
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_kernel(NormArgs a, int l
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = (i * lanes + lane) * V;
-      store_vec<T>(o + c, a.d - c, s[i]);
+      store_vec<T>(o + c, a.d - c, a.wide, s[i]);
     }
     return;
   }
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_kernel(NormArgs a, int l
     float q[8];
 #pragma unroll
     for (int j = 0; j < V; ++j) q[j] = s[i][j] / by;
-    store_e4m3(o + c, a.d - c, q, V);
+    store_e4m3(o + c, a.d - c, a.wide, q, V);
   }
 }
 
@@ -210,8 +210,8 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(NormBwdArgs a, in
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = (i * lanes + lane) * V;
-      hv[i] = load_vec(hp + c, live ? a.d - c : 0);
-      gv[i] = load_vec(gp + c, live ? a.d - c : 0);
+      hv[i] = load_vec(hp + c, live ? a.d - c : 0, a.wide);
+      gv[i] = load_vec(gp + c, live ? a.d - c : 0, a.wide);
     }
     float sum = 0.f, dot = 0.f;
 #pragma unroll
@@ -245,11 +245,11 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(NormBwdArgs a, in
       }
       if (rp) {
         float f[V];
-        unpack<T>(load_vec(rp + c, a.d - c), f);
+        unpack<T>(load_vec(rp + c, a.d - c, a.wide), f);
 #pragma unroll
         for (int j = 0; j < V; ++j) o[j] += f[j];
       }
-      store_vec<T>(op + c, a.d - c, o);
+      store_vec<T>(op + c, a.d - c, a.wide, o);
     }
   }
   float* dst = a.ws + ((int64_t)blockIdx.x * gridDim.y + head) * cols;

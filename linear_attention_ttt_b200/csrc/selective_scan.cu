@@ -149,9 +149,9 @@ __global__ void __launch_bounds__(128)
       const int row = tid / LPR + i * stride;
       if (row >= kTile) break;
       const int n = live >> row & 1 ? vn : 0;
-      xv[i] = load_vec(xp + (tb + row) * a.x.st, n);
-      const Vec<T> dv = load_vec(dp + (tb + row) * a.dt.st, n);
-      if (!kPre && zp) zv[i] = load_vec(zp + (tb + row) * a.z.st, n);
+      xv[i] = load_vec(xp + (tb + row) * a.x.st, n, a.wide);
+      const Vec<T> dv = load_vec(dp + (tb + row) * a.dt.st, n, a.wide);
+      if (!kPre && zp) zv[i] = load_vec(zp + (tb + row) * a.z.st, n, a.wide);
       float x[V], d[V], u[V];
       unpack<T>(xv[i], x);
       unpack<T>(dv, d);
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(128)
 #pragma unroll
         for (int v = 0; v < 8; v += V) {
           float f[V];
-          unpack<T>(load_vec(p + v, n - v), f);
+          unpack<T>(load_vec(p + v, n - v, a.wide), f);
 #pragma unroll
           for (int j = 0; j < V; j += 2)
             *reinterpret_cast<float4*>(s + 2 * (v + j)) = make_float4(f[j], f[j], f[j + 1], f[j + 1]);
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(128)
           v = fmaf(dskip[j], x[j], v);
           y[j] = zp ? v * silu_f(z[j]) : v;
         }
-        store_vec<T>(op + (tb + row) * a.out.st, vn, y);
+        store_vec<T>(op + (tb + row) * a.out.st, vn, a.wide, y);
       }
       __syncthreads();
     }
@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(ScanStepArgs a, int 
   const bool live = c < a.d;
   const int64_t ch = (int64_t)h * a.d + (live ? c : 0);
   const int left = live ? a.N - n0 : 0;
-  const bool whole = left >= 4 && a.N % 4 == 0;
+  const bool whole = a.wide && left >= 4 && a.N % 4 == 0;
   float A[4], s[4];
   float* sp = a.state + ((int64_t)rows.slot * a.H * a.d + ch) * a.N + n0;
   const float* ap = a.A + ch * a.N + n0;

@@ -145,7 +145,7 @@ struct Kernel {
       const T* xp = static_cast<const T*>(a.x.p) + q.b * a.x.sb + q.h * a.x.sh + q.c0 + vc + t * a.x.st;
       const T* dp = static_cast<const T*>(a.dt.p) + q.b * a.dt.sb + q.h * a.dt.sh + q.c0 + vc + t * a.dt.st;
       const T* gp = static_cast<const T*>(dy.p) + q.b * dy.sb + q.h * dy.sh + q.c0 + vc + t * dy.st;
-      const Vec<T> xv = load_vec(xp, n), dv = load_vec(dp, n), gv = load_vec(gp, n);
+      const Vec<T> xv = load_vec(xp, n, a.wide), dv = load_vec(dp, n, a.wide), gv = load_vec(gp, n, a.wide);
       float x[V], d[V], e[V], u[V];
       unpack<T>(xv, x);
       unpack<T>(dv, d);
@@ -153,7 +153,7 @@ struct Kernel {
       if (a.z.p) {
         const T* zp = static_cast<const T*>(a.z.p) + q.b * a.z.sb + q.h * a.z.sh + q.c0 + vc + t * a.z.st;
         float z[V];
-        unpack<T>(load_vec(zp, n), z);
+        unpack<T>(load_vec(zp, n, a.wide), z);
 #pragma unroll
         for (int j = 0; j < V; ++j) e[j] *= silu_f(z[j]);
       }
@@ -178,7 +178,7 @@ struct Kernel {
       const TokView& w = m ? a.Cm : a.Bm;
       const T* p = static_cast<const T*>(w.p) + q.b * w.sb + q.g * w.sh + (int64_t)(tb + row) * w.st + n0;
       float f[V];
-      unpack<T>(load_vec(p, n), f);
+      unpack<T>(load_vec(p, n, a.wide), f);
       float* s = (m ? s_c : s_b) + 2 * (row * states + n0);
 #pragma unroll
       for (int j = 0; j < V; j += 2)
@@ -481,15 +481,15 @@ __global__ void __launch_bounds__(128) main_kernel(ScanBwdArgs ga, Plan p, Ws ws
         if (!(m.live >> row & 1) || vn <= 0) continue;
         const int64_t t = tb + row;
         float x[V], z[V], g[V];
-        unpack<T>(load_vec(static_cast<const T*>(a.x.p) + q.b * a.x.sb + q.h * a.x.sh + q.c0 + vc + t * a.x.st, vn), x);
-        unpack<T>(load_vec(static_cast<const T*>(a.z.p) + q.b * a.z.sb + q.h * a.z.sh + q.c0 + vc + t * a.z.st, vn), z);
-        unpack<T>(load_vec(static_cast<const T*>(ga.dy.p) + q.b * ga.dy.sb + q.h * ga.dy.sh + q.c0 + vc + t * ga.dy.st, vn), g);
+        unpack<T>(load_vec(static_cast<const T*>(a.x.p) + q.b * a.x.sb + q.h * a.x.sh + q.c0 + vc + t * a.x.st, vn, a.wide), x);
+        unpack<T>(load_vec(static_cast<const T*>(a.z.p) + q.b * a.z.sb + q.h * a.z.sh + q.c0 + vc + t * a.z.st, vn, a.wide), z);
+        unpack<T>(load_vec(static_cast<const T*>(ga.dy.p) + q.b * ga.dy.sb + q.h * ga.dy.sh + q.c0 + vc + t * ga.dy.st, vn, a.wide), g);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           const float dskip = a.D && j < vn ? a.D[q.ch0 + vc + j] : 0.f;
           g[j] *= fmaf(dskip, x[j], joined(ysm, row, vc + j)) * dsilu_f(z[j]);
         }
-        store_vec<T>(static_cast<T*>(ga.dz.p) + q.b * ga.dz.sb + q.h * ga.dz.sh + q.c0 + vc + t * ga.dz.st, vn, g);
+        store_vec<T>(static_cast<T*>(ga.dz.p) + q.b * ga.dz.sb + q.h * ga.dz.sh + q.c0 + vc + t * ga.dz.st, vn, a.wide, g);
       }
       __syncthreads();
     }
@@ -581,8 +581,8 @@ __global__ void __launch_bounds__(128) main_kernel(ScanBwdArgs ga, Plan p, Ws ws
       if (!(m.live >> row & 1) || vn <= 0) continue;
       const int64_t t = tb + row;
       float x[V], raw[V], dx[V], dd[V];
-      unpack<T>(load_vec(static_cast<const T*>(a.x.p) + q.b * a.x.sb + q.h * a.x.sh + q.c0 + vc + t * a.x.st, vn), x);
-      unpack<T>(load_vec(static_cast<const T*>(a.dt.p) + q.b * a.dt.sb + q.h * a.dt.sh + q.c0 + vc + t * a.dt.st, vn), raw);
+      unpack<T>(load_vec(static_cast<const T*>(a.x.p) + q.b * a.x.sb + q.h * a.x.sh + q.c0 + vc + t * a.x.st, vn, a.wide), x);
+      unpack<T>(load_vec(static_cast<const T*>(a.dt.p) + q.b * a.dt.sb + q.h * a.dt.sh + q.c0 + vc + t * a.dt.st, vn, a.wide), raw);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const float dskip = a.D && j < vn ? a.D[q.ch0 + vc + j] : 0.f;
@@ -595,8 +595,8 @@ __global__ void __launch_bounds__(128) main_kernel(ScanBwdArgs ga, Plan p, Ws ws
         sD[j] = fmaf(e, x[j], sD[j]);
         sbias[j] += dd[j];
       }
-      store_vec<T>(static_cast<T*>(ga.dx.p) + q.b * ga.dx.sb + q.h * ga.dx.sh + q.c0 + vc + t * ga.dx.st, vn, dx);
-      store_vec<T>(static_cast<T*>(ga.ddt.p) + q.b * ga.ddt.sb + q.h * ga.ddt.sh + q.c0 + vc + t * ga.ddt.st, vn, dd);
+      store_vec<T>(static_cast<T*>(ga.dx.p) + q.b * ga.dx.sb + q.h * ga.dx.sh + q.c0 + vc + t * ga.dx.st, vn, a.wide, dx);
+      store_vec<T>(static_cast<T*>(ga.ddt.p) + q.b * ga.ddt.sb + q.h * ga.ddt.sh + q.c0 + vc + t * ga.ddt.st, vn, a.wide, dd);
     }
     // dB, dC over the block's channel tiles, to the block's slab
     const float* keep0 = s.keep - q.warp * (kPart / kBlk) * kPiece;

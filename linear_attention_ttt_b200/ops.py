@@ -9,7 +9,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 from typing import Optional
 
 import torch
@@ -316,57 +315,32 @@ def lact_swiglu_window_fwd(q, k, v, eta, W1, W2, W3, chunk: int, update_rule: in
 
 # ---- the recurrent block: RMS norm, short convolution, selective scan ---------
 
-_DTYPES = {torch.float32: TTT_F32, torch.bfloat16: TTT_BF16, torch.int32: TTT_I32,
-           torch.float8_e4m3fn: TTT_E4M3}
-_PACK = struct.Struct("=Qii4q4q").pack_into  # one TTTTensor
-_DESC = ctypes.sizeof(TTTTensor)
-_ZEROS = (0, 0, 0, 0)
+_ADDRESS = {}  # of the loaded library's functions
 
 
 def _block_call(name, tensors, split, scalar, stream):
     """Calls entry point `name` with the descriptors of `tensors` (None -> NULL), the
     scalar argument behind the first `split` of them. All tensors have to be on one
     CUDA device; the call is made with that device current, on `stream` or its current
-    stream."""
-    lib = load()
-    n = len(tensors)
-    buf = ctypes.create_string_buffer(n * _DESC)
-    base = ctypes.addressof(buf)
-    args = [None] * n
-    device = tensors[0].device
-    for i, t in enumerate(tensors):
-        if t is None:
-            continue
-        if t.device != device or device.type != "cuda":
-            raise ValueError(f"{name}: tensors have to be on one CUDA device, got {t.device}")
-        dt = _DTYPES.get(t.dtype)
-        if dt is None:
-            raise TypeError(f"{name}: unsupported dtype {t.dtype}")
-        shape, stride, nd = t.shape, t.stride(), t.dim()
-        if nd > 4:
-            raise ValueError(f"{name}: at most 4 dims")
-        _PACK(buf, i * _DESC, t.data_ptr(), dt, nd, *shape, *_ZEROS[nd:], *stride, *_ZEROS[nd:])
-        args[i] = base + i * _DESC
-    index = device.index
-    if index == torch.cuda.current_device():
-        code = getattr(lib, name)(*args[:split], scalar, *args[split:],
-                                  _block_stream(stream, index))
-    else:
-        with torch.cuda.device(index):
-            code = getattr(lib, name)(*args[:split], scalar, *args[split:],
-                                      _block_stream(stream, index))
-    _check(code, name)
-
-
-def _block_stream(stream, index):
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(index)
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    stream. csrc/binding.cpp does the marshalling."""
+    address = _ADDRESS.get(name)
+    if address is None:
+        from . import _binding
+        _ADDRESS[""] = _binding.call
+        address = ctypes.cast(getattr(load(), name), ctypes.c_void_p).value
+        _ADDRESS[name] = address
+    if stream is not None:
+        stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    code = _ADDRESS[""](address, tensors, split, scalar, stream, name)
+    if code != 0:
+        raise TTTError(code, name)
 
 
 def _like_tokens(x, d=None, dtype=None, zero=False):
     """A new token tensor [B,H,T,d] with x's order of storage (heads before or behind
     tokens) and rows of a multiple of 16 bytes."""
+    if not zero and d is None and x.is_contiguous() and x.shape[3] * (dtype or x.dtype).itemsize % 16 == 0:
+        return torch.empty_like(x, dtype=dtype)
     B, H, T = x.shape[:3]
     d = x.shape[3] if d is None else d
     dtype = dtype or x.dtype

@@ -164,7 +164,7 @@ def test_every_tensor_is_checked(lib, call):
         assert call()(lib, **{k: put(ndim=t.ndim % 4 + 1)}) == ERR["TTT_ERR_SHAPE"] or k == "weight", k
         assert call()(lib, **{k: put(shape={last: t.shape[last] + 1})}) < 0, k
         assert call()(lib, **{k: put(dtype=ops.TTT_E4M3)}) in (ERR["TTT_ERR_DTYPE"], ERR["TTT_ERR_NULL"]), k
-        assert call()(lib, **{k: put(data=FAKE + 60 * GAP + 2)}) == ERR["TTT_ERR_LAYOUT"], k
+        assert call()(lib, **{k: put(data=FAKE + 60 * GAP + 1)}) == ERR["TTT_ERR_LAYOUT"], k
         assert call()(lib, **{k: put(data=0)}) == ERR["TTT_ERR_NULL"], k
         assert call()(lib, **{k: put(stride={last: 2})}) == ERR["TTT_ERR_LAYOUT"], k
         if k not in OPTIONAL[call.name] and k not in ("cu", "slots", "bias", "dbias", "residual", "D", "z", "dt_bias",

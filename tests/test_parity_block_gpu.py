@@ -520,6 +520,51 @@ def test_offsets_out_of_order_or_range():
     clean()
 
 
+def test_rows_that_start_anywhere():
+    """Tensors whose rows are not 16-byte aligned give the same values, element by element."""
+    g = gen(41)
+    for dtype in (BF16, F32):
+        def moved(t):
+            """The same values, contiguous, one element behind an aligned address."""
+            if t is None:
+                return None
+            flat = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
+            return flat[1:].view(t.shape).copy_(t)
+        c, cc = scan_case(g, 2, 2, 45, 17, 12, dtype, G=2), conv_case(g, 2, 2, 45, 17, 4, dtype)
+        a, kw = scan_args(c)
+        mkw = {k: moved(v) if torch.is_tensor(v) else v for k, v in kw.items()}
+        want = ops.selective_scan_fwd(*a, h0=c["h0"], **kw)
+        out = moved(want[0]).zero_()
+        got = ops.selective_scan_fwd(*map(moved, a), h0=moved(c["h0"]), out=out, **mkw)
+        assert same(got, want)
+        want = ops.selective_scan_bwd(*a, c["dy"], h0=c["h0"], dh_final=c["dh"], **kw)
+        got = ops.selective_scan_bwd(*map(moved, a), moved(c["dy"]), h0=moved(c["h0"]), dh_final=moved(c["dh"]), **mkw)
+        assert same(got, want)
+        m = {k: moved(v) for k, v in cc.items()}
+        want = ops.causal_conv_fwd(cc["x"], cc["w"], cc["bias"], state0=cc["state"])
+        assert same(ops.causal_conv_fwd(m["x"], m["w"], m["bias"], state0=m["state"], out=moved(want[0]).zero_()), want)
+        want = ops.causal_conv_bwd(cc["x"], cc["w"], cc["dy"], cc["bias"], state0=cc["state"], dstate_final=cc["dfin"])
+        assert same(ops.causal_conv_bwd(m["x"], m["w"], m["dy"], m["bias"], state0=m["state"], dstate_final=m["dfin"]), want)
+        x, r, w = cc["x"], cc["dy"], torch.randn(17, generator=g).cuda()
+        for quant in (False, True):
+            want = ops.rms_norm_fwd(x, w, residual=r, quant=quant)
+            got = ops.rms_norm_fwd(moved(x), moved(w), residual=moved(r), quant=quant, out=moved(want[0].float()).to(want[0].dtype),
+                                   residual_out=moved(want[2]).zero_())
+            assert all(torch.equal(p.float(), q.float()) for p, q in zip(got, want) if p is not None)
+        assert same(ops.rms_norm_bwd(moved(x), moved(w), moved(r)), ops.rms_norm_bwd(x, w, r))
+        one = lambda v: v[:, :, :1]
+        pool, cpool = c["h0"].clone(), cc["state"].clone()
+        mpool, mcpool = moved(pool), moved(cpool)
+        want = ops.selective_scan_step(*(v if v.dim() == 3 else one(v) for v in a), pool, D=kw["D"], dt_bias=kw["dt_bias"])
+        got = ops.selective_scan_step(*(moved(v if v.dim() == 3 else one(v)) for v in a), mpool, D=mkw["D"], dt_bias=mkw["dt_bias"],
+                                      out=moved(want).zero_())
+        assert torch.equal(got, want) and torch.equal(pool, mpool)
+        want = ops.causal_conv_step(one(cc["x"]), cpool, cc["w"], cc["bias"])
+        got = ops.causal_conv_step(moved(one(cc["x"])), mcpool, m["w"], m["bias"], out=moved(want).zero_())
+        assert torch.equal(got, want) and torch.equal(cpool, mcpool)
+    clean()
+
+
 # ---- as they are used -------------------------------------------------------------------------
 
 class Block:
