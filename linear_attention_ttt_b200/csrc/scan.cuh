@@ -33,20 +33,36 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
-// 2^x; denormal results are 0.
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 __device__ __forceinline__ f2 ex2_pair(f2 x) {
   float a, b;
   un2(x, a, b);
   return mk2(ex2(a), ex2(b));
 }
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kNB = 16;  // states a warp holds
+constexpr int kNB = 16;    // states a warp holds
+constexpr int kCh = 16;    // channels a warp holds: a lane has 4 states of 2 channels
+constexpr int kPart = 32;  // tokens staged at once: one 32-bit mask
+constexpr int kPiece = kNB * kCh;  // a warp's states in memory: two float4 a lane
+// (float4 q of a lane: states 4*(lane&3) + 2q, +1, each with its two channels)
+
+// How a call's channels and states are laid over blocks of up to four warps:
+// channel tiles of one head beside one another, or a tile's 16-state parts.
+constexpr int tiles_per_block(int warps) { return warps >= 3 ? 1 : 4 / warps; }
+struct Grid {
+  int warps, tpb;   // 16-state warps a channel tile, channel tiles a block
+  int per_head;     // blocks a head
+  int64_t blocks;   // of the call: batch rows, heads
+  __host__ __device__ int wpb() const { return warps * tpb; }
+  __host__ __device__ int cw() const { return tpb * kCh; }  // channels a block
+};
+inline Grid grid_of(const ScanArgs& a) {
+  Grid g;
+  g.warps = (a.N + kNB - 1) / kNB;
+  g.tpb = tiles_per_block(g.warps);
+  g.per_head = (a.d + g.cw() - 1) / g.cw();
+  g.blocks = (int64_t)a.B * a.H * g.per_head;
+  return g;
+}
 
 // Step size from its raw value, and the derivative of the one by the other.
 __device__ __forceinline__ float step_of(float raw, int softplus) {
@@ -65,6 +81,135 @@ __device__ __forceinline__ TokenAt token_at(const Seqs& q, int b, int T, int t, 
     packed_seq(q.cu, r.seq, T, status, &r.lo, &r.hi);
     r.live = t >= r.lo && t < r.hi;
   }
+  return r;
+}
+
+// Which sequence events fall on a part's tokens.
+struct Marks {
+  uint32_t live, begin, end;
+};
+
+// What a block's threads know of their place.
+struct Place {
+  int tid, lane, warp, wt, wn;  // wt: the warp's channel tile in the block, wn: its 16 states
+  int sg, cg;                   // the lane's states 4 sg .. and channels 2 cg ..
+  int h, b, c0, g;              // head, batch row, first channel of the block, group
+  int64_t ch0;                  // h * d + c0
+};
+template <int W>
+__device__ __forceinline__ Place place(const ScanArgs& a, int per_head) {
+  constexpr int cw = tiles_per_block(W) * kCh;
+  Place q;
+  q.tid = threadIdx.x;
+  q.lane = q.tid & 31;
+  q.warp = q.tid >> 5;
+  q.wt = q.warp / W;
+  q.wn = q.warp % W;
+  q.sg = q.lane & 3;
+  q.cg = q.lane >> 2;
+  const int64_t blk = blockIdx.x;
+  q.c0 = (int)(blk % per_head) * cw;
+  q.h = (int)(blk / per_head % a.H);
+  q.b = (int)(blk / per_head / a.H);
+  q.g = q.h / (a.H / a.G);
+  q.ch0 = (int64_t)q.h * a.d + q.c0;
+  return q;
+}
+
+// Marks of the nt tokens at tb; *seq gets the lane's token's sequence.
+__device__ __forceinline__ Marks marks(const ScanArgs& a, const Place& q, int tb, int nt, int* seq) {
+  Marks m;
+  const TokenAt at = token_at(a.seqs, q.b, a.T, tb + q.lane, a.status);
+  const bool in = q.lane < nt && at.live;
+  m.live = __ballot_sync(0xffffffffu, in);
+  m.begin = __ballot_sync(0xffffffffu, in && tb + q.lane == at.lo);
+  m.end = __ballot_sync(0xffffffffu, in && tb + q.lane == at.hi - 1);
+  *seq = at.seq;
+  return m;
+}
+
+// The lane's decay rates, in powers of two.
+__device__ __forceinline__ void rates(const ScanArgs& a, const Place& q, f2 (&A2)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int n = q.wn * kNB + q.sg * 4 + k, c = q.wt * kCh + q.cg * 2;
+    float r[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      r[i] = n < a.N && q.c0 + c + i < a.d ? a.A[(q.ch0 + c + i) * a.N + n] * kLog2e : 0.f;
+    A2[k] = mk2(r[0], r[1]);
+  }
+}
+
+// The lane's elements of a [S,H,d,N] tensor's row `seq` (zeros for null).
+__device__ __forceinline__ void seq_state(const ScanArgs& a, const Place& q, const float* p, int seq,
+                                          f2 (&s)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int n = q.wn * kNB + q.sg * 4 + k, c = q.wt * kCh + q.cg * 2;
+    float r[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      r[i] = p && n < a.N && q.c0 + c + i < a.d ? p[((int64_t)seq * a.H * a.d + q.ch0 + c + i) * a.N + n] : 0.f;
+    s[k] = mk2(r[0], r[1]);
+  }
+}
+__device__ __forceinline__ void put_state(const ScanArgs& a, const Place& q, float* p, int seq,
+                                          const f2 (&s)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int n = q.wn * kNB + q.sg * 4 + k, c = q.wt * kCh + q.cg * 2;
+    float r[2];
+    un2(s[k], r[0], r[1]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (n < a.N && q.c0 + c + i < a.d) p[((int64_t)seq * a.H * a.d + q.ch0 + c + i) * a.N + n] = r[i];
+  }
+}
+
+// A warp's states as a piece of memory.
+__device__ __forceinline__ void load4(const float* p, int lane, f2 (&s)[4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const ulonglong2 v = reinterpret_cast<const ulonglong2*>(p)[i * 32 + lane];
+    s[2 * i] = v.x;
+    s[2 * i + 1] = v.y;
+  }
+}
+__device__ __forceinline__ void store4(float* p, int lane, const f2 (&s)[4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    reinterpret_cast<ulonglong2*>(p)[i * 32 + lane] = make_ulonglong2(s[2 * i], s[2 * i + 1]);
+}
+// Four states' values (each twice) of a token in shared memory.
+__device__ __forceinline__ void four(const float* s, f2 (&v)[4]) {
+  const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(s), b = *reinterpret_cast<const ulonglong2*>(s + 4);
+  v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+}
+
+// f(integral constant) for the 16-state warps a tile has.
+template <typename F>
+cudaError_t for_warps(int warps, F f) {
+  switch (warps) {
+    case 1: return f(std::integral_constant<int, 1>());
+    case 2: return f(std::integral_constant<int, 2>());
+    case 3: return f(std::integral_constant<int, 3>());
+    case 4: return f(std::integral_constant<int, 4>());
+  }
+  return cudaErrorInvalidValue;
+}
+
+// Where element e of [blocks][warps a block][kPiece] stands.
+struct PieceAt {
+  int64_t blk;
+  int n, cb;  // state, channel in the block
+};
+__host__ __device__ __forceinline__ PieceAt piece_at(int64_t e, const Grid& g) {
+  const int in = (int)(e % kPiece), lane = in % 128 / 4, warp = (int)(e / kPiece % g.wpb());
+  PieceAt r;
+  r.blk = e / kPiece / g.wpb();
+  r.n = warp % g.warps * kNB + (lane & 3) * 4 + in / 128 * 2 + in % 4 / 2;
+  r.cb = warp / g.warps * kCh + (lane >> 2) * 2 + in % 2;
   return r;
 }
 

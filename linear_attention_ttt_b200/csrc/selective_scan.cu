@@ -1,12 +1,12 @@
 // Selective scan, forward for prompts and single tokens (selective_scan_fwd,
 // selective_scan_step of include/ttt.h).
 //
-// A warp holds 16 states of 32 channels: a lane has 4 states of 4 channels,
-// so the sum over states takes three shuffles a token and the inputs of a
-// token are four 16-byte reads of shared memory. N > 16 gives a channel tile
-// a warp per 16 states, which add their parts of y through shared memory.
-// The tokens of a tile (16) are staged once: softplus, the products D_t x_t
-// and the gate are computed once per element, from 16-byte loads.
+// A warp holds 16 states of 16 channels: a lane has 4 states of 2 channels, so
+// the sum over states takes two shuffles a token and the inputs of a token are
+// a few wide reads of shared memory. N > 16 gives a channel tile a warp per 16
+// states, which add their parts of y through shared memory. The tokens of a
+// part (32) are staged once: softplus, the products D_t x_t and the gate are
+// computed once per element, from 16-byte loads.
 //
 // What bounds it: one exponential and four fp32 operations per (channel,
 // state, token). The special-function unit gives 16 exponentials a clock and
@@ -22,302 +22,241 @@ namespace ttt {
 namespace scan {
 namespace {
 
-constexpr int kCh = 32;    // channels a tile
-constexpr int kTile = 16;  // tokens staged at once
-
-// A warp's piece of the joined states: 512 floats, 16 a lane, as four float4
-// (state 4*(lane&3) + k, channels 4*(lane>>2) .. +3).
-constexpr int kPiece = kNB * kCh;
-
-struct Plan {
-  int warps;      // 16-state warps a channel tile
-  int64_t tiles;  // channel tiles of the call (batch rows, heads)
-  int chunks, len;
+struct Plan : Grid {
+  int chunks, len;  // len: tokens, a multiple of kPart
 };
 Plan plan(const ScanArgs& a) {
   Plan p;
-  p.warps = (a.N + kNB - 1) / kNB;
-  p.tiles = (int64_t)a.B * a.H * ((a.d + kCh - 1) / kCh);
-  const int64_t have = p.tiles * p.warps, want = 148 * 16;
+  static_cast<Grid&>(p) = grid_of(a);
+  const int64_t have = p.blocks * p.wpb(), want = 148 * 16;
   int64_t c = (want + have - 1) / have;
   const int64_t most = (a.T + 63) / 64;
   c = c < most ? c : most;
   c = c < 1 ? 1 : c;
-  p.len = (int)(((a.T + c - 1) / c + kTile - 1) / kTile * kTile);
-  if (p.len < kTile) p.len = kTile;
+  p.len = (int)(((a.T + c - 1) / c + kPart - 1) / kPart * kPart);
+  if (p.len < kPart) p.len = kPart;
   p.chunks = a.T > 0 ? (a.T + p.len - 1) / p.len : 0;
   return p;
 }
 
+// Shared memory: D_t, D_t x_t [token][channel], B, C [token][state] (each value
+// twice), and y of the block's warps where a tile has several.
+size_t smem_bytes(const Grid& g, bool pre) {
+  const int states = g.warps * kNB;
+  return (size_t)kPart * (2 * g.cw() + (pre ? 2 : 4) * states + (g.warps > 1 && !pre ? g.wpb() * kCh : 0)) *
+         sizeof(float);
+}
+
 // kPre: the first pass over a chunk (its end state and sum of D_t); otherwise
-// the outputs.
-template <typename T, bool kPre>
-__global__ void __launch_bounds__(128)
-    scan_kernel(ScanArgs a, int len, int64_t tiles, float* states, float* sums, int* cuts) {
-  constexpr int V = Vec<T>::n, LPR = kCh / V, MAXV = kTile * LPR / 32;
+// the outputs. A part's rows are loaded while the part before is scanned.
+template <typename T, int W, bool kPre>
+__global__ void __launch_bounds__(128, sizeof(T) == 2 ? 4 : 3)
+    scan_kernel(ScanArgs a, Plan p, float* states, float* sums, int* cuts) {
+  constexpr int V = Vec<T>::n, tpb = tiles_per_block(W), wpb = W * tpb;
+  constexpr int cw = tpb * kCh, ns = W * kNB, lpr = cw / V, spr = ns / V;
+  constexpr int dr = 32 * wpb / lpr, bdr = 32 * wpb / spr;  // rows between a thread's vectors
+  constexpr int kRows = (kPart + dr - 1) / dr, kBC = (kPart + bdr - 1) / bdr;
   extern __shared__ __align__(16) float sm[];
-  __shared__ int s_seq[kTile];
-  const int tid = threadIdx.x, lane = tid & 31, wb = tid >> 5, nw = blockDim.x >> 5;
-  const int sg = lane & 3, cg = lane >> 2;
+  __shared__ int s_seq[kPart];
+  const Place q = place<W>(a, p.per_head);
+  const int chunk = blockIdx.y;
   float* s_dt = sm;
-  float* s_u = s_dt + kTile * kCh;
-  float* s_b = s_u + kTile * kCh + wb * 2 * kTile * 2 * kNB;  // each value twice
-  float* s_c = s_b + kTile * 2 * kNB;
-  // one warp: y takes the place of u, token by token
-  float* s_y0 = nw == 1 ? s_u : s_u + kTile * kCh + nw * 2 * kTile * 2 * kNB;
-  float* s_y = s_y0 + wb * kTile * kCh;
+  float* s_u = s_dt + kPart * cw;
+  float* s_b = s_u + kPart * cw;
+  float* s_c = s_b + kPart * 2 * ns;
+  // one warp a tile: y takes the place of u, token by token
+  constexpr int ys = W == 1 ? cw : kCh;
+  float* s_y = W == 1 ? s_u + q.wt * kCh : s_c + kPart * 2 * ns + q.warp * kPart * kCh;
+  const int t0 = chunk * p.len, t1 = min(a.T, t0 + p.len);
 
-  const int cts = (a.d + kCh - 1) / kCh;
-  const int64_t tile = blockIdx.x;
-  const int ct = (int)(tile % cts), h = (int)(tile / cts % a.H), b = (int)(tile / cts / a.H);
-  const int c0 = ct * kCh, g = h / (a.H / a.G);
-  const int chunk = blockIdx.y, t0 = chunk * len, t1 = min(a.T, t0 + len);
+  f2 A2[4], hs[4] = {0, 0, 0, 0}, sum = 0;
+  rates(a, q, A2);
+  const int64_t piece = ((int64_t)chunk * p.blocks + blockIdx.x) * wpb + q.warp;
+  if (!kPre && chunk > 0) load4(states + piece * kPiece, q.lane, hs);
 
-  // decay rates of the lane's states and channels, in powers of two
-  f2 A2[4][2], hs[4][2];
-  const int64_t ch0 = (int64_t)h * a.d + c0;
-  {
-    float r[4][4];
+  // what the thread stages: channels vc .. of rows row0, row0 + dr, ..; states
+  // n0 .. of B's and C's rows
+  const int vc = q.tid % lpr * V, vn = a.d - q.c0 - vc, row0 = q.tid / lpr;
+  const int n0 = q.tid % spr * V, nn = a.N - n0, brow0 = q.tid / spr;
+  const T* xp = static_cast<const T*>(a.x.p) + q.b * a.x.sb + q.h * a.x.sh + q.c0 + vc;
+  const T* dp = static_cast<const T*>(a.dt.p) + q.b * a.dt.sb + q.h * a.dt.sh + q.c0 + vc;
+  const T* zp = !kPre && a.z.p ? static_cast<const T*>(a.z.p) + q.b * a.z.sb + q.h * a.z.sh + q.c0 + vc : nullptr;
+  const T* bp = static_cast<const T*>(a.Bm.p) + q.b * a.Bm.sb + q.g * a.Bm.sh + n0;
+  const T* cp = static_cast<const T*>(a.Cm.p) + q.b * a.Cm.sb + q.g * a.Cm.sh + n0;
+
+  Vec<T> xv[kRows], dv[kRows], zv[kRows], bv[kBC], cv[kBC];
+  Marks m;
+  int seq;
+  auto fetch = [&](int tb) {
+    m = marks(a, q, tb, min(kPart, t1 - tb), &seq);
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int n = wb * kNB + sg * 4 + k, cc = cg * 4 + c;
-        r[k][c] = n < a.N && c0 + cc < a.d ? a.A[(ch0 + cc) * a.N + n] * kLog2e : 0.f;
-      }
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        A2[k][p] = mk2(r[k][2 * p], r[k][2 * p + 1]);
-        hs[k][p] = 0;
-      }
-  }
-  const int64_t piece = ((int64_t)chunk * tiles + tile) * nw + wb;
-  if (!kPre && chunk > 0) {
-    const float4* in = reinterpret_cast<const float4*>(states + piece * kPiece);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float4 v = in[k * 32 + lane];
-      hs[k][0] = mk2(v.x, v.y);
-      hs[k][1] = mk2(v.z, v.w);
+    for (int i = 0; i < kRows; ++i) {
+      const int row = row0 + i * dr;
+      const int n = row < kPart && m.live >> row & 1 ? vn : 0;
+      const int64_t t = tb + row;
+      xv[i] = load_vec(xp + t * a.x.st, n, a.wide);
+      dv[i] = load_vec(dp + t * a.dt.st, n, a.wide);
+      if (zp) zv[i] = load_vec(zp + t * a.z.st, n, a.wide);
     }
-  }
-
-  // the channels a thread stages and writes: vc .. vc+V-1 of every row it has
-  const int vc = tid % LPR * V, vn = a.d - c0 - vc;
-  float bias[V], dskip[V];
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    bias[j] = a.dt_bias && j < vn ? a.dt_bias[ch0 + vc + j] : 0.f;
-    dskip[j] = !kPre && a.D && j < vn ? a.D[ch0 + vc + j] : 0.f;
-  }
-  const T* xp = static_cast<const T*>(a.x.p) + b * a.x.sb + h * a.x.sh + c0 + vc;
-  const T* dp = static_cast<const T*>(a.dt.p) + b * a.dt.sb + h * a.dt.sh + c0 + vc;
-  const T* zp = a.z.p ? static_cast<const T*>(a.z.p) + b * a.z.sb + h * a.z.sh + c0 + vc : nullptr;
-  const int bt = lane >> 1, bn = (lane & 1) * 8;  // token and first state a lane stages of B and C
-  const int bleft = a.N - wb * kNB - bn;
-  const T* bp = static_cast<const T*>(a.Bm.p) + b * a.Bm.sb + g * a.Bm.sh + wb * kNB + bn;
-  const T* cp = static_cast<const T*>(a.Cm.p) + b * a.Cm.sb + g * a.Cm.sh + wb * kNB + bn;
-  T* op = kPre ? nullptr : static_cast<T*>(a.out.p) + b * a.out.sb + h * a.out.sh + c0 + vc;
-
-  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < kBC; ++i) {
+      const int row = brow0 + i * bdr;
+      const int n = row < kPart && m.live >> row & 1 ? nn : 0;
+      bv[i] = load_vec(bp + (int64_t)(tb + row) * a.Bm.st, n, a.wide);
+      if (!kPre) cv[i] = load_vec(cp + (int64_t)(tb + row) * a.Cm.st, n, a.wide);
+    }
+  };
+  const int lane_c = q.wt * kCh + q.cg * 2, lane_s = q.wn * 2 * kNB + q.sg * 8;
   bool cut = false;  // a sequence began in this chunk
-  const int stride = blockDim.x / LPR;  // rows between a thread's vectors
 
-  for (int tb = t0; tb < t1; tb += kTile) {
-    const int nt = min(kTile, t1 - tb);
-    // which of the tile's tokens are somebody's, begin or end a sequence
-    uint32_t live, begin, end;
-    if (a.seqs.cu) {
-      const TokenAt at = token_at(a.seqs, b, a.T, tb + (lane & (kTile - 1)), a.status);
-      const bool in = lane < nt && at.live;
-      live = __ballot_sync(0xffffffffu, in);
-      begin = __ballot_sync(0xffffffffu, in && tb + lane == at.lo);
-      end = __ballot_sync(0xffffffffu, in && tb + lane == at.hi - 1);
-      if (wb == 0 && lane < kTile) s_seq[lane] = at.seq;
-    } else {
-      live = (1u << nt) - 1;
-      begin = tb == 0;
-      end = tb + nt == a.T ? 1u << (nt - 1) : 0;
-      if (tid == 0) s_seq[0] = s_seq[nt - 1] = b;
-    }
-    // stage the tile: D_t, D_t x_t, B and C
-    Vec<T> xv[MAXV], zv[MAXV];
+  fetch(t0);
+  for (int tb = t0; tb < t1; tb += kPart) {
+    const int nt = min(kPart, t1 - tb);
+    const Marks now = m;
+    // stage the part
+    Vec<T> xk[kRows], zk[kRows];  // for the outputs
 #pragma unroll
-    for (int i = 0; i < MAXV; ++i) {
-      const int row = tid / LPR + i * stride;
-      if (row >= kTile) break;
-      const int n = live >> row & 1 ? vn : 0;
-      xv[i] = load_vec(xp + (tb + row) * a.x.st, n, a.wide);
-      const Vec<T> dv = load_vec(dp + (tb + row) * a.dt.st, n, a.wide);
-      if (!kPre && zp) zv[i] = load_vec(zp + (tb + row) * a.z.st, n, a.wide);
+    for (int i = 0; i < kRows; ++i) {
+      const int row = row0 + i * dr;
+      if (row >= kPart) break;
       float x[V], d[V], u[V];
       unpack<T>(xv[i], x);
-      unpack<T>(dv, d);
+      unpack<T>(dv[i], d);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        d[j] = j < n ? step_of(d[j] + bias[j], a.softplus) : 0.f;
+        const float bias = a.dt_bias && j < vn ? a.dt_bias[q.ch0 + vc + j] : 0.f;
+        d[j] = step_of(d[j] + bias, a.softplus);
         u[j] = d[j] * x[j];
       }
 #pragma unroll
       for (int j = 0; j < V; j += 4) {
-        *reinterpret_cast<float4*>(s_dt + row * kCh + vc + j) = make_float4(d[j], d[j + 1], d[j + 2], d[j + 3]);
-        *reinterpret_cast<float4*>(s_u + row * kCh + vc + j) = make_float4(u[j], u[j + 1], u[j + 2], u[j + 3]);
+        *reinterpret_cast<float4*>(s_dt + row * cw + vc + j) = make_float4(d[j], d[j + 1], d[j + 2], d[j + 3]);
+        *reinterpret_cast<float4*>(s_u + row * cw + vc + j) = make_float4(u[j], u[j + 1], u[j + 2], u[j + 3]);
+      }
+      xk[i] = xv[i];
+      if (zp) zk[i] = zv[i];
+    }
+#pragma unroll
+    for (int i = 0; i < kBC; ++i) {
+      const int row = brow0 + i * bdr;
+      if (row >= kPart) break;
+#pragma unroll
+      for (int w = 0; w < (kPre ? 1 : 2); ++w) {
+        float f[V];
+        unpack<T>(w ? cv[i] : bv[i], f);
+        float* s = (w ? s_c : s_b) + 2 * (row * ns + n0);
+#pragma unroll
+        for (int j = 0; j < V; j += 2) *reinterpret_cast<float4*>(s + 2 * j) = make_float4(f[j], f[j], f[j + 1], f[j + 1]);
       }
     }
-    {
-      const int n = live >> bt & 1 ? bleft : 0;
-#pragma unroll
-      for (int m = 0; m < (kPre ? 1 : 2); ++m) {
-        const T* p = m ? cp + (tb + bt) * a.Cm.st : bp + (tb + bt) * a.Bm.st;
-        float* s = (m ? s_c : s_b) + bt * 2 * kNB + 2 * bn;
-#pragma unroll
-        for (int v = 0; v < 8; v += V) {
-          float f[V];
-          unpack<T>(load_vec(p + v, n - v, a.wide), f);
-#pragma unroll
-          for (int j = 0; j < V; j += 2)
-            *reinterpret_cast<float4*>(s + 2 * (v + j)) = make_float4(f[j], f[j], f[j + 1], f[j + 1]);
-        }
-      }
-    }
+    if (q.warp == 0) s_seq[q.lane] = seq;
     __syncthreads();
-    for (int t = 0; t < nt; ++t) {
-      if (begin >> t & 1) {
+    if (tb + kPart < t1) fetch(tb + kPart);
+
+    auto token = [&](int t, bool events) {
+      if (events && (now.begin >> t & 1)) {
         cut = true;
-        const int64_t row = (int64_t)s_seq[t] * a.H * a.d + ch0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float v[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int n = wb * kNB + sg * 4 + k, cc = cg * 4 + c;
-            v[c] = a.h0 && n < a.N && c0 + cc < a.d ? a.h0[(row + cc) * a.N + n] : 0.f;
-          }
-          hs[k][0] = mk2(v[0], v[1]);
-          hs[k][1] = mk2(v[2], v[3]);
-        }
+        seq_state(a, q, a.h0, s_seq[t], hs);
       }
-      const ulonglong2 dt = *reinterpret_cast<const ulonglong2*>(s_dt + t * kCh + cg * 4);
-      const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(s_u + t * kCh + cg * 4);
-      f2 bb[4], y[2] = {0, 0};
-      {
-        const ulonglong2 v0 = *reinterpret_cast<const ulonglong2*>(s_b + t * 2 * kNB + sg * 8);
-        const ulonglong2 v1 = *reinterpret_cast<const ulonglong2*>(s_b + t * 2 * kNB + sg * 8 + 4);
-        bb[0] = v0.x, bb[1] = v0.y, bb[2] = v1.x, bb[3] = v1.y;
-      }
+      const f2 dt = *reinterpret_cast<const f2*>(s_dt + t * cw + lane_c);
+      const f2 u = *reinterpret_cast<const f2*>(s_u + t * cw + lane_c);
+      f2 bb[4];
+      four(s_b + t * 2 * ns + lane_s, bb);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        hs[k][0] = fma2(ex2_pair(mul2(dt.x, A2[k][0])), hs[k][0], mul2(u.x, bb[k]));
-        hs[k][1] = fma2(ex2_pair(mul2(dt.y, A2[k][1])), hs[k][1], mul2(u.y, bb[k]));
-      }
+      for (int k = 0; k < 4; ++k) hs[k] = fma2(ex2_pair(mul2(dt, A2[k])), hs[k], mul2(u, bb[k]));
       if (kPre) {
-        float d0, d1, d2, d3;
-        un2(dt.x, d0, d1);
-        un2(dt.y, d2, d3);
-        sum[0] += d0, sum[1] += d1, sum[2] += d2, sum[3] += d3;
+        sum = add2(sum, dt);
       } else {
-        const ulonglong2 v0 = *reinterpret_cast<const ulonglong2*>(s_c + t * 2 * kNB + sg * 8);
-        const ulonglong2 v1 = *reinterpret_cast<const ulonglong2*>(s_c + t * 2 * kNB + sg * 8 + 4);
-        const f2 cc[4] = {v0.x, v0.y, v1.x, v1.y};
+        f2 cc[4];
+        four(s_c + t * 2 * ns + lane_s, cc);
+        f2 y = mul2(hs[0], cc[0]);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          y[0] = fma2(hs[k][0], cc[k], y[0]);
-          y[1] = fma2(hs[k][1], cc[k], y[1]);
-        }
-        // four channels over four lanes: halve twice, a channel a lane is left
-        float y0, y1, y2, y3;
-        un2(y[0], y0, y1);
-        un2(y[1], y2, y3);
-        const bool up = sg & 1;
-        const float p0 = __shfl_xor_sync(0xffffffffu, up ? y0 : y2, 1);
-        const float p1 = __shfl_xor_sync(0xffffffffu, up ? y1 : y3, 1);
-        const float q0 = (up ? y2 : y0) + p0, q1 = (up ? y3 : y1) + p1;
-        const bool up2 = sg & 2;
-        const float r = __shfl_xor_sync(0xffffffffu, up2 ? q0 : q1, 2);
-        s_y[t * kCh + cg * 4 + (up ? 2 : 0) + (up2 ? 1 : 0)] = (up2 ? q1 : q0) + r;
-        if ((end >> t & 1) && a.h_final) {
-          const int64_t row = (int64_t)s_seq[t] * a.H * a.d + ch0;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float v[4];
-            un2(hs[k][0], v[0], v[1]);
-            un2(hs[k][1], v[2], v[3]);
-            const int n = wb * kNB + sg * 4 + k;
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              if (n < a.N && c0 + cg * 4 + c < a.d) a.h_final[(row + cg * 4 + c) * a.N + n] = v[c];
-          }
-        }
+        for (int k = 1; k < 4; ++k) y = fma2(hs[k], cc[k], y);
+        // two channels over four lanes
+        float y0, y1;
+        un2(y, y0, y1);
+        const bool up = q.sg & 1;
+        float v = (up ? y1 : y0) + __shfl_xor_sync(0xffffffffu, up ? y0 : y1, 1);
+        v += __shfl_xor_sync(0xffffffffu, v, 2);
+        if (q.sg < 2) s_y[t * ys + q.cg * 2 + up] = v;
+        if (events && (now.end >> t & 1) && a.h_final) put_state(a, q, a.h_final, s_seq[t], hs);
       }
+    };
+    if (nt == kPart && !(now.begin | now.end)) {
+#pragma unroll 4
+      for (int t = 0; t < kPart; ++t) token(t, false);
+    } else {
+      for (int t = 0; t < nt; ++t) token(t, true);
     }
     __syncthreads();
     if (!kPre) {
 #pragma unroll
-      for (int i = 0; i < MAXV; ++i) {
-        const int row = tid / LPR + i * stride;
-        if (row >= kTile) break;
-        if (!(live >> row & 1)) continue;
+      for (int i = 0; i < kRows; ++i) {
+        const int row = row0 + i * dr;
+        if (row >= kPart) break;
+        if (!(now.live >> row & 1)) continue;
         float x[V], z[V], y[V];
-        unpack<T>(xv[i], x);
-        if (zp) unpack<T>(zv[i], z);
+        unpack<T>(xk[i], x);
+        if (zp) unpack<T>(zk[i], z);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          float v = s_y0[row * kCh + vc + j];
-          for (int w = 1; w < nw; ++w) v += s_y0[(w * kTile + row) * kCh + vc + j];
-          v = fmaf(dskip[j], x[j], v);
+          float v;
+          if (W == 1) {
+            v = s_u[row * cw + vc + j];
+          } else {
+            const float* base = s_c + kPart * 2 * ns + ((vc + j) / kCh * W * kPart + row) * kCh + (vc + j) % kCh;
+            v = base[0];
+#pragma unroll
+            for (int w = 1; w < W; ++w) v += base[w * kPart * kCh];
+          }
+          const float dskip = a.D && j < vn ? a.D[q.ch0 + vc + j] : 0.f;
+          v = fmaf(dskip, x[j], v);
           y[j] = zp ? v * silu_f(z[j]) : v;
         }
-        store_vec<T>(op + (tb + row) * a.out.st, vn, a.wide, y);
+        store_vec<T>(static_cast<T*>(a.out.p) + q.b * a.out.sb + q.h * a.out.sh + q.c0 + vc + (int64_t)(tb + row) * a.out.st,
+                     vn, a.wide, y);
       }
       __syncthreads();
     }
   }
   if (kPre) {
-    float4* o = reinterpret_cast<float4*>(states + piece * kPiece);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      float4 v;
-      un2(hs[k][0], v.x, v.y);
-      un2(hs[k][1], v.z, v.w);
-      o[k * 32 + lane] = v;
-    }
-    if (wb == 0 && sg == 0)
-      *reinterpret_cast<float4*>(sums + ((int64_t)chunk * tiles + tile) * kCh + cg * 4) =
-          make_float4(sum[0], sum[1], sum[2], sum[3]);
-    if (tile == 0 && tid == 0) cuts[chunk] = cut;
+    store4(states + piece * kPiece, q.lane, hs);
+    if (q.wn == 0 && q.sg == 0)
+      *reinterpret_cast<f2*>(sums + ((int64_t)chunk * p.blocks + blockIdx.x) * cw + lane_c) = sum;
+    if (blockIdx.x == 0 && q.tid == 0) cuts[chunk] = cut;
   }
 }
 
 // states[c] (a chunk's end from zero) -> the state before chunk c: an element
-// a thread, over the chunks in order.
-__global__ void join_kernel(ScanArgs a, int chunks, int64_t tiles, int nw, float* states,
-                            const float* sums, const int* cuts) {
+// a thread, over the chunks in order, eight loads ahead.
+constexpr int kAhead = 8;
+__global__ void join_kernel(ScanArgs a, Plan p, float* states, const float* __restrict__ sums,
+                            const int* __restrict__ cuts) {
   const int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  const int64_t per = tiles * nw * kPiece;
+  const int64_t per = p.blocks * p.wpb() * kPiece, row = p.blocks * p.cw();
   if (e >= per) return;
-  const int in = (int)(e % kPiece), k = in / 128, lane = in % 128 / 4, c = (lane >> 2) * 4 + in % 4;
-  const int64_t w = e / kPiece, tile = w / nw;
-  const int n = (int)(w % nw) * kNB + (lane & 3) * 4 + k;
-  const int cts = (a.d + kCh - 1) / kCh;
-  const int ch = (int)(tile % cts) * kCh + c, h = (int)(tile / cts % a.H);
-  const bool in_range = n < a.N && ch < a.d;
-  const float A2 = in_range ? a.A[((int64_t)h * a.d + ch) * a.N + n] * kLog2e : 0.f;
+  const PieceAt at = piece_at(e, p);
+  const int c = (int)(at.blk % p.per_head) * p.cw() + at.cb, h = (int)(at.blk / p.per_head % a.H);
+  const float A2 = at.n < a.N && c < a.d ? a.A[((int64_t)h * a.d + c) * a.N + at.n] * kLog2e : 0.f;
+  const float* sum = sums + at.blk * p.cw() + at.cb;
   float carry = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < chunks; ++i) {
-    float* p = states + i * per + e;
-    const float local = i + 1 < chunks ? *p : 0.f;
-    const float dec = i + 1 < chunks ? ex2(A2 * sums[(i * tiles + tile) * kCh + c]) : 0.f;
-    *p = carry;
-    carry = (i + 1 < chunks && cuts[i]) ? local : fmaf(dec, carry, local);
+  for (int i0 = 0; i0 < p.chunks; i0 += kAhead) {
+    float local[kAhead], dec[kAhead];
+    bool cut[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const bool in = i0 + j + 1 < p.chunks;  // the last chunk passes nothing on
+      local[j] = in ? states[(i0 + j) * per + e] : 0.f;
+      dec[j] = in ? ex2(A2 * sum[(i0 + j) * row]) : 0.f;
+      cut[j] = in && cuts[i0 + j];
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (i0 + j >= p.chunks) break;
+      states[(i0 + j) * per + e] = carry;
+      carry = cut[j] ? local[j] : fmaf(dec[j], carry, local[j]);
+    }
   }
-}
-
-size_t smem_bytes(int nw, bool pre) {
-  return (size_t)(2 * kTile * kCh + nw * 2 * kTile * 2 * kNB + (nw > 1 && !pre ? nw * kTile * kCh : 0)) *
-         sizeof(float);
 }
 
 template <typename T>
@@ -326,19 +265,20 @@ cudaError_t fwd(const ScanArgs& a, cudaStream_t s) {
   cudaError_t e = copy_empty_states(a.seqs, a.T, (int64_t)a.H * a.d * a.N, a.h0, a.h_final, a.status, s);
   if (e != cudaSuccess || a.T == 0) return e;
   float* states = a.ws;
-  float* sums = states + (int64_t)p.chunks * p.tiles * p.warps * kPiece;
-  int* cuts = reinterpret_cast<int*>(sums + (int64_t)p.chunks * p.tiles * kCh);
-  if (p.chunks > 1) {
-    scan_kernel<T, true><<<dim3((unsigned)p.tiles, p.chunks - 1), 32 * p.warps, smem_bytes(p.warps, true), s>>>(
-        a, p.len, p.tiles, states, sums, cuts);
-    const int64_t n = p.tiles * p.warps * kPiece;
-    join_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(a, p.chunks, p.tiles, p.warps, states, sums, cuts);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  }
-  const size_t sh = smem_bytes(p.warps, false);
-  scan_kernel<T, false><<<dim3((unsigned)p.tiles, p.chunks), 32 * p.warps, sh, s>>>(a, p.len, p.tiles, states,
-                                                                                   sums, cuts);
-  return cudaGetLastError();
+  float* sums = states + (int64_t)p.chunks * p.blocks * p.wpb() * kPiece;
+  int* cuts = reinterpret_cast<int*>(sums + (int64_t)p.chunks * p.blocks * p.cw());
+  const int threads = 32 * p.wpb();
+  return for_warps(p.warps, [&](auto w) {
+    constexpr int W = decltype(w)::value;
+    const dim3 first((unsigned)p.blocks, p.chunks - 1), all((unsigned)p.blocks, p.chunks);
+    if (p.chunks > 1) {
+      scan_kernel<T, W, true><<<first, threads, smem_bytes(p, true), s>>>(a, p, states, sums, cuts);
+      const int64_t n = p.blocks * p.wpb() * kPiece;
+      join_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(a, p, states, sums, cuts);
+    }
+    scan_kernel<T, W, false><<<all, threads, smem_bytes(p, false), s>>>(a, p, states, sums, cuts);
+    return cudaGetLastError();
+  });
 }
 
 __global__ void copy_empty_kernel(Seqs q, int T, int64_t n, const float* src, float* dst, int* status) {
@@ -434,7 +374,7 @@ cudaError_t copy_empty_states(const Seqs& q, int T, int64_t n, const float* src,
 size_t selective_scan_workspace(const ScanArgs& a) {
   const scan::Plan p = scan::plan(a);
   if (p.chunks <= 1) return 0;
-  return (size_t)p.chunks * (p.tiles * (p.warps * scan::kPiece + scan::kCh) + 1) * sizeof(float);
+  return (size_t)p.chunks * (p.blocks * (p.wpb() * scan::kPiece + p.cw()) + 1) * sizeof(float);
 }
 cudaError_t launch_selective_scan_fwd(const ScanArgs& a, bool bf16, cudaStream_t s) {
   return bf16 ? scan::fwd<__nv_bfloat16>(a, s) : scan::fwd<float>(a, s);

@@ -27,24 +27,14 @@ namespace ttt {
 namespace scan {
 namespace {
 
-constexpr int kCh = 16;     // channels a warp
-constexpr int kPart = 32;   // tokens staged at once: one 32-bit mask
 constexpr int kBlk = 4;     // tokens held in registers
-constexpr int kPiece = kNB * kCh;  // a warp's states: two float4 a lane
-// (float4 q of a lane: states 4*(lane&3) + 2q, +1, each with its two channels)
 
-struct Plan {
-  int warps, tpb;         // 16-state warps a channel tile, channel tiles a block
-  int64_t blocks;         // channel blocks of the call (batch rows, heads)
-  int per_head;           // of them, in a head
+struct Plan : Grid {
   int parts, chunk, chunks;  // parts in all, parts a chunk, chunks
 };
 Plan plan(const ScanArgs& a) {
   Plan p;
-  p.warps = (a.N + kNB - 1) / kNB;
-  p.tpb = p.warps >= 3 ? 1 : 4 / p.warps;
-  p.per_head = (a.d + p.tpb * kCh - 1) / (p.tpb * kCh);
-  p.blocks = (int64_t)a.B * a.H * p.per_head;
+  static_cast<Grid&>(p) = grid_of(a);
   p.parts = (a.T + kPart - 1) / kPart;
   // eight rounds of three blocks an SM; a chunk of one part costs the most
   // join traffic, a long one leaves SMs idle at the end
@@ -84,61 +74,19 @@ Ws carve(const ScanArgs& a, const Plan& p, float* base) {
   return w;
 }
 
-// Which sequence events fall on a part's tokens.
-struct Marks {
-  uint32_t live, begin, end;
-};
-
-// What a block's threads know of their place.
-struct Place {
-  int tid, lane, warp, wt, wn;  // wt: the warp's channel tile in the block, wn: its 16 states
-  int sg, cg;
-  int h, b, c0, g;              // first channel of the block
-  int64_t ch0;                  // h * d + c0
-};
-
-template <typename T>
+template <typename T, int W>
 struct Kernel {
-  static constexpr int V = Vec<T>::n;
-
-  static __device__ __forceinline__ Place place(const ScanArgs& a, int warps, int tpb, int per_head) {
-    Place q;
-    q.tid = threadIdx.x;
-    q.lane = q.tid & 31;
-    q.warp = q.tid >> 5;
-    q.wt = q.warp / warps;
-    q.wn = q.warp % warps;
-    q.sg = q.lane & 3;
-    q.cg = q.lane >> 2;
-    const int64_t blk = blockIdx.x;
-    q.c0 = (int)(blk % per_head) * tpb * kCh;
-    q.h = (int)(blk / per_head % a.H);
-    q.b = (int)(blk / per_head / a.H);
-    q.g = q.h / (a.H / a.G);
-    q.ch0 = (int64_t)q.h * a.d + q.c0;
-    return q;
-  }
-
-  // Marks of the part at tb; s_seq gets its tokens' sequences.
-  static __device__ __forceinline__ Marks marks(const ScanArgs& a, const Place& q, int tb, int nt, int* s_seq) {
-    Marks m;
-    const TokenAt at = token_at(a.seqs, q.b, a.T, tb + q.lane, a.status);
-    const bool in = q.lane < nt && at.live;
-    m.live = __ballot_sync(0xffffffffu, in);
-    m.begin = __ballot_sync(0xffffffffu, in && tb + q.lane == at.lo);
-    m.end = __ballot_sync(0xffffffffu, in && tb + q.lane == at.hi - 1);
-    if (q.warp == 0) s_seq[q.lane] = at.seq;
-    return m;
-  }
+  static constexpr int V = Vec<T>::n, tpb = tiles_per_block(W), nw = W * tpb;
+  static constexpr int cw = tpb * kCh, states = W * kNB;
 
   // Stages a part: D_t, D_t x_t and e_t (the gradient of y_t) of the block's
   // channels [token][channel], B and C of its states [token][state], each
   // value twice. Dead tokens and channels are zeros.
-  static __device__ __forceinline__ void stage(const ScanArgs& a, const TokView& dy, const Place& q, int cw,
-                                               int states, int tb, uint32_t live, float* s_dt, float* s_u,
+  static __device__ __forceinline__ void stage(const ScanArgs& a, const TokView& dy, const Place& q, int tb, uint32_t live, float* s_dt, float* s_u,
                                                float* s_e, float* s_b, float* s_c) {
-    const int lpr = cw / V;
-    for (int i = q.tid; i < kPart * lpr; i += blockDim.x) {
+    constexpr int lpr = cw / V;
+#pragma unroll
+    for (int i = q.tid; i < kPart * lpr; i += 32 * nw) {
       const int row = i / lpr, vc = i % lpr * V;
       const int n = live >> row & 1 ? a.d - q.c0 - vc : 0;
       const int64_t t = tb + row;
@@ -171,8 +119,8 @@ struct Kernel {
         *reinterpret_cast<float4*>(s_e + o) = make_float4(e[j], e[j + 1], e[j + 2], e[j + 3]);
       }
     }
-    const int spr = states / V;
-    for (int i = q.tid; i < kPart * spr * 2; i += blockDim.x) {
+    constexpr int spr = states / V;
+    for (int i = q.tid; i < kPart * spr * 2; i += 32 * nw) {
       const int m = i / (kPart * spr), row = i / spr % kPart, n0 = i % spr * V;
       const int n = live >> row & 1 ? a.N - n0 : 0;
       const TokView& w = m ? a.Cm : a.Bm;
@@ -185,90 +133,28 @@ struct Kernel {
         *reinterpret_cast<float4*>(s + 2 * j) = make_float4(f[j], f[j], f[j + 1], f[j + 1]);
     }
   }
-
-  // The lane's decay rates in powers of two.
-  static __device__ __forceinline__ void rates(const ScanArgs& a, const Place& q, f2 (&A2)[4]) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int n = q.wn * kNB + q.sg * 4 + k, c = q.wt * kCh + q.cg * 2;
-      float r[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        r[i] = n < a.N && q.c0 + c + i < a.d ? a.A[(q.ch0 + c + i) * a.N + n] * kLog2e : 0.f;
-      A2[k] = mk2(r[0], r[1]);
-    }
-  }
-
-  // The lane's elements of a [S,H,d,N] tensor's row `seq` (zeros for null).
-  static __device__ __forceinline__ void seq_state(const ScanArgs& a, const Place& q, const float* p, int seq,
-                                                   f2 (&s)[4]) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int n = q.wn * kNB + q.sg * 4 + k, c = q.wt * kCh + q.cg * 2;
-      float r[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        r[i] = p && n < a.N && q.c0 + c + i < a.d ? p[((int64_t)seq * a.H * a.d + q.ch0 + c + i) * a.N + n] : 0.f;
-      s[k] = mk2(r[0], r[1]);
-    }
-  }
-  static __device__ __forceinline__ void put_state(const ScanArgs& a, const Place& q, float* p, int seq,
-                                                   const f2 (&s)[4]) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int n = q.wn * kNB + q.sg * 4 + k, c = q.wt * kCh + q.cg * 2;
-      float r[2];
-      un2(s[k], r[0], r[1]);
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (n < a.N && q.c0 + c + i < a.d) p[((int64_t)seq * a.H * a.d + q.ch0 + c + i) * a.N + n] = r[i];
-    }
-  }
-  static __device__ __forceinline__ void load4(const float* p, int lane, f2 (&s)[4]) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const ulonglong2 v = reinterpret_cast<const ulonglong2*>(p)[i * 32 + lane];
-      s[2 * i] = v.x;
-      s[2 * i + 1] = v.y;
-    }
-  }
-  static __device__ __forceinline__ void store4(float* p, int lane, const f2 (&s)[4]) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      reinterpret_cast<ulonglong2*>(p)[i * 32 + lane] = make_ulonglong2(s[2 * i], s[2 * i + 1]);
-  }
-  // Four states' values (each twice) of a token.
-  static __device__ __forceinline__ void four(const float* s, f2 (&v)[4]) {
-    const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(s), b = *reinterpret_cast<const ulonglong2*>(s + 4);
-    v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
-  }
 };
 
 struct Shared {
-  int cw, states;        // channels and states of the block
   float *dt, *u, *e, *b, *c;  // [32][cw], [32][2 * states]
-  float *y, *r;          // a warp's: [32][16]; r takes the place of u where a tile has one warp
-  int ystride;           // tokens of y and r are this far apart
+  float *y, *r;          // a warp's: [32][ystride]; r takes the place of u where a tile has one warp
   float* keep;           // a warp's kept states: [8][kPiece], later its dB, dC [32][32]
 };
-__device__ __forceinline__ Shared shared_of(float* sm, const Place& q, int warps, int tpb) {
+template <int W>
+__device__ __forceinline__ Shared shared_of(float* sm, const Place& q) {
+  constexpr int tpb = tiles_per_block(W), cw = tpb * kCh, states = W * kNB, nw = W * tpb;
   Shared s;
-  s.cw = tpb * kCh;
-  s.states = warps * kNB;
   s.dt = sm;
-  s.u = s.dt + kPart * s.cw;
-  s.e = s.u + kPart * s.cw;
-  s.b = s.e + kPart * s.cw;
-  s.c = s.b + kPart * 2 * s.states;
-  float* next = s.c + kPart * 2 * s.states;
-  const int nw = warps * tpb;
-  if (warps == 1) {
-    s.ystride = s.cw;
+  s.u = s.dt + kPart * cw;
+  s.e = s.u + kPart * cw;
+  s.b = s.e + kPart * cw;
+  s.c = s.b + kPart * 2 * states;
+  float* next = s.c + kPart * 2 * states;
+  if (W == 1) {
     s.y = next + q.wt * kCh;
     s.r = s.u + q.wt * kCh;
-    next += kPart * s.cw;
+    next += kPart * cw;
   } else {
-    s.ystride = kCh;
     s.y = next + q.warp * kPart * kCh;
     s.r = s.y + nw * kPart * kCh;
     next += 2 * nw * kPart * kCh;
@@ -286,17 +172,18 @@ size_t smem_bytes(const Plan& p, bool pre) {
 // First pass over a chunk: start states of its parts from a zero start, sums
 // of D_t before each part and over the chunk, the chunk's end state (to hin of
 // the chunk itself, joined later), and the gradient it sends back (to gin).
-template <typename T>
+template <typename T, int W>
 __global__ void __launch_bounds__(128) pre_kernel(ScanBwdArgs ga, Plan p, Ws ws) {
-  using K = Kernel<T>;
+  using K = Kernel<T, W>;
   extern __shared__ __align__(16) float sm[];
   __shared__ int s_seq[kPart];
   const ScanArgs& a = ga.f;
-  const Place q = K::place(a, p.warps, p.tpb, p.per_head);
-  const Shared s = shared_of(sm, q, p.warps, p.tpb);
-  const int nw = p.tpb * p.warps, chunk = blockIdx.y;
+  const Place q = place<W>(a, p.per_head);
+  const Shared s = shared_of<W>(sm, q);
+  constexpr int nw = K::nw;
+  const int chunk = blockIdx.y;
   f2 A2[4], hs[4] = {0, 0, 0, 0}, gs[4] = {0, 0, 0, 0}, P[4];
-  K::rates(a, q, A2);
+  rates(a, q, A2);
   const f2 one = mk2(1.f, 1.f);
 #pragma unroll
   for (int k = 0; k < 4; ++k) P[k] = one;
@@ -306,23 +193,25 @@ __global__ void __launch_bounds__(128) pre_kernel(ScanBwdArgs ga, Plan p, Ws ws)
   for (int part = chunk * p.chunk; part < part1; ++part) {
     const int64_t at = (int64_t)part * p.blocks + blockIdx.x;
     if (part > chunk * p.chunk) {
-      K::store4(ws.start + (at * nw + q.warp) * kPiece, q.lane, hs);
+      store4(ws.start + (at * nw + q.warp) * kPiece, q.lane, hs);
       if (q.wn == 0 && q.sg == 0)
-        *reinterpret_cast<f2*>(ws.sums + at * s.cw + q.wt * kCh + q.cg * 2) = sum;
+        *reinterpret_cast<f2*>(ws.sums + at * K::cw + q.wt * kCh + q.cg * 2) = sum;
     }
     const int tb = part * kPart, nt = min(kPart, a.T - tb);
-    const Marks m = K::marks(a, q, tb, nt, s_seq);
-    K::stage(a, ga.dy, q, s.cw, s.states, tb, m.live, s.dt, s.u, s.e, s.b, s.c);
+    int seq;
+    const Marks m = marks(a, q, tb, nt, &seq);
+    if (q.warp == 0) s_seq[q.lane] = seq;
+    K::stage(a, ga.dy, q, tb, m.live, s.dt, s.u, s.e, s.b, s.c);
     __syncthreads();
     for (int t = 0; t < nt; ++t) {
       if (m.begin >> t & 1) {
-        K::seq_state(a, q, a.h0, s_seq[t], hs);
+        seq_state(a, q, a.h0, s_seq[t], hs);
         if (tb + t != chunk * p.chunk * kPart) open = false;
       }
-      const int o = t * s.cw + q.wt * kCh + q.cg * 2;
+      const int o = t * K::cw + q.wt * kCh + q.cg * 2;
       const f2 dt = *reinterpret_cast<const f2*>(s.dt + o), u = *reinterpret_cast<const f2*>(s.u + o);
       f2 bb[4], cc[4], dec[4];
-      K::four(s.b + t * 2 * s.states + q.wn * 2 * kNB + q.sg * 8, bb);
+      four(s.b + t * 2 * K::states + q.wn * 2 * kNB + q.sg * 8, bb);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         dec[k] = ex2_pair(mul2(dt, A2[k]));
@@ -331,7 +220,7 @@ __global__ void __launch_bounds__(128) pre_kernel(ScanBwdArgs ga, Plan p, Ws ws)
       sum = add2(sum, dt);
       if (open) {
         const f2 e = *reinterpret_cast<const f2*>(s.e + o);
-        K::four(s.c + t * 2 * s.states + q.wn * 2 * kNB + q.sg * 8, cc);
+        four(s.c + t * 2 * K::states + q.wn * 2 * kNB + q.sg * 8, cc);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           P[k] = mul2(P[k], dec[k]);
@@ -340,7 +229,7 @@ __global__ void __launch_bounds__(128) pre_kernel(ScanBwdArgs ga, Plan p, Ws ws)
         if (m.end >> t & 1) {
           open = false;
           f2 df[4];
-          K::seq_state(a, q, ga.dh_final, s_seq[t], df);
+          seq_state(a, q, ga.dh_final, s_seq[t], df);
 #pragma unroll
           for (int k = 0; k < 4; ++k) gs[k] = fma2(P[k], df[k], gs[k]);
         }
@@ -349,71 +238,78 @@ __global__ void __launch_bounds__(128) pre_kernel(ScanBwdArgs ga, Plan p, Ws ws)
     __syncthreads();
   }
   const int64_t at = (int64_t)chunk * p.blocks + blockIdx.x;
-  K::store4(ws.hin + (at * nw + q.warp) * kPiece, q.lane, hs);
-  K::store4(ws.gin + (at * nw + q.warp) * kPiece, q.lane, gs);
-  if (q.wn == 0 && q.sg == 0) *reinterpret_cast<f2*>(ws.total + at * s.cw + q.wt * kCh + q.cg * 2) = sum;
+  store4(ws.hin + (at * nw + q.warp) * kPiece, q.lane, hs);
+  store4(ws.gin + (at * nw + q.warp) * kPiece, q.lane, gs);
+  if (q.wn == 0 && q.sg == 0) *reinterpret_cast<f2*>(ws.total + at * K::cw + q.wt * kCh + q.cg * 2) = sum;
 }
+
+constexpr int kAhead = 8;  // chunks read before their use
 
 // Joins the chunks: hin becomes the state before each chunk, gin the gradient
 // that reaches the state behind it. An element a thread. A chunk in which a
-// sequence begins (or ends) passes nothing through.
+// sequence begins (or ends) passes nothing through, and nothing crosses a
+// border at which one begins.
 __global__ void join_kernel(ScanArgs a, Plan p, Ws ws) {
-  const int nw = p.tpb * p.warps;
-  const int64_t per = p.blocks * nw * kPiece, e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  const int64_t per = p.blocks * p.wpb() * kPiece, e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (e >= per) return;
-  const int in = (int)(e % kPiece), lane = in % 128 / 4;
-  const int warp = (int)(e / kPiece % nw);
-  const int64_t blk = e / kPiece / nw;
-  const int n = warp % p.warps * kNB + (lane & 3) * 4 + in / 128 * 2 + in % 4 / 2;
-  const int cb = warp / p.warps * kCh + (lane >> 2) * 2 + in % 2;  // channel in the block
-  const int c = (int)(blk % p.per_head) * p.tpb * kCh + cb, h = (int)(blk / p.per_head % a.H);
+  const PieceAt at = piece_at(e, p);
+  const int n = at.n, cb = at.cb;
+  const int64_t blk = at.blk;
+  const int c = (int)(blk % p.per_head) * p.cw() + cb, h = (int)(blk / p.per_head % a.H);
   const int b = (int)(blk / p.per_head / a.H);
   const float A2 = n < a.N && c < a.d ? a.A[((int64_t)h * a.d + c) * a.N + n] * kLog2e : 0.f;
-  const int span = p.chunk * kPart, cw = p.tpb * kCh;
-  const float* total = ws.total + blk * cw + cb;
-  float carry = 0.f;
-  for (int i = 0; i < p.chunks; ++i) {
-    float* x = ws.hin + i * per + e;
-    const float local = *x, dec = ex2(A2 * total[i * p.blocks * cw]);
-    *x = carry;
-    bool through = i > 0;
-    if (a.seqs.cu && i + 1 < p.chunks) {
-      const TokenAt at = token_at(a.seqs, b, a.T, (i + 1) * span, a.status);
-      through = at.live && at.lo < i * span;
+  const int span = p.chunk * kPart;
+  const int64_t row = p.blocks * p.cw();
+  const float* total = ws.total + blk * p.cw() + cb;
+  for (int way = 0; way < 2; ++way) {  // forward: states, backward: gradients
+    float* x = (way ? ws.gin : ws.hin) + e;
+    float carry = 0.f;
+    for (int i0 = 0; i0 < p.chunks; i0 += kAhead) {
+      float local[kAhead], dec[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int64_t i = way ? p.chunks - 1 - (i0 + j) : i0 + j;
+        const bool in = i0 + j < p.chunks;
+        local[j] = in ? x[i * per] : 0.f;
+        dec[j] = in ? ex2(A2 * total[i * row]) : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (i0 + j >= p.chunks) break;
+        const int i = way ? p.chunks - 1 - (i0 + j) : i0 + j;
+        x[i * per] = carry;
+        bool through = way ? i + 1 < p.chunks : i > 0, on = true;
+        if (a.seqs.cu) {
+          // the token behind the border that the carry crosses, and its sequence
+          const int border = way ? i * span : (i + 1) * span;
+          const TokenAt at = token_at(a.seqs, b, a.T, border, a.status);
+          on = at.live && at.lo < border;
+          through = on && (way ? at.hi > (i + 1) * span : at.lo < i * span);
+        }
+        carry = !on ? 0.f : through ? fmaf(dec[j], carry, local[j]) : local[j];
+      }
     }
-    carry = through ? fmaf(dec, carry, local) : local;
-  }
-  carry = 0.f;
-  for (int i = p.chunks - 1; i >= 0; --i) {
-    float* x = ws.gin + i * per + e;
-    const float local = *x, dec = ex2(A2 * total[i * p.blocks * cw]);
-    *x = carry;
-    bool through = i + 1 < p.chunks;
-    if (a.seqs.cu && through) {
-      const TokenAt at = token_at(a.seqs, b, a.T, i * span, a.status);
-      through = at.live && at.hi > (i + 1) * span;
-    }
-    carry = through ? fmaf(dec, carry, local) : local;
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(128) main_kernel(ScanBwdArgs ga, Plan p, Ws ws) {
-  using K = Kernel<T>;
-  constexpr int V = K::V;
+template <typename T, int W>
+__global__ void __launch_bounds__(128, 3) main_kernel(ScanBwdArgs ga, Plan p, Ws ws) {
+  using K = Kernel<T, W>;
+  constexpr int V = K::V, lpr = K::cw / V;
   extern __shared__ __align__(16) float sm[];
   __shared__ int s_seq[kPart];
   const ScanArgs& a = ga.f;
-  const Place q = K::place(a, p.warps, p.tpb, p.per_head);
-  const Shared s = shared_of(sm, q, p.warps, p.tpb);
-  const int nw = p.tpb * p.warps, chunk = blockIdx.y;
+  const Place q = place<W>(a, p.per_head);
+  const Shared s = shared_of<W>(sm, q);
+  constexpr int nw = K::nw;
+  const int chunk = blockIdx.y;
   const int64_t chat = (int64_t)chunk * p.blocks + blockIdx.x;
   f2 A2[4], h_in[4], gs[4], dA[4] = {0, 0, 0, 0};
-  K::rates(a, q, A2);
-  K::load4(ws.hin + (chat * nw + q.warp) * kPiece, q.lane, h_in);
-  K::load4(ws.gin + (chat * nw + q.warp) * kPiece, q.lane, gs);
+  rates(a, q, A2);
+  load4(ws.hin + (chat * nw + q.warp) * kPiece, q.lane, h_in);
+  load4(ws.gin + (chat * nw + q.warp) * kPiece, q.lane, gs);
   // channel sums of the thread's vectors: their channels are the same in every turn
-  const int lpr = s.cw / V;
+  constexpr int ystride = W == 1 ? K::cw : kCh;
   const int vc = q.tid % lpr * V, vn = a.d - q.c0 - vc;
   float sD[V], sbias[V];
 #pragma unroll
@@ -423,8 +319,10 @@ __global__ void __launch_bounds__(128) main_kernel(ScanBwdArgs ga, Plan p, Ws ws
   const int part0 = chunk * p.chunk, part1 = min(p.parts, part0 + p.chunk);
   for (int part = part1 - 1; part >= part0; --part) {
     const int tb = part * kPart, nt = min(kPart, a.T - tb);
-    const Marks m = K::marks(a, q, tb, nt, s_seq);
-    K::stage(a, ga.dy, q, s.cw, s.states, tb, m.live, s.dt, s.u, s.e, s.b, s.c);
+    int seq;
+    const Marks m = marks(a, q, tb, nt, &seq);
+    if (q.warp == 0) s_seq[q.lane] = seq;
+    K::stage(a, ga.dy, q, tb, m.live, s.dt, s.u, s.e, s.b, s.c);
     // the state before the part
     f2 hs[4];
     if (part == part0) {
@@ -432,10 +330,10 @@ __global__ void __launch_bounds__(128) main_kernel(ScanBwdArgs ga, Plan p, Ws ws
       for (int k = 0; k < 4; ++k) hs[k] = h_in[k];
     } else {
       const int64_t at = (int64_t)part * p.blocks + blockIdx.x;
-      K::load4(ws.start + (at * nw + q.warp) * kPiece, q.lane, hs);
+      load4(ws.start + (at * nw + q.warp) * kPiece, q.lane, hs);
       const TokenAt here = token_at(a.seqs, q.b, a.T, tb, a.status);
       if (here.live && here.lo < part0 * kPart) {  // its sequence entered the chunk from before
-        const f2 sum = *reinterpret_cast<const f2*>(ws.sums + at * s.cw + q.wt * kCh + q.cg * 2);
+        const f2 sum = *reinterpret_cast<const f2*>(ws.sums + at * K::cw + q.wt * kCh + q.cg * 2);
 #pragma unroll
         for (int k = 0; k < 4; ++k) hs[k] = fma2(ex2_pair(mul2(sum, A2[k])), h_in[k], hs[k]);
       }
@@ -444,16 +342,16 @@ __global__ void __launch_bounds__(128) main_kernel(ScanBwdArgs ga, Plan p, Ws ws
     const int lane_o = q.wt * kCh + q.cg * 2, lane_s = q.wn * 2 * kNB + q.sg * 8;
     // forward, keeping the state before every block
     for (int t = 0; t < nt; ++t) {
-      if (t % kBlk == 0) K::store4(s.keep + t / kBlk * kPiece, q.lane, hs);
-      if (m.begin >> t & 1) K::seq_state(a, q, a.h0, s_seq[t], hs);
-      const f2 dt = *reinterpret_cast<const f2*>(s.dt + t * s.cw + lane_o);
-      const f2 u = *reinterpret_cast<const f2*>(s.u + t * s.cw + lane_o);
+      if (t % kBlk == 0) store4(s.keep + t / kBlk * kPiece, q.lane, hs);
+      if (m.begin >> t & 1) seq_state(a, q, a.h0, s_seq[t], hs);
+      const f2 dt = *reinterpret_cast<const f2*>(s.dt + t * K::cw + lane_o);
+      const f2 u = *reinterpret_cast<const f2*>(s.u + t * K::cw + lane_o);
       f2 bb[4], cc[4], y = 0;
-      K::four(s.b + t * 2 * s.states + lane_s, bb);
+      four(s.b + t * 2 * K::states + lane_s, bb);
 #pragma unroll
       for (int k = 0; k < 4; ++k) hs[k] = fma2(ex2_pair(mul2(dt, A2[k])), hs[k], mul2(u, bb[k]));
       if (a.z.p) {
-        K::four(s.c + t * 2 * s.states + lane_s, cc);
+        four(s.c + t * 2 * K::states + lane_s, cc);
 #pragma unroll
         for (int k = 0; k < 4; ++k) y = fma2(hs[k], cc[k], y);
         float y0, y1;
@@ -462,16 +360,17 @@ __global__ void __launch_bounds__(128) main_kernel(ScanBwdArgs ga, Plan p, Ws ws
         const float o = __shfl_xor_sync(0xffffffffu, up ? y0 : y1, 1);
         float v = (up ? y1 : y0) + o;
         v += __shfl_xor_sync(0xffffffffu, v, 2);
-        if (q.sg < 2) s.y[t * s.ystride + q.cg * 2 + up] = v;
+        if (q.sg < 2) s.y[t * ystride + q.cg * 2 + up] = v;
       }
     }
-    const float* ysm = s.y - (p.warps == 1 ? q.wt * kCh : q.warp * kPart * kCh);
-    const float* rsm = s.r - (p.warps == 1 ? q.wt * kCh : q.warp * kPart * kCh);
+    const float* ysm = s.y - (W == 1 ? q.wt * kCh : q.warp * kPart * kCh);
+    const float* rsm = s.r - (W == 1 ? q.wt * kCh : q.warp * kPart * kCh);
     // the sum over a tile's warps of y or r, at a token and channel of the block
     auto joined = [&](const float* base, int row, int c) {
-      if (p.warps == 1) return base[row * s.cw + c];
+      if (W == 1) return base[row * K::cw + c];
       float v = 0.f;
-      for (int w = 0; w < p.warps; ++w) v += base[((c / kCh * p.warps + w) * kPart + row) * kCh + c % kCh];
+#pragma unroll
+      for (int w = 0; w < W; ++w) v += base[((c / kCh * W + w) * kPart + row) * kCh + c % kCh];
       return v;
     };
     if (a.z.p) {  // dz = dy y silu'(z)
@@ -497,16 +396,16 @@ __global__ void __launch_bounds__(128) main_kernel(ScanBwdArgs ga, Plan p, Ws ws
     for (int blk = (nt - 1) / kBlk; blk >= 0; --blk) {
       f2 dec[kBlk][4], st[kBlk][4];  // the decays, and the decayed states exp(D A) h_{t-1}
       f2 h[4];
-      K::load4(s.keep + blk * kPiece, q.lane, h);
+      load4(s.keep + blk * kPiece, q.lane, h);
 #pragma unroll
       for (int i = 0; i < kBlk; ++i) {
         const int t = blk * kBlk + i;
         if (t < nt) {
-          if (m.begin >> t & 1) K::seq_state(a, q, a.h0, s_seq[t], h);
-          const f2 dt = *reinterpret_cast<const f2*>(s.dt + t * s.cw + lane_o);
-          const f2 u = *reinterpret_cast<const f2*>(s.u + t * s.cw + lane_o);
+          if (m.begin >> t & 1) seq_state(a, q, a.h0, s_seq[t], h);
+          const f2 dt = *reinterpret_cast<const f2*>(s.dt + t * K::cw + lane_o);
+          const f2 u = *reinterpret_cast<const f2*>(s.u + t * K::cw + lane_o);
           f2 bb[4];
-          K::four(s.b + t * 2 * s.states + lane_s, bb);
+          four(s.b + t * 2 * K::states + lane_s, bb);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             dec[i][k] = ex2_pair(mul2(dt, A2[k]));
@@ -520,13 +419,13 @@ __global__ void __launch_bounds__(128) main_kernel(ScanBwdArgs ga, Plan p, Ws ws
       for (int i = kBlk - 1; i >= 0; --i) {
         const int t = blk * kBlk + i;
         if (t < nt) {
-          if (m.end >> t & 1) K::seq_state(a, q, ga.dh_final, s_seq[t], gs);
-          const f2 dt = *reinterpret_cast<const f2*>(s.dt + t * s.cw + lane_o);
-          const f2 u = *reinterpret_cast<const f2*>(s.u + t * s.cw + lane_o);
-          const f2 e = *reinterpret_cast<const f2*>(s.e + t * s.cw + lane_o);
+          if (m.end >> t & 1) seq_state(a, q, ga.dh_final, s_seq[t], gs);
+          const f2 dt = *reinterpret_cast<const f2*>(s.dt + t * K::cw + lane_o);
+          const f2 u = *reinterpret_cast<const f2*>(s.u + t * K::cw + lane_o);
+          const f2 e = *reinterpret_cast<const f2*>(s.e + t * K::cw + lane_o);
           f2 bb[4], cc[4], sq = 0, sr = 0, dB[4], dC[4];
-          K::four(s.b + t * 2 * s.states + lane_s, bb);
-          K::four(s.c + t * 2 * s.states + lane_s, cc);
+          four(s.b + t * 2 * K::states + lane_s, bb);
+          four(s.c + t * 2 * K::states + lane_s, cc);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const f2 g = fma2(e, cc[k], gs[k]);
@@ -538,7 +437,7 @@ __global__ void __launch_bounds__(128) main_kernel(ScanBwdArgs ga, Plan p, Ws ws
             dA[k] = fma2(gh, dt, dA[k]);
             gs[k] = mul2(dec[i][k], g);
           }
-          if ((m.begin >> t & 1) && ga.dh0) K::put_state(a, q, ga.dh0, s_seq[t], gs);
+          if ((m.begin >> t & 1) && ga.dh0) put_state(a, q, ga.dh0, s_seq[t], gs);
           // <g, B> and <g, A exp(DA) h> of two channels over the tile's four state lanes
           float v[4];
           un2(sq, v[0], v[1]);
@@ -549,7 +448,7 @@ __global__ void __launch_bounds__(128) main_kernel(ScanBwdArgs ga, Plan p, Ws ws
           const float w0 = (up ? v[2] : v[0]) + p0, w1 = (up ? v[3] : v[1]) + p1;
           const float r0 = __shfl_xor_sync(0xffffffffu, up2 ? w0 : w1, 2);
           const float w = (up2 ? w1 : w0) + r0;
-          (up ? s.r : s.y)[t * s.ystride + q.cg * 2 + (up2 ? 1 : 0)] = up ? w * ln2 : w;
+          (up ? s.r : s.y)[t * ystride + q.cg * 2 + (up2 ? 1 : 0)] = up ? w * ln2 : w;
           // dB, dC of four states over the warp's 16 channels: pairs, then 8 lanes
           float f[8];
 #pragma unroll
@@ -587,7 +486,7 @@ __global__ void __launch_bounds__(128) main_kernel(ScanBwdArgs ga, Plan p, Ws ws
       for (int j = 0; j < V; ++j) {
         const float dskip = a.D && j < vn ? a.D[q.ch0 + vc + j] : 0.f;
         const float bias = a.dt_bias && j < vn ? a.dt_bias[q.ch0 + vc + j] : 0.f;
-        const int o = row * s.cw + vc + j;
+        const int o = row * K::cw + vc + j;
         const float gb = joined(ysm, row, vc + j), ga_ = joined(rsm, row, vc + j), e = s.e[o];
         dx[j] = fmaf(dskip, e, s.dt[o] * gb);
         dd[j] = fmaf(x[j], gb, ga_);
@@ -600,26 +499,26 @@ __global__ void __launch_bounds__(128) main_kernel(ScanBwdArgs ga, Plan p, Ws ws
     }
     // dB, dC over the block's channel tiles, to the block's slab
     const float* keep0 = s.keep - q.warp * (kPart / kBlk) * kPiece;
-    for (int i = q.tid; i < nt * 2 * s.states; i += blockDim.x) {
-      const int t = i / (2 * s.states), which = i / s.states % 2, n = i % s.states;
+    for (int i = q.tid; i < nt * 2 * K::states; i += blockDim.x) {
+      const int t = i / (2 * K::states), which = i / K::states % 2, n = i % K::states;
       float v = 0.f;
-      for (int w = 0; w < p.tpb; ++w)
-        v += keep0[((w * p.warps + n / kNB) * (kPart / kBlk) + t / kBlk) * kPiece + t % kBlk * 32 + which * 16 + n % kNB];
-      ws.dBC[(((int64_t)blockIdx.x * a.T + tb + t) * 2 + which) * s.states + n] = v;
+      for (int w = 0; w < K::tpb; ++w)
+        v += keep0[((w * W + n / kNB) * (kPart / kBlk) + t / kBlk) * kPiece + t % kBlk * 32 + which * 16 + n % kNB];
+      ws.dBC[(((int64_t)blockIdx.x * a.T + tb + t) * 2 + which) * K::states + n] = v;
     }
     __syncthreads();
   }
-  K::store4(ws.dA + (chat * nw + q.warp) * kPiece, q.lane, dA);
+  store4(ws.dA + (chat * nw + q.warp) * kPiece, q.lane, dA);
   // the threads' channel sums: rows of threads that share a vector, in order
   for (int w = 0; w < 2; ++w) {
     float* sh = s.dt;  // [threads / lpr][cw]: within the three staged tensors
 #pragma unroll
-    for (int j = 0; j < V; ++j) sh[q.tid / lpr * s.cw + vc + j] = w ? sbias[j] : sD[j];
+    for (int j = 0; j < V; ++j) sh[q.tid / lpr * K::cw + vc + j] = w ? sbias[j] : sD[j];
     __syncthreads();
-    for (int c = q.tid; c < s.cw; c += blockDim.x) {
+    for (int c = q.tid; c < K::cw; c += blockDim.x) {
       float v = 0.f;
-      for (int i = 0; i < (int)blockDim.x / lpr; ++i) v += sh[i * s.cw + c];
-      ws.dD[(chat * 2 + w) * s.cw + c] = v;
+      for (int i = 0; i < (int)blockDim.x / lpr; ++i) v += sh[i * K::cw + c];
+      ws.dD[(chat * 2 + w) * K::cw + c] = v;
     }
     __syncthreads();
   }
@@ -629,14 +528,13 @@ __global__ void __launch_bounds__(128) main_kernel(ScanBwdArgs ga, Plan p, Ws ws
 // element of the block's layout for one (head, channel block).
 struct PutA {
   float* dA;
-  int d, N, per_head, tpb, warps;
+  int d, N;
+  Grid g;
   __device__ void operator()(int64_t col, float v) const {
-    const int nw = tpb * warps, in = (int)(col % kPiece), lane = in % 128 / 4;
-    const int warp = (int)(col / kPiece % nw);
-    const int64_t blk = col / kPiece / nw, h = blk / per_head;
-    const int n = warp % warps * kNB + (lane & 3) * 4 + in / 128 * 2 + in % 4 / 2;
-    const int c = (int)(blk % per_head) * tpb * kCh + warp / warps * kCh + (lane >> 2) * 2 + in % 2;
-    if (n < N && c < d) dA[(h * d + c) * N + n] = v;
+    const PieceAt at = piece_at(col, g);
+    const int64_t h = at.blk / g.per_head;
+    const int c = (int)(at.blk % g.per_head) * g.cw() + at.cb;
+    if (at.n < N && c < d) dA[(h * d + c) * N + at.n] = v;
   }
 };
 struct PutD {
@@ -686,21 +584,26 @@ cudaError_t bwd(const ScanBwdArgs& ga, cudaStream_t s) {
   const int nw = p.tpb * p.warps, cw = p.tpb * kCh;
   const int64_t heads = (int64_t)a.H * p.per_head;  // channel blocks of a batch row
   if (a.T > 0) {
-    const size_t sh = smem_bytes(p, false);
-    e = cudaFuncSetAttribute(main_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sh);
+    e = for_warps(p.warps, [&](auto w) {
+      constexpr int W = decltype(w)::value;
+      const size_t sh = smem_bytes(p, false);
+      const cudaError_t r =
+          cudaFuncSetAttribute(main_kernel<T, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sh);
+      if (r != cudaSuccess) return r;
+      const dim3 grid((unsigned)p.blocks, p.chunks);
+      pre_kernel<T, W><<<grid, 32 * nw, smem_bytes(p, true), s>>>(ga, p, ws);
+      const int64_t n = p.blocks * nw * kPiece;
+      join_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(a, p, ws);
+      main_kernel<T, W><<<grid, 32 * nw, sh, s>>>(ga, p, ws);
+      const int64_t bc = (int64_t)a.B * a.G * a.T * 2 * p.warps * kNB;
+      put_bc_kernel<T><<<(unsigned)((bc + 255) / 256), 256, 0, s>>>(ga, p, ws.dBC);
+      return cudaGetLastError();
+    });
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)p.blocks, p.chunks);
-    pre_kernel<T><<<grid, 32 * nw, smem_bytes(p, true), s>>>(ga, p, ws);
-    const int64_t n = p.blocks * nw * kPiece;
-    join_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(a, p, ws);
-    main_kernel<T><<<grid, 32 * nw, sh, s>>>(ga, p, ws);
-    const int64_t bc = (int64_t)a.B * a.G * a.T * 2 * p.warps * kNB;
-    put_bc_kernel<T><<<(unsigned)((bc + 255) / 256), 256, 0, s>>>(ga, p, ws.dBC);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   // [chunk][batch row][head block]: parts are (chunk, batch row) pairs
   const int64_t parts = (int64_t)p.chunks * a.B;
-  e = sum_parts(ws.dA, parts, heads * nw * kPiece, PutA{ga.dA, a.d, a.N, p.per_head, p.tpb, p.warps}, s);
+  e = sum_parts(ws.dA, parts, heads * nw * kPiece, PutA{ga.dA, a.d, a.N, p}, s);
   if (e != cudaSuccess || (!ga.dD && !ga.ddt_bias)) return e;
   return sum_parts(ws.dD, parts, heads * 2 * cw, PutD{ga.dD, ga.ddt_bias, a.d, p.per_head, cw}, s);
 }
