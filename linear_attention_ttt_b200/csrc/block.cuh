@@ -200,6 +200,65 @@ __device__ __forceinline__ void store_vec(T* p, int n, bool wide, const float (&
   }
 }
 
+// V channels of a token row, in fp32: 16 bytes of bf16 (V = 8) or fp32 (V = 4),
+// or 8 bytes of bf16 (V = 4).
+template <typename T, int V>
+__device__ __forceinline__ void load_row(const T* p, int n, bool wide, float (&f)[V]) {
+  if constexpr (V * sizeof(T) == 16) {
+    unpack<T>(load_vec(p, n, wide), f);
+  } else {
+    if (wide && n >= V) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      f[0] = __uint_as_float(v.x << 16);
+      f[1] = __uint_as_float(v.x & 0xffff0000u);
+      f[2] = __uint_as_float(v.y << 16);
+      f[3] = __uint_as_float(v.y & 0xffff0000u);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) f[i] = i < n ? to_f32(p[i]) : 0.f;
+    }
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_row(T* p, int n, bool wide, const float (&f)[V]) {
+  if constexpr (V * sizeof(T) == 16) {
+    store_vec<T>(p, n, wide, f);
+  } else {
+    if (wide && n >= V) {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
+      *reinterpret_cast<uint2*>(p) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (i < n) p[i] = from_f32<T>(f[i]);
+    }
+  }
+}
+
+// Asynchronous copy of a row piece of 16 bytes into shared memory: the first n
+// elements, zeros behind them (n <= 0: zeros, nothing is read). Rows that are
+// not 16-byte aligned are copied at once, element by element.
+template <typename T>
+__device__ __forceinline__ void copy_async(T* dst, const T* src, int n, bool wide) {
+  constexpr int V = Vec<T>::n;
+  n = n < 0 ? 0 : n > V ? V : n;
+  if (wide) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+                 "r"((int)(n * sizeof(T)))
+                 : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) dst[i] = i < n ? src[i] : from_f32<T>(0.f);
+  }
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the last kLeft groups of this thread's copies have arrived.
+template <int kLeft>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
 // 2^x and 1/x by the special-function unit (2^-22 relative); denormal results
 // are 0, 1/inf is 0, NaN stays NaN.
 __device__ __forceinline__ float ex2(float x) {

@@ -12,42 +12,6 @@ namespace {
 
 constexpr int kThreads = 128;
 
-// V channels of a token row, in fp32: 16 bytes of bf16 (V = 8) or fp32 (V = 4),
-// or 8 bytes of bf16 (V = 4).
-template <typename T, int V>
-__device__ __forceinline__ void load_row(const T* p, int n, bool wide, float (&f)[V]) {
-  if constexpr (V * sizeof(T) == 16) {
-    unpack<T>(load_vec(p, n, wide), f);
-  } else {
-    if (wide && n >= V) {
-      const uint2 v = *reinterpret_cast<const uint2*>(p);
-      f[0] = __uint_as_float(v.x << 16);
-      f[1] = __uint_as_float(v.x & 0xffff0000u);
-      f[2] = __uint_as_float(v.y << 16);
-      f[3] = __uint_as_float(v.y & 0xffff0000u);
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i) f[i] = i < n ? to_f32(p[i]) : 0.f;
-    }
-  }
-}
-template <typename T, int V>
-__device__ __forceinline__ void store_row(T* p, int n, bool wide, const float (&f)[V]) {
-  if constexpr (V * sizeof(T) == 16) {
-    store_vec<T>(p, n, wide, f);
-  } else {
-    if (wide && n >= V) {
-      const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
-      *reinterpret_cast<uint2*>(p) =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (i < n) p[i] = from_f32<T>(f[i]);
-    }
-  }
-}
-
 // Which channels and tokens a thread has.
 struct Run {
   int h, c, n;    // head, first channel, channels that exist (of V)

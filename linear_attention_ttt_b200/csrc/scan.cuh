@@ -119,6 +119,13 @@ __device__ __forceinline__ Place place(const ScanArgs& a, int per_head) {
 // Marks of the nt tokens at tb; *seq gets the lane's token's sequence.
 __device__ __forceinline__ Marks marks(const ScanArgs& a, const Place& q, int tb, int nt, int* seq) {
   Marks m;
+  if (!a.seqs.cu) {
+    m.live = nt < 32 ? (1u << nt) - 1 : 0xffffffffu;
+    m.begin = tb == 0;
+    m.end = tb + nt == a.T ? 1u << (nt - 1) : 0;
+    *seq = q.b;
+    return m;
+  }
   const TokenAt at = token_at(a.seqs, q.b, a.T, tb + q.lane, a.status);
   const bool in = q.lane < nt && at.live;
   m.live = __ballot_sync(0xffffffffu, in);
@@ -126,6 +133,34 @@ __device__ __forceinline__ Marks marks(const ScanArgs& a, const Place& q, int tb
   m.end = __ballot_sync(0xffffffffu, in && tb + q.lane == at.hi - 1);
   *seq = at.seq;
   return m;
+}
+
+// A token tensor's piece of a block (kPart rows of kWidth elements from p, of
+// which `left` exist) on its way into shared memory; dead rows become zeros.
+template <typename T, int kWidth, int kThreads>
+__device__ __forceinline__ void copy_part(T* dst, const T* p, int64_t stride, int left, uint32_t live, int tid,
+                                          bool wide) {
+  constexpr int V = Vec<T>::n, per = kWidth / V;
+#pragma unroll
+  for (int i0 = 0; i0 < kPart * per; i0 += kThreads) {
+    const int i = i0 + tid, row = i / per, c = i % per * V;
+    if (kPart * per % kThreads == 0 || i < kPart * per)
+      copy_async(dst + i * V, p + row * stride + c, live >> row & 1 ? left - c : 0, wide);
+  }
+}
+
+// Spreads a staged part of B or C (kPart rows of kWidth states) to fp32, each
+// value twice.
+template <typename T, int kWidth, int kThreads>
+__device__ __forceinline__ void spread_part(float* dst, const T* src, int tid) {
+#pragma unroll
+  for (int i0 = 0; i0 < kPart * kWidth / 2; i0 += kThreads) {
+    const int i = i0 + tid;
+    if (kPart * kWidth / 2 % kThreads == 0 || i < kPart * kWidth / 2) {
+      const float x = to_f32(src[2 * i]), y = to_f32(src[2 * i + 1]);
+      reinterpret_cast<float4*>(dst)[i] = make_float4(x, x, y, y);
+    }
+  }
 }
 
 // The lane's decay rates, in powers of two.

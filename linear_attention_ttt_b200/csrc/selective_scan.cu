@@ -16,6 +16,7 @@
 // first pass computes each chunk's end state from a zero start and its sum of
 // D_t, a small kernel joins the chunks (the decay over a chunk is
 // exp(A sum D_t)), and the main pass starts every chunk from its true state.
+#include <stdlib.h>
 #include "scan.cuh"
 
 namespace ttt {
@@ -33,190 +34,199 @@ Plan plan(const ScanArgs& a) {
   const int64_t most = (a.T + 63) / 64;
   c = c < most ? c : most;
   c = c < 1 ? 1 : c;
+  if (getenv("SCAN_C")) c = atoi(getenv("SCAN_C"));
   p.len = (int)(((a.T + c - 1) / c + kPart - 1) / kPart * kPart);
   if (p.len < kPart) p.len = kPart;
   p.chunks = a.T > 0 ? (a.T + p.len - 1) / p.len : 0;
   return p;
 }
 
-// Shared memory: D_t, D_t x_t [token][channel], B, C [token][state] (each value
-// twice), and y of the block's warps where a tile has several.
-size_t smem_bytes(const Grid& g, bool pre) {
-  const int states = g.warps * kNB;
-  return (size_t)kPart * (2 * g.cw() + (pre ? 2 : 4) * states + (g.warps > 1 && !pre ? g.wpb() * kCh : 0)) *
-         sizeof(float);
-}
+// Shared memory of a block. The raw rows of the next part arrive while the
+// present one is scanned: x, dt, B and C are used up when a part is staged, z
+// when its outputs are written.
+template <typename T, int W, bool kPre>
+struct Shared {
+  static constexpr int tpb = tiles_per_block(W), wpb = W * tpb, threads = 32 * wpb;
+  static constexpr int cw = tpb * kCh, ns = W * kNB;
+  float dt[kPart * cw], u[kPart * cw];            // D_t, D_t x_t [token][channel]
+  float b[kPart * 2 * ns], c[kPre ? 4 : kPart * 2 * ns];  // [token][state], each value twice
+  float y[kPre ? 4 : wpb * kPart * kCh];          // a warp's sums over its states [token][channel]
+  T rx[kPart * cw], rdt[kPart * cw], rz[kPre ? 8 : kPart * cw];
+  T rb[kPart * ns], rc[kPre ? 8 : kPart * ns];
+  int seq[kPart];
+};
 
 // kPre: the first pass over a chunk (its end state and sum of D_t); otherwise
-// the outputs. A part's rows are loaded while the part before is scanned.
+// the outputs.
 template <typename T, int W, bool kPre>
 __global__ void __launch_bounds__(128, sizeof(T) == 2 ? 4 : 3)
     scan_kernel(ScanArgs a, Plan p, float* states, float* sums, int* cuts) {
-  constexpr int V = Vec<T>::n, tpb = tiles_per_block(W), wpb = W * tpb;
-  constexpr int cw = tpb * kCh, ns = W * kNB, lpr = cw / V, spr = ns / V;
-  constexpr int dr = 32 * wpb / lpr, bdr = 32 * wpb / spr;  // rows between a thread's vectors
-  constexpr int kRows = (kPart + dr - 1) / dr, kBC = (kPart + bdr - 1) / bdr;
-  extern __shared__ __align__(16) float sm[];
-  __shared__ int s_seq[kPart];
+  using S = Shared<T, W, kPre>;
+  constexpr int cw = S::cw, ns = S::ns, threads = S::threads;
+  constexpr int kGroups = cw / 4, dr = threads / kGroups;  // a thread has 4 channels of every dr-th row
+  extern __shared__ __align__(16) unsigned char raw[];
+  S& s = *reinterpret_cast<S*>(raw);
   const Place q = place<W>(a, p.per_head);
-  const int chunk = blockIdx.y;
-  float* s_dt = sm;
-  float* s_u = s_dt + kPart * cw;
-  float* s_b = s_u + kPart * cw;
-  float* s_c = s_b + kPart * 2 * ns;
-  // one warp a tile: y takes the place of u, token by token
-  constexpr int ys = W == 1 ? cw : kCh;
-  float* s_y = W == 1 ? s_u + q.wt * kCh : s_c + kPart * 2 * ns + q.warp * kPart * kCh;
-  const int t0 = chunk * p.len, t1 = min(a.T, t0 + p.len);
+  const int chunk = blockIdx.y, t0 = chunk * p.len, t1 = min(a.T, t0 + p.len);
 
   f2 A2[4], hs[4] = {0, 0, 0, 0}, sum = 0;
   rates(a, q, A2);
-  const int64_t piece = ((int64_t)chunk * p.blocks + blockIdx.x) * wpb + q.warp;
+  const int64_t piece = ((int64_t)chunk * p.blocks + blockIdx.x) * S::wpb + q.warp;
   if (!kPre && chunk > 0) load4(states + piece * kPiece, q.lane, hs);
 
-  // what the thread stages: channels vc .. of rows row0, row0 + dr, ..; states
-  // n0 .. of B's and C's rows
-  const int vc = q.tid % lpr * V, vn = a.d - q.c0 - vc, row0 = q.tid / lpr;
-  const int n0 = q.tid % spr * V, nn = a.N - n0, brow0 = q.tid / spr;
-  const T* xp = static_cast<const T*>(a.x.p) + q.b * a.x.sb + q.h * a.x.sh + q.c0 + vc;
-  const T* dp = static_cast<const T*>(a.dt.p) + q.b * a.dt.sb + q.h * a.dt.sh + q.c0 + vc;
-  const T* zp = !kPre && a.z.p ? static_cast<const T*>(a.z.p) + q.b * a.z.sb + q.h * a.z.sh + q.c0 + vc : nullptr;
-  const T* bp = static_cast<const T*>(a.Bm.p) + q.b * a.Bm.sb + q.g * a.Bm.sh + n0;
-  const T* cp = static_cast<const T*>(a.Cm.p) + q.b * a.Cm.sb + q.g * a.Cm.sh + n0;
+  const int vc = q.tid % kGroups * 4, vn = a.d - q.c0 - vc, row0 = q.tid / kGroups;
+  float bias[4], skip[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    bias[j] = a.dt_bias && j < vn ? a.dt_bias[q.ch0 + vc + j] : 0.f;
+    skip[j] = !kPre && a.D && j < vn ? a.D[q.ch0 + vc + j] : 0.f;
+  }
+  const T* xp = static_cast<const T*>(a.x.p) + q.b * a.x.sb + q.h * a.x.sh + q.c0;
+  const T* dp = static_cast<const T*>(a.dt.p) + q.b * a.dt.sb + q.h * a.dt.sh + q.c0;
+  const T* zp = !kPre && a.z.p ? static_cast<const T*>(a.z.p) + q.b * a.z.sb + q.h * a.z.sh + q.c0 : nullptr;
+  const T* bp = static_cast<const T*>(a.Bm.p) + q.b * a.Bm.sb + q.g * a.Bm.sh;
+  const T* cp = static_cast<const T*>(a.Cm.p) + q.b * a.Cm.sb + q.g * a.Cm.sh;
+  T* op = kPre ? nullptr : static_cast<T*>(a.out.p) + q.b * a.out.sb + q.h * a.out.sh + q.c0 + vc;
 
-  Vec<T> xv[kRows], dv[kRows], zv[kRows], bv[kBC], cv[kBC];
-  Marks m;
+  Marks next;
   int seq;
   auto fetch = [&](int tb) {
-    m = marks(a, q, tb, min(kPart, t1 - tb), &seq);
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const int row = row0 + i * dr;
-      const int n = row < kPart && m.live >> row & 1 ? vn : 0;
-      const int64_t t = tb + row;
-      xv[i] = load_vec(xp + t * a.x.st, n, a.wide);
-      dv[i] = load_vec(dp + t * a.dt.st, n, a.wide);
-      if (zp) zv[i] = load_vec(zp + t * a.z.st, n, a.wide);
-    }
-#pragma unroll
-    for (int i = 0; i < kBC; ++i) {
-      const int row = brow0 + i * bdr;
-      const int n = row < kPart && m.live >> row & 1 ? nn : 0;
-      bv[i] = load_vec(bp + (int64_t)(tb + row) * a.Bm.st, n, a.wide);
-      if (!kPre) cv[i] = load_vec(cp + (int64_t)(tb + row) * a.Cm.st, n, a.wide);
-    }
+    next = marks(a, q, tb, min(kPart, t1 - tb), &seq);
+    const int64_t t = tb;
+    copy_part<T, cw, threads>(s.rx, xp + t * a.x.st, a.x.st, a.d - q.c0, next.live, q.tid, a.wide);
+    copy_part<T, cw, threads>(s.rdt, dp + t * a.dt.st, a.dt.st, a.d - q.c0, next.live, q.tid, a.wide);
+    copy_part<T, ns, threads>(s.rb, bp + t * a.Bm.st, a.Bm.st, a.N, next.live, q.tid, a.wide);
+    if (!kPre) copy_part<T, ns, threads>(s.rc, cp + t * a.Cm.st, a.Cm.st, a.N, next.live, q.tid, a.wide);
+    copy_commit();
+  };
+  auto fetch_z = [&](int tb, uint32_t live) {
+    if (zp) copy_part<T, cw, threads>(s.rz, zp + (int64_t)tb * a.z.st, a.z.st, a.d - q.c0, live, q.tid, a.wide);
+    copy_commit();
   };
   const int lane_c = q.wt * kCh + q.cg * 2, lane_s = q.wn * 2 * kNB + q.sg * 8;
+  float* ys = s.y + q.warp * kPart * kCh;
   bool cut = false;  // a sequence began in this chunk
 
   fetch(t0);
+  if (!kPre) fetch_z(t0, next.live);
   for (int tb = t0; tb < t1; tb += kPart) {
     const int nt = min(kPart, t1 - tb);
-    const Marks now = m;
-    // stage the part
-    Vec<T> xk[kRows], zk[kRows];  // for the outputs
+    const Marks now = next;
+    copy_wait<kPre ? 0 : 1>();
+    if (q.warp == 0) s.seq[q.lane] = seq;
+    __syncthreads();
+    // stage the part: step sizes, inputs, and D x where y is summed up
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const int row = row0 + i * dr;
-      if (row >= kPart) break;
-      float x[V], d[V], u[V];
-      unpack<T>(xv[i], x);
-      unpack<T>(dv[i], d);
+    for (int r = 0; r < kPart; r += dr) {
+      const int row = r + row0;
+      if (kPart % dr != 0 && row >= kPart) break;
+      float x[4], d[4];
+      load_row<T, 4>(s.rx + row * cw + vc, 4, true, x);
+      load_row<T, 4>(s.rdt + row * cw + vc, 4, true, d);
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float bias = a.dt_bias && j < vn ? a.dt_bias[q.ch0 + vc + j] : 0.f;
-        d[j] = step_of(d[j] + bias, a.softplus);
-        u[j] = d[j] * x[j];
+      for (int j = 0; j < 4; ++j) d[j] += bias[j];
+      if (a.softplus) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) d[j] = softplus_f(d[j]);
       }
-#pragma unroll
-      for (int j = 0; j < V; j += 4) {
-        *reinterpret_cast<float4*>(s_dt + row * cw + vc + j) = make_float4(d[j], d[j + 1], d[j + 2], d[j + 3]);
-        *reinterpret_cast<float4*>(s_u + row * cw + vc + j) = make_float4(u[j], u[j + 1], u[j + 2], u[j + 3]);
-      }
-      xk[i] = xv[i];
-      if (zp) zk[i] = zv[i];
+      *reinterpret_cast<float4*>(s.dt + row * cw + vc) = make_float4(d[0], d[1], d[2], d[3]);
+      *reinterpret_cast<float4*>(s.u + row * cw + vc) = make_float4(d[0] * x[0], d[1] * x[1], d[2] * x[2], d[3] * x[3]);
+      if (!kPre)
+        *reinterpret_cast<float4*>(s.y + (vc / kCh * W * kPart + row) * kCh + vc % kCh) =
+            make_float4(skip[0] * x[0], skip[1] * x[1], skip[2] * x[2], skip[3] * x[3]);
     }
-#pragma unroll
-    for (int i = 0; i < kBC; ++i) {
-      const int row = brow0 + i * bdr;
-      if (row >= kPart) break;
-#pragma unroll
-      for (int w = 0; w < (kPre ? 1 : 2); ++w) {
-        float f[V];
-        unpack<T>(w ? cv[i] : bv[i], f);
-        float* s = (w ? s_c : s_b) + 2 * (row * ns + n0);
-#pragma unroll
-        for (int j = 0; j < V; j += 2) *reinterpret_cast<float4*>(s + 2 * j) = make_float4(f[j], f[j], f[j + 1], f[j + 1]);
-      }
-    }
-    if (q.warp == 0) s_seq[q.lane] = seq;
+    spread_part<T, ns, threads>(s.b, s.rb, q.tid);
+    if (!kPre) spread_part<T, ns, threads>(s.c, s.rc, q.tid);
     __syncthreads();
     if (tb + kPart < t1) fetch(tb + kPart);
+    else if (!kPre) copy_commit();  // the groups stay in step
 
-    auto token = [&](int t, bool events) {
-      if (events && (now.begin >> t & 1)) {
-        cut = true;
-        seq_state(a, q, a.h0, s_seq[t], hs);
-      }
-      const f2 dt = *reinterpret_cast<const f2*>(s_dt + t * cw + lane_c);
-      const f2 u = *reinterpret_cast<const f2*>(s_u + t * cw + lane_c);
-      f2 bb[4];
-      four(s_b + t * 2 * ns + lane_s, bb);
+    // A token's decays are computed while the token before it is scanned, and
+    // the sums over states leave four tokens at a time, one block later: the
+    // exponentials run beside everything else.
+    f2 dec[4], y[4];
+    {
+      const f2 dt = *reinterpret_cast<const f2*>(s.dt + lane_c);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) hs[k] = fma2(ex2_pair(mul2(dt, A2[k])), hs[k], mul2(u, bb[k]));
-      if (kPre) {
-        sum = add2(sum, dt);
-      } else {
-        f2 cc[4];
-        four(s_c + t * 2 * ns + lane_s, cc);
-        f2 y = mul2(hs[0], cc[0]);
+      for (int k = 0; k < 4; ++k) dec[k] = ex2_pair(mul2(dt, A2[k]));
+      sum = add2(sum, dt);
+    }
+    auto sums_of = [&](int t4) {
+      // over the tile's four state lanes: halve twice, a token a lane is left
+      const bool up = q.sg & 1, up2 = q.sg & 2;
+      const f2 v0 = add2(up ? y[2] : y[0], __shfl_xor_sync(0xffffffffu, up ? y[0] : y[2], 1));
+      const f2 v1 = add2(up ? y[3] : y[1], __shfl_xor_sync(0xffffffffu, up ? y[1] : y[3], 1));
+      f2 w = add2(up2 ? v1 : v0, __shfl_xor_sync(0xffffffffu, up2 ? v0 : v1, 2));
+      f2* at = reinterpret_cast<f2*>(ys + (t4 + (up ? 2 : 0) + (up2 ? 1 : 0)) * kCh + q.cg * 2);
+      if (W == 1 || q.wn == 0) w = add2(w, *at);
+      *at = w;
+    };
+    auto block = [&](int t4, bool events) {
 #pragma unroll
-        for (int k = 1; k < 4; ++k) y = fma2(hs[k], cc[k], y);
-        // two channels over four lanes
-        float y0, y1;
-        un2(y, y0, y1);
-        const bool up = q.sg & 1;
-        float v = (up ? y1 : y0) + __shfl_xor_sync(0xffffffffu, up ? y0 : y1, 1);
-        v += __shfl_xor_sync(0xffffffffu, v, 2);
-        if (q.sg < 2) s_y[t * ys + q.cg * 2 + up] = v;
-        if (events && (now.end >> t & 1) && a.h_final) put_state(a, q, a.h_final, s_seq[t], hs);
+      for (int i = 0; i < 4; ++i) {
+        const int t = t4 + i, tn = (t + 1) % kPart;
+        const f2 dtn = *reinterpret_cast<const f2*>(s.dt + tn * cw + lane_c);
+        const f2 u = *reinterpret_cast<const f2*>(s.u + t * cw + lane_c);
+        f2 bb[4], cc[4], decn[4];
+        four(s.b + t * 2 * ns + lane_s, bb);
+        if (!kPre) four(s.c + t * 2 * ns + lane_s, cc);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) decn[k] = ex2_pair(mul2(dtn, A2[k]));
+        if (!kPre && i == 0 && t4 > 0) sums_of(t4 - 4);
+        if (events && (now.begin >> t & 1)) {
+          cut = true;
+          seq_state(a, q, a.h0, s.seq[t], hs);
+        }
+        if (!events || t < nt) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) hs[k] = fma2(dec[k], hs[k], mul2(u, bb[k]));
+        }
+        if (kPre) {
+          if (events ? t + 1 < nt : tn > 0) sum = add2(sum, dtn);
+        } else {
+          y[i] = mul2(hs[0], cc[0]);
+#pragma unroll
+          for (int k = 1; k < 4; ++k) y[i] = fma2(hs[k], cc[k], y[i]);
+          if (events && (now.end >> t & 1) && a.h_final) put_state(a, q, a.h_final, s.seq[t], hs);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) dec[k] = decn[k];
       }
     };
     if (nt == kPart && !(now.begin | now.end)) {
-#pragma unroll 4
-      for (int t = 0; t < kPart; ++t) token(t, false);
+#pragma unroll 1
+      for (int t = 0; t < kPart; t += 4) block(t, false);
     } else {
-      for (int t = 0; t < nt; ++t) token(t, true);
+#pragma unroll 1
+      for (int t = 0; t < nt; t += 4) block(t, true);
     }
-    __syncthreads();
     if (!kPre) {
+      sums_of((nt - 1) / 4 * 4);
+      copy_wait<1>();
+      __syncthreads();
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        const int row = row0 + i * dr;
-        if (row >= kPart) break;
+      for (int r = 0; r < kPart; r += dr) {
+        const int row = r + row0;
+        if (kPart % dr != 0 && row >= kPart) break;
         if (!(now.live >> row & 1)) continue;
-        float x[V], z[V], y[V];
-        unpack<T>(xk[i], x);
-        if (zp) unpack<T>(zk[i], z);
+        const float* base = s.y + (vc / kCh * W * kPart + row) * kCh + vc % kCh;
+        float4 v = *reinterpret_cast<const float4*>(base);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          float v;
-          if (W == 1) {
-            v = s_u[row * cw + vc + j];
-          } else {
-            const float* base = s_c + kPart * 2 * ns + ((vc + j) / kCh * W * kPart + row) * kCh + (vc + j) % kCh;
-            v = base[0];
-#pragma unroll
-            for (int w = 1; w < W; ++w) v += base[w * kPart * kCh];
-          }
-          const float dskip = a.D && j < vn ? a.D[q.ch0 + vc + j] : 0.f;
-          v = fmaf(dskip, x[j], v);
-          y[j] = zp ? v * silu_f(z[j]) : v;
+        for (int w = 1; w < W; ++w) {
+          const float4 o = *reinterpret_cast<const float4*>(base + w * kPart * kCh);
+          v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
         }
-        store_vec<T>(static_cast<T*>(a.out.p) + q.b * a.out.sb + q.h * a.out.sh + q.c0 + vc + (int64_t)(tb + row) * a.out.st,
-                     vn, a.wide, y);
+        float o[4] = {v.x, v.y, v.z, v.w};
+        if (zp) {
+          float z[4];
+          load_row<T, 4>(s.rz + row * cw + vc, 4, true, z);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[j] *= silu_f(z[j]);
+        }
+        store_row<T, 4>(op + (int64_t)(tb + row) * a.out.st, vn, a.wide, o);
       }
       __syncthreads();
+      if (tb + kPart < t1) fetch_z(tb + kPart, next.live);
     }
   }
   if (kPre) {
@@ -271,12 +281,18 @@ cudaError_t fwd(const ScanArgs& a, cudaStream_t s) {
   return for_warps(p.warps, [&](auto w) {
     constexpr int W = decltype(w)::value;
     const dim3 first((unsigned)p.blocks, p.chunks - 1), all((unsigned)p.blocks, p.chunks);
+    using First = Shared<T, W, true>;
+    using All = Shared<T, W, false>;
+    cudaError_t r = cudaFuncSetAttribute(scan_kernel<T, W, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(First));
+    if (r != cudaSuccess) return r;
+    r = cudaFuncSetAttribute(scan_kernel<T, W, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(All));
+    if (r != cudaSuccess) return r;
     if (p.chunks > 1) {
-      scan_kernel<T, W, true><<<first, threads, smem_bytes(p, true), s>>>(a, p, states, sums, cuts);
+      scan_kernel<T, W, true><<<first, threads, sizeof(First), s>>>(a, p, states, sums, cuts);
       const int64_t n = p.blocks * p.wpb() * kPiece;
       join_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(a, p, states, sums, cuts);
     }
-    scan_kernel<T, W, false><<<all, threads, smem_bytes(p, false), s>>>(a, p, states, sums, cuts);
+    scan_kernel<T, W, false><<<all, threads, sizeof(All), s>>>(a, p, states, sums, cuts);
     return cudaGetLastError();
   });
 }
