@@ -40,14 +40,17 @@ __device__ __forceinline__ f2 ex2_pair(f2 x) {
 }
 
 constexpr int kNB = 16;    // states a warp holds
-constexpr int kCh = 16;    // channels a warp holds: a lane has 4 states of 2 channels
 constexpr int kPart = 32;  // tokens staged at once: one 32-bit mask
+
+// A warp holds 16 states of 16 channels: a lane has 4 states of 2 channels, a
+// pair of fp32 being one state of both.
+constexpr int kCh = 16;
 constexpr int kPiece = kNB * kCh;  // a warp's states in memory: two float4 a lane
 // (float4 q of a lane: states 4*(lane&3) + 2q, +1, each with its two channels)
-
-// How a call's channels and states are laid over blocks of up to four warps:
-// channel tiles of one head beside one another, or a tile's 16-state parts.
 constexpr int tiles_per_block(int warps) { return warps >= 3 ? 1 : 4 / warps; }
+
+// How a call's channels and states are laid over blocks: channel tiles of one
+// head beside one another, each with a warp for every 16 states.
 struct Grid {
   int warps, tpb;   // 16-state warps a channel tile, channel tiles a block
   int per_head;     // blocks a head
@@ -64,11 +67,6 @@ inline Grid grid_of(const ScanArgs& a) {
   return g;
 }
 
-// Step size from its raw value, and the derivative of the one by the other.
-__device__ __forceinline__ float step_of(float raw, int softplus) {
-  return softplus ? softplus_f(raw) : raw;
-}
-
 // Where a token stands in its sequence.
 struct TokenAt {
   int seq, lo, hi;
@@ -82,6 +80,11 @@ __device__ __forceinline__ TokenAt token_at(const Seqs& q, int b, int T, int t, 
     r.live = t >= r.lo && t < r.hi;
   }
   return r;
+}
+
+// Step size from its raw value.
+__device__ __forceinline__ float step_of(float raw, int softplus) {
+  return softplus ? softplus_f(raw) : raw;
 }
 
 // Which sequence events fall on a part's tokens.
@@ -149,14 +152,15 @@ __device__ __forceinline__ void copy_part(T* dst, const T* p, int64_t stride, in
   }
 }
 
-// Spreads a staged part of B or C (kPart rows of kWidth states) to fp32, each
-// value twice.
+// A staged part of B or C (kPart rows of kWidth states) to fp32, each value
+// twice: a packed operation takes two channels with one state.
 template <typename T, int kWidth, int kThreads>
 __device__ __forceinline__ void spread_part(float* dst, const T* src, int tid) {
+  constexpr int n = kPart * kWidth / 2;
 #pragma unroll
-  for (int i0 = 0; i0 < kPart * kWidth / 2; i0 += kThreads) {
+  for (int i0 = 0; i0 < n; i0 += kThreads) {
     const int i = i0 + tid;
-    if (kPart * kWidth / 2 % kThreads == 0 || i < kPart * kWidth / 2) {
+    if (n % kThreads == 0 || i < n) {
       const float x = to_f32(src[2 * i]), y = to_f32(src[2 * i + 1]);
       reinterpret_cast<float4*>(dst)[i] = make_float4(x, x, y, y);
     }
@@ -167,11 +171,12 @@ __device__ __forceinline__ void spread_part(float* dst, const T* src, int tid) {
 __device__ __forceinline__ void rates(const ScanArgs& a, const Place& q, f2 (&A2)[4]) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const int n = q.wn * kNB + q.sg * 4 + k, c = q.wt * kCh + q.cg * 2;
     float r[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      r[i] = n < a.N && q.c0 + c + i < a.d ? a.A[(q.ch0 + c + i) * a.N + n] * kLog2e : 0.f;
+    for (int i = 0; i < 2; ++i) {
+      const int n = q.wn * kNB + q.sg * 4 + k, c = q.wt * kCh + q.cg * 2 + i;
+      r[i] = n < a.N && q.c0 + c < a.d ? a.A[(q.ch0 + c) * a.N + n] * kLog2e : 0.f;
+    }
     A2[k] = mk2(r[0], r[1]);
   }
 }
@@ -181,11 +186,12 @@ __device__ __forceinline__ void seq_state(const ScanArgs& a, const Place& q, con
                                           f2 (&s)[4]) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const int n = q.wn * kNB + q.sg * 4 + k, c = q.wt * kCh + q.cg * 2;
     float r[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      r[i] = p && n < a.N && q.c0 + c + i < a.d ? p[((int64_t)seq * a.H * a.d + q.ch0 + c + i) * a.N + n] : 0.f;
+    for (int i = 0; i < 2; ++i) {
+      const int n = q.wn * kNB + q.sg * 4 + k, c = q.wt * kCh + q.cg * 2 + i;
+      r[i] = p && n < a.N && q.c0 + c < a.d ? p[((int64_t)seq * a.H * a.d + q.ch0 + c) * a.N + n] : 0.f;
+    }
     s[k] = mk2(r[0], r[1]);
   }
 }
@@ -193,17 +199,18 @@ __device__ __forceinline__ void put_state(const ScanArgs& a, const Place& q, flo
                                           const f2 (&s)[4]) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const int n = q.wn * kNB + q.sg * 4 + k, c = q.wt * kCh + q.cg * 2;
     float r[2];
     un2(s[k], r[0], r[1]);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (n < a.N && q.c0 + c + i < a.d) p[((int64_t)seq * a.H * a.d + q.ch0 + c + i) * a.N + n] = r[i];
+    for (int i = 0; i < 2; ++i) {
+      const int n = q.wn * kNB + q.sg * 4 + k, c = q.wt * kCh + q.cg * 2 + i;
+      if (n < a.N && q.c0 + c < a.d) p[((int64_t)seq * a.H * a.d + q.ch0 + c) * a.N + n] = r[i];
+    }
   }
 }
 
 // A warp's states as a piece of memory.
-__device__ __forceinline__ void load4(const float* p, int lane, f2 (&s)[4]) {
+__device__ __forceinline__ void load_piece(const float* p, int lane, f2 (&s)[4]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const ulonglong2 v = reinterpret_cast<const ulonglong2*>(p)[i * 32 + lane];
@@ -211,7 +218,7 @@ __device__ __forceinline__ void load4(const float* p, int lane, f2 (&s)[4]) {
     s[2 * i + 1] = v.y;
   }
 }
-__device__ __forceinline__ void store4(float* p, int lane, const f2 (&s)[4]) {
+__device__ __forceinline__ void store_piece(float* p, int lane, const f2 (&s)[4]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i)
     reinterpret_cast<ulonglong2*>(p)[i * 32 + lane] = make_ulonglong2(s[2 * i], s[2 * i + 1]);
@@ -234,17 +241,18 @@ cudaError_t for_warps(int warps, F f) {
   return cudaErrorInvalidValue;
 }
 
-// Where element e of [blocks][warps a block][kPiece] stands.
+// Where element e of [blocks][warps a block][piece] stands.
 struct PieceAt {
   int64_t blk;
   int n, cb;  // state, channel in the block
 };
 __host__ __device__ __forceinline__ PieceAt piece_at(int64_t e, const Grid& g) {
-  const int in = (int)(e % kPiece), lane = in % 128 / 4, warp = (int)(e / kPiece % g.wpb());
+  const int in = (int)(e % kPiece), lane = in % 128 / 4, k = in / 128 * 2 + in % 4 / 2, i = in % 2;
+  const int warp = (int)(e / kPiece % g.wpb());
   PieceAt r;
   r.blk = e / kPiece / g.wpb();
-  r.n = warp % g.warps * kNB + (lane & 3) * 4 + in / 128 * 2 + in % 4 / 2;
-  r.cb = warp / g.warps * kCh + (lane >> 2) * 2 + in % 2;
+  r.n = warp % g.warps * kNB + (lane & 3) * 4 + k;
+  r.cb = warp / g.warps * kCh + (lane >> 2) * 2 + i;
   return r;
 }
 

@@ -16,7 +16,6 @@
 // first pass computes each chunk's end state from a zero start and its sum of
 // D_t, a small kernel joins the chunks (the decay over a chunk is
 // exp(A sum D_t)), and the main pass starts every chunk from its true state.
-#include <stdlib.h>
 #include "scan.cuh"
 
 namespace ttt {
@@ -26,15 +25,19 @@ namespace {
 struct Plan : Grid {
   int chunks, len;  // len: tokens, a multiple of kPart
 };
+// Chunks cost a second pass, which only idle SMs pay for. Measured at N = 16,
+// bf16, gated: with 1024 warps and more one chunk wins (B4 T4096 d4096: 690 us
+// against 797 with four chunks a warp; B16 T1024 d4096: 490 against 670), with
+// 256 and fewer about 4096 warps in all do (B1 T4096 d4096: 541 us in one chunk,
+// 226 in 16; B1 T16384 d2048: 2135 in one, 436 in 32). Chunks below 64 tokens
+// gain nothing.
 Plan plan(const ScanArgs& a) {
   Plan p;
   static_cast<Grid&>(p) = grid_of(a);
-  const int64_t have = p.blocks * p.wpb(), want = 148 * 16;
-  int64_t c = (want + have - 1) / have;
-  const int64_t most = (a.T + 63) / 64;
+  const int64_t warps = p.blocks * p.wpb(), most = (a.T + 63) / 64;
+  int64_t c = warps >= 640 || warps == 0 ? 1 : 4096 / warps;
   c = c < most ? c : most;
   c = c < 1 ? 1 : c;
-  if (getenv("SCAN_C")) c = atoi(getenv("SCAN_C"));
   p.len = (int)(((a.T + c - 1) / c + kPart - 1) / kPart * kPart);
   if (p.len < kPart) p.len = kPart;
   p.chunks = a.T > 0 ? (a.T + p.len - 1) / p.len : 0;
@@ -72,7 +75,7 @@ __global__ void __launch_bounds__(128, sizeof(T) == 2 ? 4 : 3)
   f2 A2[4], hs[4] = {0, 0, 0, 0}, sum = 0;
   rates(a, q, A2);
   const int64_t piece = ((int64_t)chunk * p.blocks + blockIdx.x) * S::wpb + q.warp;
-  if (!kPre && chunk > 0) load4(states + piece * kPiece, q.lane, hs);
+  if (!kPre && chunk > 0) load_piece(states + piece * kPiece, q.lane, hs);
 
   const int vc = q.tid % kGroups * 4, vn = a.d - q.c0 - vc, row0 = q.tid / kGroups;
   float bias[4], skip[4];
@@ -230,7 +233,7 @@ __global__ void __launch_bounds__(128, sizeof(T) == 2 ? 4 : 3)
     }
   }
   if (kPre) {
-    store4(states + piece * kPiece, q.lane, hs);
+    store_piece(states + piece * kPiece, q.lane, hs);
     if (q.wn == 0 && q.sg == 0)
       *reinterpret_cast<f2*>(sums + ((int64_t)chunk * p.blocks + blockIdx.x) * cw + lane_c) = sum;
     if (blockIdx.x == 0 && q.tid == 0) cuts[chunk] = cut;

@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(128) pre_kernel(ScanBwdArgs ga, Plan p, Ws ws)
   for (int part = chunk * p.chunk; part < part1; ++part) {
     const int64_t at = (int64_t)part * p.blocks + blockIdx.x;
     if (part > chunk * p.chunk) {
-      store4(ws.start + (at * nw + q.warp) * kPiece, q.lane, hs);
+      store_piece(ws.start + (at * nw + q.warp) * kPiece, q.lane, hs);
       if (q.wn == 0 && q.sg == 0)
         *reinterpret_cast<f2*>(ws.sums + at * K::cw + q.wt * kCh + q.cg * 2) = sum;
     }
@@ -238,8 +238,8 @@ __global__ void __launch_bounds__(128) pre_kernel(ScanBwdArgs ga, Plan p, Ws ws)
     __syncthreads();
   }
   const int64_t at = (int64_t)chunk * p.blocks + blockIdx.x;
-  store4(ws.hin + (at * nw + q.warp) * kPiece, q.lane, hs);
-  store4(ws.gin + (at * nw + q.warp) * kPiece, q.lane, gs);
+  store_piece(ws.hin + (at * nw + q.warp) * kPiece, q.lane, hs);
+  store_piece(ws.gin + (at * nw + q.warp) * kPiece, q.lane, gs);
   if (q.wn == 0 && q.sg == 0) *reinterpret_cast<f2*>(ws.total + at * K::cw + q.wt * kCh + q.cg * 2) = sum;
 }
 
@@ -306,8 +306,8 @@ __global__ void __launch_bounds__(128, 3) main_kernel(ScanBwdArgs ga, Plan p, Ws
   const int64_t chat = (int64_t)chunk * p.blocks + blockIdx.x;
   f2 A2[4], h_in[4], gs[4], dA[4] = {0, 0, 0, 0};
   rates(a, q, A2);
-  load4(ws.hin + (chat * nw + q.warp) * kPiece, q.lane, h_in);
-  load4(ws.gin + (chat * nw + q.warp) * kPiece, q.lane, gs);
+  load_piece(ws.hin + (chat * nw + q.warp) * kPiece, q.lane, h_in);
+  load_piece(ws.gin + (chat * nw + q.warp) * kPiece, q.lane, gs);
   // channel sums of the thread's vectors: their channels are the same in every turn
   constexpr int ystride = W == 1 ? K::cw : kCh;
   const int vc = q.tid % lpr * V, vn = a.d - q.c0 - vc;
@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(128, 3) main_kernel(ScanBwdArgs ga, Plan p, Ws
       for (int k = 0; k < 4; ++k) hs[k] = h_in[k];
     } else {
       const int64_t at = (int64_t)part * p.blocks + blockIdx.x;
-      load4(ws.start + (at * nw + q.warp) * kPiece, q.lane, hs);
+      load_piece(ws.start + (at * nw + q.warp) * kPiece, q.lane, hs);
       const TokenAt here = token_at(a.seqs, q.b, a.T, tb, a.status);
       if (here.live && here.lo < part0 * kPart) {  // its sequence entered the chunk from before
         const f2 sum = *reinterpret_cast<const f2*>(ws.sums + at * K::cw + q.wt * kCh + q.cg * 2);
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(128, 3) main_kernel(ScanBwdArgs ga, Plan p, Ws
     const int lane_o = q.wt * kCh + q.cg * 2, lane_s = q.wn * 2 * kNB + q.sg * 8;
     // forward, keeping the state before every block
     for (int t = 0; t < nt; ++t) {
-      if (t % kBlk == 0) store4(s.keep + t / kBlk * kPiece, q.lane, hs);
+      if (t % kBlk == 0) store_piece(s.keep + t / kBlk * kPiece, q.lane, hs);
       if (m.begin >> t & 1) seq_state(a, q, a.h0, s_seq[t], hs);
       const f2 dt = *reinterpret_cast<const f2*>(s.dt + t * K::cw + lane_o);
       const f2 u = *reinterpret_cast<const f2*>(s.u + t * K::cw + lane_o);
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(128, 3) main_kernel(ScanBwdArgs ga, Plan p, Ws
     for (int blk = (nt - 1) / kBlk; blk >= 0; --blk) {
       f2 dec[kBlk][4], st[kBlk][4];  // the decays, and the decayed states exp(D A) h_{t-1}
       f2 h[4];
-      load4(s.keep + blk * kPiece, q.lane, h);
+      load_piece(s.keep + blk * kPiece, q.lane, h);
 #pragma unroll
       for (int i = 0; i < kBlk; ++i) {
         const int t = blk * kBlk + i;
@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(128, 3) main_kernel(ScanBwdArgs ga, Plan p, Ws
     }
     __syncthreads();
   }
-  store4(ws.dA + (chat * nw + q.warp) * kPiece, q.lane, dA);
+  store_piece(ws.dA + (chat * nw + q.warp) * kPiece, q.lane, dA);
   // the threads' channel sums: rows of threads that share a vector, in order
   for (int w = 0; w < 2; ++w) {
     float* sh = s.dt;  // [threads / lpr][cw]: within the three staged tensors
