@@ -219,6 +219,14 @@ __device__ __forceinline__ void load_row(const T* p, int n, bool wide, float (&f
     }
   }
 }
+// kWhole: the piece is known to be aligned and whole. Loads without a choice
+// stay in flight beside one another; behind a choice each is waited for where
+// its two ways meet. Kernels choose once for all of a block's loads.
+template <bool kWhole, typename T, int V>
+__device__ __forceinline__ void read_row(const T* p, int n, bool wide, float (&f)[V]) {
+  if constexpr (kWhole) load_row<T, V>(p, V, true, f);
+  else load_row<T, V>(p, n, wide, f);
+}
 template <typename T, int V>
 __device__ __forceinline__ void store_row(T* p, int n, bool wide, const float (&f)[V]) {
   if constexpr (V * sizeof(T) == 16) {
@@ -234,6 +242,12 @@ __device__ __forceinline__ void store_row(T* p, int n, bool wide, const float (&
         if (i < n) p[i] = from_f32<T>(f[i]);
     }
   }
+}
+
+template <bool kWhole, typename T, int V>
+__device__ __forceinline__ void write_row(T* p, int n, bool wide, const float (&f)[V]) {
+  if constexpr (kWhole) store_row<T, V>(p, V, true, f);
+  else store_row<T, V>(p, n, wide, f);
 }
 
 // Asynchronous copy of a row piece of 16 bytes into shared memory: the first n

@@ -36,11 +36,23 @@ Plan plan(const ScanArgs& a) {
   Plan p;
   static_cast<Grid&>(p) = grid_of(a);
   p.parts = (a.T + kPart - 1) / kPart;
-  // eight rounds of three blocks an SM; a chunk of one part costs the most
-  // join traffic, a long one leaves SMs idle at the end
-  const int64_t want = 148 * 3 * 8, c = (want + p.blocks - 1) / p.blocks;
-  p.chunk = (int)(c >= p.parts ? 1 : (p.parts + c - 1) / c);
-  if (p.chunk < 1) p.chunk = 1;
+  // Blocks run three an SM; a chunk costs its parts and about 0.6 of one for
+  // itself (rates, sums, the join), the last round of blocks 0.8 of a chunk.
+  // Measured against this, chunks of 1 to 64 parts: B4 T2048 d4096 takes 1327 us
+  // at its best (3 parts; 4 parts, which this picks, 1351; 1 part 1457, 64 parts
+  // 1816), B1 T2048 d4096 394 us (3 parts; 2, picked, 424; 64 parts 1396).
+  const double slots = 148 * 3;
+  double best = 0;
+  p.chunk = 1;
+  for (int c = 1; c <= p.parts && c <= 1024; ++c) {
+    const double rounds = (double)p.blocks * ((p.parts + c - 1) / c) / slots;
+    const double cost = ((rounds > 1 ? rounds : 1) + 0.8) * (c + 0.6);
+    if ((p.parts + c - 1) / c <= 65535 && (best == 0 || cost < best)) {
+      best = cost;
+      p.chunk = c;
+    }
+  }
+  if (p.parts / 65535 >= p.chunk) p.chunk = p.parts / 65535 + 1;
   p.chunks = (p.parts + p.chunk - 1) / p.chunk;
   return p;
 }
@@ -74,173 +86,187 @@ Ws carve(const ScanArgs& a, const Plan& p, float* base) {
   return w;
 }
 
-template <typename T, int W>
-struct Kernel {
-  static constexpr int V = Vec<T>::n, tpb = tiles_per_block(W), nw = W * tpb;
-  static constexpr int cw = tpb * kCh, states = W * kNB;
-
-  // Stages a part: D_t, D_t x_t and e_t (the gradient of y_t) of the block's
-  // channels [token][channel], B and C of its states [token][state], each
-  // value twice. Dead tokens and channels are zeros.
-  static __device__ __forceinline__ void stage(const ScanArgs& a, const TokView& dy, const Place& q, int tb, uint32_t live, float* s_dt, float* s_u,
-                                               float* s_e, float* s_b, float* s_c) {
-    constexpr int lpr = cw / V;
-#pragma unroll
-    for (int i = q.tid; i < kPart * lpr; i += 32 * nw) {
-      const int row = i / lpr, vc = i % lpr * V;
-      const int n = live >> row & 1 ? a.d - q.c0 - vc : 0;
-      const int64_t t = tb + row;
-      const T* xp = static_cast<const T*>(a.x.p) + q.b * a.x.sb + q.h * a.x.sh + q.c0 + vc + t * a.x.st;
-      const T* dp = static_cast<const T*>(a.dt.p) + q.b * a.dt.sb + q.h * a.dt.sh + q.c0 + vc + t * a.dt.st;
-      const T* gp = static_cast<const T*>(dy.p) + q.b * dy.sb + q.h * dy.sh + q.c0 + vc + t * dy.st;
-      const Vec<T> xv = load_vec(xp, n, a.wide), dv = load_vec(dp, n, a.wide), gv = load_vec(gp, n, a.wide);
-      float x[V], d[V], e[V], u[V];
-      unpack<T>(xv, x);
-      unpack<T>(dv, d);
-      unpack<T>(gv, e);
-      if (a.z.p) {
-        const T* zp = static_cast<const T*>(a.z.p) + q.b * a.z.sb + q.h * a.z.sh + q.c0 + vc + t * a.z.st;
-        float z[V];
-        unpack<T>(load_vec(zp, n, a.wide), z);
-#pragma unroll
-        for (int j = 0; j < V; ++j) e[j] *= silu_f(z[j]);
-      }
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float bias = a.dt_bias && j < n ? a.dt_bias[q.ch0 + vc + j] : 0.f;
-        d[j] = j < n ? step_of(d[j] + bias, a.softplus) : 0.f;
-        u[j] = d[j] * x[j];
-      }
-#pragma unroll
-      for (int j = 0; j < V; j += 4) {
-        const int o = row * cw + vc + j;
-        *reinterpret_cast<float4*>(s_dt + o) = make_float4(d[j], d[j + 1], d[j + 2], d[j + 3]);
-        *reinterpret_cast<float4*>(s_u + o) = make_float4(u[j], u[j + 1], u[j + 2], u[j + 3]);
-        *reinterpret_cast<float4*>(s_e + o) = make_float4(e[j], e[j + 1], e[j + 2], e[j + 3]);
-      }
-    }
-    constexpr int spr = states / V;
-    for (int i = q.tid; i < kPart * spr * 2; i += 32 * nw) {
-      const int m = i / (kPart * spr), row = i / spr % kPart, n0 = i % spr * V;
-      const int n = live >> row & 1 ? a.N - n0 : 0;
-      const TokView& w = m ? a.Cm : a.Bm;
-      const T* p = static_cast<const T*>(w.p) + q.b * w.sb + q.g * w.sh + (int64_t)(tb + row) * w.st + n0;
-      float f[V];
-      unpack<T>(load_vec(p, n, a.wide), f);
-      float* s = (m ? s_c : s_b) + 2 * (row * states + n0);
-#pragma unroll
-      for (int j = 0; j < V; j += 2)
-        *reinterpret_cast<float4*>(s + 2 * j) = make_float4(f[j], f[j], f[j + 1], f[j + 1]);
-    }
-  }
-};
-
+// Shared memory of a block.
+template <int W, bool kPre>
 struct Shared {
-  float *dt, *u, *e, *b, *c;  // [32][cw], [32][2 * states]
-  float *y, *r;          // a warp's: [32][ystride]; r takes the place of u where a tile has one warp
-  float* keep;           // a warp's kept states: [8][kPiece], later its dB, dC [32][32]
+  static constexpr int tpb = tiles_per_block(W), wpb = W * tpb, threads = 32 * wpb;
+  static constexpr int cw = tpb * kCh, ns = W * kNB;
+  static constexpr int kBlocks = kPart / kBlk;
+  float dt[kPart * cw], u[kPart * cw], e[kPart * cw];  // D_t, D_t x_t, e_t [token][channel]
+  float b[kPart * 2 * ns], c[kPart * 2 * ns];          // [token][state], each value twice
+  // A warp's sums over its states of g B, g A exp(DA) h and C h [token][channel].
+  // With one warp a tile the last two take the places of u and e, token by token.
+  float q[kPre ? 4 : wpb * kPart * kCh];
+  float ry[kPre || W == 1 ? 4 : 2 * wpb * kPart * kCh];
+  // A warp's states before every block but the last; a block's dB, dC [4][32]
+  // take the place of its states, the last block's have room of their own.
+  float keep[kPre ? 4 : wpb * ((kBlocks - 1) * kPiece + kBlk * 32)];
+  float red[kPre ? 4 : wpb * 256];                     // a token's dB, dC on their way over lanes
+  int seq[kPart];
 };
-template <int W>
-__device__ __forceinline__ Shared shared_of(float* sm, const Place& q) {
-  constexpr int tpb = tiles_per_block(W), cw = tpb * kCh, states = W * kNB, nw = W * tpb;
-  Shared s;
-  s.dt = sm;
-  s.u = s.dt + kPart * cw;
-  s.e = s.u + kPart * cw;
-  s.b = s.e + kPart * cw;
-  s.c = s.b + kPart * 2 * states;
-  float* next = s.c + kPart * 2 * states;
-  if (W == 1) {
-    s.y = next + q.wt * kCh;
-    s.r = s.u + q.wt * kCh;
-    next += kPart * cw;
-  } else {
-    s.y = next + q.warp * kPart * kCh;
-    s.r = s.y + nw * kPart * kCh;
-    next += 2 * nw * kPart * kCh;
+
+// Stages a part: D_t, D_t x_t and e_t (the gradient of y_t) of the block's
+// channels, B and C of its states. Dead tokens are zeros, so that nothing of
+// theirs enters a sum.
+template <bool kWhole, typename T, typename S>
+__device__ __forceinline__ void stage_as(const ScanArgs& a, const TokView& dy, const Place& q, int tb, uint32_t live,
+                                      const float (&bias)[4], S& s) {
+  constexpr int kGroups = S::cw / 4, dr = S::threads / kGroups;
+  const int vc = q.tid % kGroups * 4, vn = a.d - q.c0 - vc;
+  constexpr int kTurns = (kPart + dr - 1) / dr;
+  const T* xp = static_cast<const T*>(a.x.p) + q.b * a.x.sb + q.h * a.x.sh + q.c0 + vc;
+  const T* dp = static_cast<const T*>(a.dt.p) + q.b * a.dt.sb + q.h * a.dt.sh + q.c0 + vc;
+  const T* gp = static_cast<const T*>(dy.p) + q.b * dy.sb + q.h * dy.sh + q.c0 + vc;
+  // without a gate the gradient stands in its place and is not used
+  const bool gate = a.z.p != nullptr;
+  const T* zp = gate ? static_cast<const T*>(a.z.p) + q.b * a.z.sb + q.h * a.z.sh + q.c0 + vc : gp;
+  const int64_t zs = gate ? a.z.st : dy.st;
+  float x[kTurns][4], d[kTurns][4], e[kTurns][4], z[kTurns][4];
+#pragma unroll
+  for (int i = 0; i < kTurns; ++i) {
+    const int row = min(i * dr + q.tid / kGroups, kPart - 1);
+    const int n = kWhole || live >> row & 1 ? vn : 0;
+    const int64_t t = tb + row;
+    read_row<kWhole, T, 4>(xp + t * a.x.st, n, a.wide, x[i]);
+    read_row<kWhole, T, 4>(dp + t * a.dt.st, n, a.wide, d[i]);
+    read_row<kWhole, T, 4>(gp + t * dy.st, n, a.wide, e[i]);
+    read_row<kWhole, T, 4>(zp + t * zs, n, a.wide, z[i]);
   }
-  s.keep = next + q.warp * (kPart / kBlk) * kPiece;
-  return s;
+#pragma unroll
+  for (int i = 0; i < kTurns; ++i) {
+    const int row = i * dr + q.tid / kGroups;
+    if (kPart % dr != 0 && row >= kPart) break;
+    const bool on = kWhole || live >> row & 1;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      d[i][j] += bias[j];
+      if (a.softplus) d[i][j] = softplus_f(d[i][j]);
+      if (gate) e[i][j] *= silu_f(z[i][j]);
+      if (!on) d[i][j] = 0.f;
+    }
+    const int o = row * S::cw + vc;
+    *reinterpret_cast<float4*>(s.dt + o) = make_float4(d[i][0], d[i][1], d[i][2], d[i][3]);
+    *reinterpret_cast<float4*>(s.u + o) =
+        make_float4(d[i][0] * x[i][0], d[i][1] * x[i][1], d[i][2] * x[i][2], d[i][3] * x[i][3]);
+    *reinterpret_cast<float4*>(s.e + o) = make_float4(e[i][0], e[i][1], e[i][2], e[i][3]);
+  }
+  constexpr int per = S::ns / 2;  // two states a turn: consecutive threads write consecutive 16 bytes
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const TokView& v = w ? a.Cm : a.Bm;
+    const T* p = static_cast<const T*>(v.p) + q.b * v.sb + q.g * v.sh;
+#pragma unroll
+    for (int i0 = 0; i0 < kPart * per; i0 += S::threads) {
+      const int i = i0 + q.tid, row = i / per, n0 = i % per * 2;
+      if (kPart * per % S::threads != 0 && i >= kPart * per) break;
+      const bool on = kWhole || live >> row & 1;
+      const T* at = p + (int64_t)(tb + row) * v.st + n0;
+      const float f0 = on && n0 < a.N ? to_f32(at[0]) : 0.f, f1 = on && n0 + 1 < a.N ? to_f32(at[1]) : 0.f;
+      reinterpret_cast<float4*>(w ? s.c : s.b)[i] = make_float4(f0, f0, f1, f1);
+    }
+  }
 }
-size_t smem_bytes(const Plan& p, bool pre) {
-  const int cw = p.tpb * kCh, nw = p.tpb * p.warps;
-  int64_t n = 3 * kPart * cw + 2 * kPart * 2 * p.warps * kNB;
-  if (!pre) n += (p.warps == 1 ? kPart * cw : 2 * nw * kPart * kCh) + nw * (kPart / kBlk) * kPiece;
-  return (size_t)n * sizeof(float);
+
+// Whether a part is whole: every token live, every channel there, rows aligned.
+template <typename S>
+__device__ __forceinline__ bool is_whole(const ScanArgs& a, const Place& q, uint32_t live) {
+  return a.wide && live == 0xffffffffu && q.c0 + S::cw <= a.d;
+}
+template <typename T, typename S>
+__device__ __forceinline__ void stage(const ScanArgs& a, const TokView& dy, const Place& q, int tb, uint32_t live,
+                                      const float (&bias)[4], S& s) {
+  if (is_whole<S>(a, q, live)) stage_as<true, T>(a, dy, q, tb, live, bias, s);
+  else stage_as<false, T>(a, dy, q, tb, live, bias, s);
+}
+
+__device__ __forceinline__ void four_of(const float* p, int n, float (&f)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) f[j] = p && j < n ? p[j] : 0.f;
 }
 
 // First pass over a chunk: start states of its parts from a zero start, sums
 // of D_t before each part and over the chunk, the chunk's end state (to hin of
 // the chunk itself, joined later), and the gradient it sends back (to gin).
 template <typename T, int W>
-__global__ void __launch_bounds__(128) pre_kernel(ScanBwdArgs ga, Plan p, Ws ws) {
-  using K = Kernel<T, W>;
-  extern __shared__ __align__(16) float sm[];
-  __shared__ int s_seq[kPart];
+__global__ void __launch_bounds__(128, 4) pre_kernel(ScanBwdArgs ga, Plan p, Ws ws) {
+  using S = Shared<W, true>;
+  extern __shared__ __align__(16) unsigned char raw[];
+  S& s = *reinterpret_cast<S*>(raw);
   const ScanArgs& a = ga.f;
   const Place q = place<W>(a, p.per_head);
-  const Shared s = shared_of<W>(sm, q);
-  constexpr int nw = K::nw;
   const int chunk = blockIdx.y;
   f2 A2[4], hs[4] = {0, 0, 0, 0}, gs[4] = {0, 0, 0, 0}, P[4];
   rates(a, q, A2);
-  const f2 one = mk2(1.f, 1.f);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) P[k] = one;
+  for (int k = 0; k < 4; ++k) P[k] = mk2(1.f, 1.f);
   f2 sum = 0;
+  float bias[4];
+  {
+    const int vc = q.tid % (S::cw / 4) * 4;
+    four_of(a.dt_bias ? a.dt_bias + q.ch0 + vc : nullptr, a.d - q.c0 - vc, bias);
+  }
   bool open = true;  // the sequence that enters the chunk has not ended
+  const int lane_c = q.wt * kCh + q.cg * 2, lane_s = q.wn * 2 * kNB + q.sg * 8;
   const int part1 = min(p.parts, (chunk + 1) * p.chunk);
   for (int part = chunk * p.chunk; part < part1; ++part) {
     const int64_t at = (int64_t)part * p.blocks + blockIdx.x;
     if (part > chunk * p.chunk) {
-      store_piece(ws.start + (at * nw + q.warp) * kPiece, q.lane, hs);
-      if (q.wn == 0 && q.sg == 0)
-        *reinterpret_cast<f2*>(ws.sums + at * K::cw + q.wt * kCh + q.cg * 2) = sum;
+      store_piece(ws.start + (at * S::wpb + q.warp) * kPiece, q.lane, hs);
+      if (q.wn == 0 && q.sg == 0) *reinterpret_cast<f2*>(ws.sums + at * S::cw + lane_c) = sum;
     }
     const int tb = part * kPart, nt = min(kPart, a.T - tb);
     int seq;
     const Marks m = marks(a, q, tb, nt, &seq);
-    if (q.warp == 0) s_seq[q.lane] = seq;
-    K::stage(a, ga.dy, q, tb, m.live, s.dt, s.u, s.e, s.b, s.c);
+    if (q.warp == 0) s.seq[q.lane] = seq;
+    stage<T>(a, ga.dy, q, tb, m.live, bias, s);
     __syncthreads();
-    for (int t = 0; t < nt; ++t) {
-      if (m.begin >> t & 1) {
-        seq_state(a, q, a.h0, s_seq[t], hs);
+    auto token = [&](int t, bool events) {
+      if (events && (m.begin >> t & 1)) {
+        seq_state(a, q, a.h0, s.seq[t], hs);
         if (tb + t != chunk * p.chunk * kPart) open = false;
       }
-      const int o = t * K::cw + q.wt * kCh + q.cg * 2;
-      const f2 dt = *reinterpret_cast<const f2*>(s.dt + o), u = *reinterpret_cast<const f2*>(s.u + o);
+      const f2 dt = *reinterpret_cast<const f2*>(s.dt + t * S::cw + lane_c);
+      const f2 u = *reinterpret_cast<const f2*>(s.u + t * S::cw + lane_c);
+      const f2 e = *reinterpret_cast<const f2*>(s.e + t * S::cw + lane_c);
       f2 bb[4], cc[4], dec[4];
-      four(s.b + t * 2 * K::states + q.wn * 2 * kNB + q.sg * 8, bb);
+      four(s.b + t * 2 * S::ns + lane_s, bb);
+      four(s.c + t * 2 * S::ns + lane_s, cc);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         dec[k] = ex2_pair(mul2(dt, A2[k]));
         hs[k] = fma2(dec[k], hs[k], mul2(u, bb[k]));
       }
       sum = add2(sum, dt);
-      if (open) {
-        const f2 e = *reinterpret_cast<const f2*>(s.e + o);
-        four(s.c + t * 2 * K::states + q.wn * 2 * kNB + q.sg * 8, cc);
+      if (events && !open) return;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          P[k] = mul2(P[k], dec[k]);
-          gs[k] = fma2(P[k], mul2(e, cc[k]), gs[k]);
-        }
-        if (m.end >> t & 1) {
-          open = false;
-          f2 df[4];
-          seq_state(a, q, ga.dh_final, s_seq[t], df);
+      for (int k = 0; k < 4; ++k) {
+        P[k] = mul2(P[k], dec[k]);
+        gs[k] = fma2(P[k], mul2(e, cc[k]), gs[k]);
+      }
+      if (events && (m.end >> t & 1)) {
+        open = false;
+        f2 df[4];
+        seq_state(a, q, ga.dh_final, s.seq[t], df);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) gs[k] = fma2(P[k], df[k], gs[k]);
-        }
+        for (int k = 0; k < 4; ++k) gs[k] = fma2(P[k], df[k], gs[k]);
+      }
+    };
+#pragma unroll 1
+    for (int t4 = 0; t4 < nt; t4 += 4) {
+      if (open && t4 + 4 <= nt && !((m.begin | m.end) >> t4 & 15)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) token(t4 + i, false);
+      } else {
+#pragma unroll 1
+        for (int t = t4; t < min(t4 + 4, nt); ++t) token(t, true);
       }
     }
     __syncthreads();
   }
   const int64_t at = (int64_t)chunk * p.blocks + blockIdx.x;
-  store_piece(ws.hin + (at * nw + q.warp) * kPiece, q.lane, hs);
-  store_piece(ws.gin + (at * nw + q.warp) * kPiece, q.lane, gs);
-  if (q.wn == 0 && q.sg == 0) *reinterpret_cast<f2*>(ws.total + at * K::cw + q.wt * kCh + q.cg * 2) = sum;
+  store_piece(ws.hin + (at * S::wpb + q.warp) * kPiece, q.lane, hs);
+  store_piece(ws.gin + (at * S::wpb + q.warp) * kPiece, q.lane, gs);
+  if (q.wn == 0 && q.sg == 0) *reinterpret_cast<f2*>(ws.total + at * S::cw + lane_c) = sum;
 }
 
 constexpr int kAhead = 8;  // chunks read before their use
@@ -292,233 +318,284 @@ __global__ void join_kernel(ScanArgs a, Plan p, Ws ws) {
   }
 }
 
+// Where a warp's sums go: [token * stride + channel], and its kept states.
+struct WarpMem {
+  float *q, *r, *y, *keep, *red;
+};
+struct BackRegs {
+  f2 hs[4], gs[4], dA[4];
+};
+
+// One block of tokens: forward from its kept state hs with the decays and
+// states in registers, then backward, carrying gs. kEvents: sequences may begin
+// or end in the block, or the tokens end.
+template <int W, bool kEvents>
+__device__ __forceinline__ void back_block(const ScanBwdArgs& ga, Shared<W, false>& s, const Place& q, const Marks& m,
+                                           int nt, int blk, const f2 (&A2)[4], BackRegs& g_, const WarpMem& mem) {
+  using S = Shared<W, false>;
+  constexpr int cw = S::cw, ns = S::ns, qs = W == 1 ? cw : kCh;
+  const ScanArgs& a = ga.f;
+  const int lane_c = q.wt * kCh + q.cg * 2, lane_s = q.wn * 2 * kNB + q.sg * 8;
+  f2(&hs)[4] = g_.hs;
+  f2(&gs)[4] = g_.gs;
+  f2(&dA)[4] = g_.dA;
+  float *keep = mem.keep, *red = mem.red, *sq = mem.q, *sr = mem.r, *sy = mem.y;
+  f2 dec[kBlk][4], st[kBlk][4];  // the decays, and the decayed states exp(D A) h_{t-1}
+#pragma unroll
+  for (int i = 0; i < kBlk; ++i) {
+    const int t = blk * kBlk + i;
+    if (kEvents && t >= nt) continue;
+    if (kEvents && (m.begin >> t & 1)) seq_state(a, q, a.h0, s.seq[t], hs);
+    const f2 dt = *reinterpret_cast<const f2*>(s.dt + t * cw + lane_c);
+    const f2 u = *reinterpret_cast<const f2*>(s.u + t * cw + lane_c);
+    f2 bb[4];
+    four(s.b + t * 2 * ns + lane_s, bb);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      dec[i][k] = ex2_pair(mul2(dt, A2[k]));
+      st[i][k] = mul2(dec[i][k], hs[k]);
+      hs[k] = fma2(u, bb[k], st[i][k]);
+    }
+  }
+  f2 vq[kBlk], vr[kBlk], vy[kBlk];
+  float* out = keep + (blk < S::kBlocks - 1 ? blk * kPiece : (S::kBlocks - 1) * kPiece);
+#pragma unroll
+  for (int i = kBlk - 1; i >= 0; --i) {
+    const int t = blk * kBlk + i;
+    vq[i] = vr[i] = vy[i] = 0;
+    if (kEvents && t >= nt) continue;
+    if (kEvents && (m.end >> t & 1)) seq_state(a, q, ga.dh_final, s.seq[t], gs);
+    const f2 dt = *reinterpret_cast<const f2*>(s.dt + t * cw + lane_c);
+    const f2 u = *reinterpret_cast<const f2*>(s.u + t * cw + lane_c);
+    const f2 e = *reinterpret_cast<const f2*>(s.e + t * cw + lane_c);
+    f2 bb[4], cc[4];
+    float dB[4], dC[4];
+    four(s.b + t * 2 * ns + lane_s, bb);
+    four(s.c + t * 2 * ns + lane_s, cc);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const f2 g = fma2(e, cc[k], gs[k]), h = fma2(u, bb[k], st[i][k]);
+      vq[i] = fma2(g, bb[k], vq[i]);
+      vy[i] = fma2(h, cc[k], vy[i]);
+      const f2 gh = mul2(g, st[i][k]);
+      vr[i] = fma2(gh, A2[k], vr[i]);
+      dA[k] = fma2(gh, dt, dA[k]);
+      gs[k] = mul2(dec[i][k], g);
+      float lo, hi;
+      un2(mul2(g, u), lo, hi);
+      dB[k] = lo + hi;
+      un2(mul2(e, h), lo, hi);
+      dC[k] = lo + hi;
+    }
+    if (kEvents && (m.begin >> t & 1) && ga.dh0) put_state(a, q, ga.dh0, s.seq[t], gs);
+    // dB, dC over the warp's 8 channel lanes, through memory: a value a lane
+    // (which = lane / 16 of state lane % 16)
+    *reinterpret_cast<float4*>(red + q.cg * 32 + q.sg * 4) = make_float4(dB[0], dB[1], dB[2], dB[3]);
+    *reinterpret_cast<float4*>(red + q.cg * 32 + 16 + q.sg * 4) = make_float4(dC[0], dC[1], dC[2], dC[3]);
+    __syncwarp();
+    float v = red[q.lane];
+#pragma unroll
+    for (int c = 1; c < 8; ++c) v += red[c * 32 + q.lane];
+    out[i * 32 + q.lane] = v;
+    __syncwarp();
+  }
+  // the four tokens' sums over the tile's state lanes: halve twice, a token a lane is left
+  const bool up = q.sg & 1, up2 = q.sg & 2;
+  const int t = blk * kBlk + (up ? 2 : 0) + (up2 ? 1 : 0);
+  auto join = [&](const f2 (&v)[kBlk]) {
+    const f2 v0 = add2(up ? v[2] : v[0], __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 1));
+    const f2 v1 = add2(up ? v[3] : v[1], __shfl_xor_sync(0xffffffffu, up ? v[1] : v[3], 1));
+    return add2(up2 ? v1 : v0, __shfl_xor_sync(0xffffffffu, up2 ? v0 : v1, 2));
+  };
+  *reinterpret_cast<f2*>(sq + t * qs + q.cg * 2) = join(vq);
+  *reinterpret_cast<f2*>(sr + t * qs + q.cg * 2) = join(vr);
+  *reinterpret_cast<f2*>(sy + t * qs + q.cg * 2) = join(vy);
+}
+// The rare form stays out of the other's registers.
+template <int W>
+__device__ __noinline__ void back_block_events(const ScanBwdArgs& ga, Shared<W, false>& s, const Place& q,
+                                               const Marks& m, int nt, int blk, const BackRegs& rate, BackRegs& g_,
+                                               const WarpMem& mem) {
+  back_block<W, true>(ga, s, q, m, nt, blk, rate.hs, g_, mem);
+}
+
 template <typename T, int W>
-__global__ void __launch_bounds__(128, 3) main_kernel(ScanBwdArgs ga, Plan p, Ws ws) {
-  using K = Kernel<T, W>;
-  constexpr int V = K::V, lpr = K::cw / V;
-  extern __shared__ __align__(16) float sm[];
-  __shared__ int s_seq[kPart];
+__global__ void __launch_bounds__(128, 3) main_kernel(const __grid_constant__ ScanBwdArgs ga, Plan p, Ws ws) {
+  using S = Shared<W, false>;
+  constexpr int cw = S::cw, ns = S::ns, wpb = S::wpb;
+  constexpr int kGroups = cw / 4, dr = S::threads / kGroups;
+  extern __shared__ __align__(16) unsigned char raw[];
+  S& s = *reinterpret_cast<S*>(raw);
   const ScanArgs& a = ga.f;
   const Place q = place<W>(a, p.per_head);
-  const Shared s = shared_of<W>(sm, q);
-  constexpr int nw = K::nw;
   const int chunk = blockIdx.y;
   const int64_t chat = (int64_t)chunk * p.blocks + blockIdx.x;
-  f2 A2[4], h_in[4], gs[4], dA[4] = {0, 0, 0, 0};
-  rates(a, q, A2);
-  load_piece(ws.hin + (chat * nw + q.warp) * kPiece, q.lane, h_in);
-  load_piece(ws.gin + (chat * nw + q.warp) * kPiece, q.lane, gs);
-  // channel sums of the thread's vectors: their channels are the same in every turn
-  constexpr int ystride = W == 1 ? K::cw : kCh;
-  const int vc = q.tid % lpr * V, vn = a.d - q.c0 - vc;
-  float sD[V], sbias[V];
+  f2 A2[4];
+  BackRegs regs;
 #pragma unroll
-  for (int j = 0; j < V; ++j) sD[j] = sbias[j] = 0.f;
+  for (int k = 0; k < 4; ++k) regs.dA[k] = 0;
+  rates(a, q, A2);
+  load_piece(ws.gin + (chat * wpb + q.warp) * kPiece, q.lane, regs.gs);
+  const int vc = q.tid % kGroups * 4, vn = a.d - q.c0 - vc;
+  float bias[4], sD[4] = {0.f, 0.f, 0.f, 0.f}, sbias[4] = {0.f, 0.f, 0.f, 0.f};
+  float dskip[4];
+  four_of(a.dt_bias ? a.dt_bias + q.ch0 + vc : nullptr, vn, bias);
+  four_of(a.D ? a.D + q.ch0 + vc : nullptr, vn, dskip);
   const float ln2 = 0.6931471805599453f;
+  const int lane_c = q.wt * kCh + q.cg * 2, lane_s = q.wn * 2 * kNB + q.sg * 8;
+  WarpMem mem;
+  mem.q = s.q + (W == 1 ? q.wt * kCh : q.warp * kPart * kCh);
+  mem.r = W == 1 ? s.u + q.wt * kCh : s.ry + q.warp * kPart * kCh;
+  mem.y = W == 1 ? s.e + q.wt * kCh : s.ry + (wpb + q.warp) * kPart * kCh;
+  mem.keep = s.keep + q.warp * ((S::kBlocks - 1) * kPiece + kBlk * 32);
+  mem.red = s.red + q.warp * 256;
 
   const int part0 = chunk * p.chunk, part1 = min(p.parts, part0 + p.chunk);
   for (int part = part1 - 1; part >= part0; --part) {
-    const int tb = part * kPart, nt = min(kPart, a.T - tb);
+    const int tb = part * kPart, nt = min(kPart, a.T - tb), last = (nt - 1) / kBlk;
     int seq;
     const Marks m = marks(a, q, tb, nt, &seq);
-    if (q.warp == 0) s_seq[q.lane] = seq;
-    K::stage(a, ga.dy, q, tb, m.live, s.dt, s.u, s.e, s.b, s.c);
+    if (q.warp == 0) s.seq[q.lane] = seq;
+    stage<T>(a, ga.dy, q, tb, m.live, bias, s);
     // the state before the part
-    f2 hs[4];
-    if (part == part0) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) hs[k] = h_in[k];
-    } else {
+    f2(&hs)[4] = regs.hs;
+    load_piece(ws.hin + (chat * wpb + q.warp) * kPiece, q.lane, hs);
+    if (part > part0) {
       const int64_t at = (int64_t)part * p.blocks + blockIdx.x;
-      load_piece(ws.start + (at * nw + q.warp) * kPiece, q.lane, hs);
+      f2 local[4];
+      load_piece(ws.start + (at * wpb + q.warp) * kPiece, q.lane, local);
       const TokenAt here = token_at(a.seqs, q.b, a.T, tb, a.status);
-      if (here.live && here.lo < part0 * kPart) {  // its sequence entered the chunk from before
-        const f2 sum = *reinterpret_cast<const f2*>(ws.sums + at * K::cw + q.wt * kCh + q.cg * 2);
+      const bool entered = here.live && here.lo < part0 * kPart;  // its sequence was there before the chunk
+      const f2 sum = *reinterpret_cast<const f2*>(ws.sums + at * cw + lane_c);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) hs[k] = fma2(ex2_pair(mul2(sum, A2[k])), h_in[k], hs[k]);
-      }
+      for (int k = 0; k < 4; ++k) hs[k] = entered ? fma2(ex2_pair(mul2(sum, A2[k])), hs[k], local[k]) : local[k];
     }
     __syncthreads();
-    const int lane_o = q.wt * kCh + q.cg * 2, lane_s = q.wn * 2 * kNB + q.sg * 8;
-    // forward, keeping the state before every block
-    for (int t = 0; t < nt; ++t) {
-      if (t % kBlk == 0) store_piece(s.keep + t / kBlk * kPiece, q.lane, hs);
-      if (m.begin >> t & 1) seq_state(a, q, a.h0, s_seq[t], hs);
-      const f2 dt = *reinterpret_cast<const f2*>(s.dt + t * K::cw + lane_o);
-      const f2 u = *reinterpret_cast<const f2*>(s.u + t * K::cw + lane_o);
-      f2 bb[4], cc[4], y = 0;
-      four(s.b + t * 2 * K::states + lane_s, bb);
+    // whether block blk is whole and no sequence begins or ends in it
+    auto plain = [&](int blk) {
+      return blk * kBlk + kBlk <= nt && !((m.begin | m.end) >> (blk * kBlk) & ((1u << kBlk) - 1));
+    };
+    // forward, keeping the state before every block; hs ends before the last one
+    auto step = [&](int t, bool events) {
+      if (events && (m.begin >> t & 1)) seq_state(a, q, a.h0, s.seq[t], hs);
+      const f2 dt = *reinterpret_cast<const f2*>(s.dt + t * cw + lane_c);
+      const f2 u = *reinterpret_cast<const f2*>(s.u + t * cw + lane_c);
+      f2 bb[4];
+      four(s.b + t * 2 * ns + lane_s, bb);
 #pragma unroll
       for (int k = 0; k < 4; ++k) hs[k] = fma2(ex2_pair(mul2(dt, A2[k])), hs[k], mul2(u, bb[k]));
-      if (a.z.p) {
-        four(s.c + t * 2 * K::states + lane_s, cc);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) y = fma2(hs[k], cc[k], y);
-        float y0, y1;
-        un2(y, y0, y1);
-        const bool up = q.sg & 1;
-        const float o = __shfl_xor_sync(0xffffffffu, up ? y0 : y1, 1);
-        float v = (up ? y1 : y0) + o;
-        v += __shfl_xor_sync(0xffffffffu, v, 2);
-        if (q.sg < 2) s.y[t * ystride + q.cg * 2 + up] = v;
-      }
-    }
-    const float* ysm = s.y - (W == 1 ? q.wt * kCh : q.warp * kPart * kCh);
-    const float* rsm = s.r - (W == 1 ? q.wt * kCh : q.warp * kPart * kCh);
-    // the sum over a tile's warps of y or r, at a token and channel of the block
-    auto joined = [&](const float* base, int row, int c) {
-      if (W == 1) return base[row * K::cw + c];
-      float v = 0.f;
-#pragma unroll
-      for (int w = 0; w < W; ++w) v += base[((c / kCh * W + w) * kPart + row) * kCh + c % kCh];
-      return v;
     };
-    if (a.z.p) {  // dz = dy y silu'(z)
-      __syncthreads();
-      for (int i = q.tid; i < kPart * lpr; i += blockDim.x) {
-        const int row = i / lpr;
-        if (!(m.live >> row & 1) || vn <= 0) continue;
-        const int64_t t = tb + row;
-        float x[V], z[V], g[V];
-        unpack<T>(load_vec(static_cast<const T*>(a.x.p) + q.b * a.x.sb + q.h * a.x.sh + q.c0 + vc + t * a.x.st, vn, a.wide), x);
-        unpack<T>(load_vec(static_cast<const T*>(a.z.p) + q.b * a.z.sb + q.h * a.z.sh + q.c0 + vc + t * a.z.st, vn, a.wide), z);
-        unpack<T>(load_vec(static_cast<const T*>(ga.dy.p) + q.b * ga.dy.sb + q.h * ga.dy.sh + q.c0 + vc + t * ga.dy.st, vn, a.wide), g);
+#pragma unroll 1
+    for (int blk = 0; blk < last; ++blk) {
+      store_piece(mem.keep + blk * kPiece, q.lane, hs);
+      if (plain(blk)) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float dskip = a.D && j < vn ? a.D[q.ch0 + vc + j] : 0.f;
-          g[j] *= fmaf(dskip, x[j], joined(ysm, row, vc + j)) * dsilu_f(z[j]);
-        }
-        store_vec<T>(static_cast<T*>(ga.dz.p) + q.b * ga.dz.sb + q.h * ga.dz.sh + q.c0 + vc + t * ga.dz.st, vn, a.wide, g);
+        for (int i = 0; i < kBlk; ++i) step(blk * kBlk + i, false);
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < kBlk; ++i) step(blk * kBlk + i, true);
       }
-      __syncthreads();
     }
     // backward, block by block
-    for (int blk = (nt - 1) / kBlk; blk >= 0; --blk) {
-      f2 dec[kBlk][4], st[kBlk][4];  // the decays, and the decayed states exp(D A) h_{t-1}
-      f2 h[4];
-      load_piece(s.keep + blk * kPiece, q.lane, h);
-#pragma unroll
-      for (int i = 0; i < kBlk; ++i) {
-        const int t = blk * kBlk + i;
-        if (t < nt) {
-          if (m.begin >> t & 1) seq_state(a, q, a.h0, s_seq[t], h);
-          const f2 dt = *reinterpret_cast<const f2*>(s.dt + t * K::cw + lane_o);
-          const f2 u = *reinterpret_cast<const f2*>(s.u + t * K::cw + lane_o);
-          f2 bb[4];
-          four(s.b + t * 2 * K::states + lane_s, bb);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            dec[i][k] = ex2_pair(mul2(dt, A2[k]));
-            st[i][k] = mul2(dec[i][k], h[k]);
-            h[k] = fma2(u, bb[k], st[i][k]);
-          }
-        }
+#pragma unroll 1
+    for (int blk = last; blk >= 0; --blk) {
+      if (blk < last) {
+        load_piece(mem.keep + blk * kPiece, q.lane, hs);
+        __syncwarp();  // read by every lane before the block's dB, dC go there
       }
-      __syncwarp();  // keep[blk] is read by every lane before the block's dB, dC go there
+      if (plain(blk)) {
+        back_block<W, false>(ga, s, q, m, nt, blk, A2, regs, mem);
+      } else {
+        BackRegs rate, copy = regs;
 #pragma unroll
-      for (int i = kBlk - 1; i >= 0; --i) {
-        const int t = blk * kBlk + i;
-        if (t < nt) {
-          if (m.end >> t & 1) seq_state(a, q, ga.dh_final, s_seq[t], gs);
-          const f2 dt = *reinterpret_cast<const f2*>(s.dt + t * K::cw + lane_o);
-          const f2 u = *reinterpret_cast<const f2*>(s.u + t * K::cw + lane_o);
-          const f2 e = *reinterpret_cast<const f2*>(s.e + t * K::cw + lane_o);
-          f2 bb[4], cc[4], sq = 0, sr = 0, dB[4], dC[4];
-          four(s.b + t * 2 * K::states + lane_s, bb);
-          four(s.c + t * 2 * K::states + lane_s, cc);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const f2 g = fma2(e, cc[k], gs[k]);
-            sq = fma2(g, bb[k], sq);
-            dB[k] = mul2(g, u);
-            dC[k] = mul2(e, fma2(u, bb[k], st[i][k]));
-            const f2 gh = mul2(g, st[i][k]);
-            sr = fma2(gh, A2[k], sr);
-            dA[k] = fma2(gh, dt, dA[k]);
-            gs[k] = mul2(dec[i][k], g);
-          }
-          if ((m.begin >> t & 1) && ga.dh0) put_state(a, q, ga.dh0, s_seq[t], gs);
-          // <g, B> and <g, A exp(DA) h> of two channels over the tile's four state lanes
-          float v[4];
-          un2(sq, v[0], v[1]);
-          un2(sr, v[2], v[3]);
-          const bool up = q.sg & 1, up2 = q.sg & 2;
-          const float p0 = __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 1);
-          const float p1 = __shfl_xor_sync(0xffffffffu, up ? v[1] : v[3], 1);
-          const float w0 = (up ? v[2] : v[0]) + p0, w1 = (up ? v[3] : v[1]) + p1;
-          const float r0 = __shfl_xor_sync(0xffffffffu, up2 ? w0 : w1, 2);
-          const float w = (up2 ? w1 : w0) + r0;
-          (up ? s.r : s.y)[t * ystride + q.cg * 2 + (up2 ? 1 : 0)] = up ? w * ln2 : w;
-          // dB, dC of four states over the warp's 16 channels: pairs, then 8 lanes
-          float f[8];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float lo, hi;
-            un2(dB[k], lo, hi);
-            f[k] = lo + hi;
-            un2(dC[k], lo, hi);
-            f[4 + k] = lo + hi;
-          }
-          const bool b0 = q.cg & 1, b1 = q.cg & 2, b2 = q.cg & 4;
-          float f4[4], f2_[2];
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            f4[k] = (b0 ? f[4 + k] : f[k]) + __shfl_xor_sync(0xffffffffu, b0 ? f[k] : f[4 + k], 4);
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            f2_[k] = (b1 ? f4[2 + k] : f4[k]) + __shfl_xor_sync(0xffffffffu, b1 ? f4[k] : f4[2 + k], 8);
-          const float fin = (b2 ? f2_[1] : f2_[0]) + __shfl_xor_sync(0xffffffffu, b2 ? f2_[0] : f2_[1], 16);
-          // dB (b0 = 0) or dC of state 4 sg + 2 b1 + b2: into the block's used-up kept states
-          s.keep[blk * kPiece + i * 32 + (b0 ? 16 : 0) + q.sg * 4 + (b1 ? 2 : 0) + (b2 ? 1 : 0)] = fin;
-        }
+        for (int k = 0; k < 4; ++k) rate.hs[k] = A2[k];
+        const Place qc = q;
+        const Marks mc = m;
+        const WarpMem memc = mem;
+        back_block_events<W>(ga, s, qc, mc, nt, blk, rate, copy, memc);
+        regs = copy;
       }
     }
     __syncthreads();
-    // dx, ddt, and the channels' sums
-    for (int i = q.tid; i < kPart * lpr; i += blockDim.x) {
-      const int row = i / lpr;
-      if (!(m.live >> row & 1) || vn <= 0) continue;
-      const int64_t t = tb + row;
-      float x[V], raw[V], dx[V], dd[V];
-      unpack<T>(load_vec(static_cast<const T*>(a.x.p) + q.b * a.x.sb + q.h * a.x.sh + q.c0 + vc + t * a.x.st, vn, a.wide), x);
-      unpack<T>(load_vec(static_cast<const T*>(a.dt.p) + q.b * a.dt.sb + q.h * a.dt.sh + q.c0 + vc + t * a.dt.st, vn, a.wide), raw);
+    // dx, ddt, dz, and the channels' sums
+    const float* q0 = s.q;
+    const float* r0 = W == 1 ? s.u : s.ry;
+    const float* y0 = W == 1 ? s.e : s.ry + wpb * kPart * kCh;
+    auto finish = [&](auto whole) {
+      constexpr bool kWhole = decltype(whole)::value;
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float dskip = a.D && j < vn ? a.D[q.ch0 + vc + j] : 0.f;
-        const float bias = a.dt_bias && j < vn ? a.dt_bias[q.ch0 + vc + j] : 0.f;
-        const int o = row * K::cw + vc + j;
-        const float gb = joined(ysm, row, vc + j), ga_ = joined(rsm, row, vc + j), e = s.e[o];
-        dx[j] = fmaf(dskip, e, s.dt[o] * gb);
-        dd[j] = fmaf(x[j], gb, ga_);
-        if (a.softplus) dd[j] *= sigmoid_f(raw[j] + bias);
-        sD[j] = fmaf(e, x[j], sD[j]);
-        sbias[j] += dd[j];
+      for (int r = 0; r < kPart; r += dr) {
+        const int row = r + q.tid / kGroups;
+        if (kPart % dr != 0 && row >= kPart) break;
+        if (!kWhole && (!(m.live >> row & 1) || vn <= 0)) continue;
+        const int64_t t = tb + row;
+        auto joined = [&](const float* base, float (&v)[4]) {  // over a tile's warps
+          const float* at = W == 1 ? base + row * cw + vc : base + (vc / kCh * W * kPart + row) * kCh + vc % kCh;
+          float4 x = *reinterpret_cast<const float4*>(at);
+#pragma unroll
+          for (int w = 1; w < W; ++w) {
+            const float4 o = *reinterpret_cast<const float4*>(at + w * kPart * kCh);
+            x.x += o.x, x.y += o.y, x.z += o.z, x.w += o.w;
+          }
+          v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+        };
+        float x[4], w[4], e[4], z[4], gb[4], gr[4], y[4], o[4];
+        read_row<kWhole, T, 4>(static_cast<const T*>(a.x.p) + q.b * a.x.sb + q.h * a.x.sh + q.c0 + vc + t * a.x.st, vn, a.wide, x);
+        read_row<kWhole, T, 4>(static_cast<const T*>(a.dt.p) + q.b * a.dt.sb + q.h * a.dt.sh + q.c0 + vc + t * a.dt.st, vn, a.wide, w);
+        read_row<kWhole, T, 4>(static_cast<const T*>(ga.dy.p) + q.b * ga.dy.sb + q.h * ga.dy.sh + q.c0 + vc + t * ga.dy.st, vn, a.wide, e);
+        if (a.z.p)
+          read_row<kWhole, T, 4>(static_cast<const T*>(a.z.p) + q.b * a.z.sb + q.h * a.z.sh + q.c0 + vc + t * a.z.st, vn, a.wide, z);
+        joined(q0, gb);
+        joined(r0, gr);
+        if (a.z.p) {
+          joined(y0, y);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            o[j] = e[j] * fmaf(dskip[j], x[j], y[j]) * dsilu_f(z[j]);
+            e[j] *= silu_f(z[j]);
+          }
+          write_row<kWhole, T, 4>(static_cast<T*>(ga.dz.p) + q.b * ga.dz.sb + q.h * ga.dz.sh + q.c0 + vc + t * ga.dz.st, vn, a.wide, o);
+        }
+        const float4 d = *reinterpret_cast<const float4*>(s.dt + row * cw + vc);
+        o[0] = fmaf(dskip[0], e[0], d.x * gb[0]), o[1] = fmaf(dskip[1], e[1], d.y * gb[1]);
+        o[2] = fmaf(dskip[2], e[2], d.z * gb[2]), o[3] = fmaf(dskip[3], e[3], d.w * gb[3]);
+        write_row<kWhole, T, 4>(static_cast<T*>(ga.dx.p) + q.b * ga.dx.sb + q.h * ga.dx.sh + q.c0 + vc + t * ga.dx.st, vn, a.wide, o);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          o[j] = fmaf(x[j], gb[j], gr[j] * ln2);  // the rates are in powers of two
+          if (a.softplus) o[j] *= sigmoid_f(w[j] + bias[j]);
+          sD[j] = fmaf(e[j], x[j], sD[j]);
+          sbias[j] += o[j];
+        }
+        write_row<kWhole, T, 4>(static_cast<T*>(ga.ddt.p) + q.b * ga.ddt.sb + q.h * ga.ddt.sh + q.c0 + vc + t * ga.ddt.st, vn, a.wide, o);
       }
-      store_vec<T>(static_cast<T*>(ga.dx.p) + q.b * ga.dx.sb + q.h * ga.dx.sh + q.c0 + vc + t * ga.dx.st, vn, a.wide, dx);
-      store_vec<T>(static_cast<T*>(ga.ddt.p) + q.b * ga.ddt.sb + q.h * ga.ddt.sh + q.c0 + vc + t * ga.ddt.st, vn, a.wide, dd);
-    }
+    };
+    if (is_whole<S>(a, q, m.live)) finish(std::true_type());
+    else finish(std::false_type());
     // dB, dC over the block's channel tiles, to the block's slab
-    const float* keep0 = s.keep - q.warp * (kPart / kBlk) * kPiece;
-    for (int i = q.tid; i < nt * 2 * K::states; i += blockDim.x) {
-      const int t = i / (2 * K::states), which = i / K::states % 2, n = i % K::states;
+    for (int i = q.tid; i < nt * 2 * ns; i += S::threads) {
+      const int t = i / (2 * ns), which = i / ns % 2, n = i % ns;
       float v = 0.f;
-      for (int w = 0; w < K::tpb; ++w)
-        v += keep0[((w * W + n / kNB) * (kPart / kBlk) + t / kBlk) * kPiece + t % kBlk * 32 + which * 16 + n % kNB];
-      ws.dBC[(((int64_t)blockIdx.x * a.T + tb + t) * 2 + which) * K::states + n] = v;
+#pragma unroll
+      for (int w = 0; w < S::tpb; ++w)
+        v += s.keep[(w * W + n / kNB) * ((S::kBlocks - 1) * kPiece + kBlk * 32) + t / kBlk * kPiece + t % kBlk * 32 +
+                    which * 16 + n % kNB];
+      ws.dBC[(((int64_t)blockIdx.x * a.T + tb + t) * 2 + which) * ns + n] = v;
     }
     __syncthreads();
   }
-  store_piece(ws.dA + (chat * nw + q.warp) * kPiece, q.lane, dA);
-  // the threads' channel sums: rows of threads that share a vector, in order
-  for (int w = 0; w < 2; ++w) {
-    float* sh = s.dt;  // [threads / lpr][cw]: within the three staged tensors
+  store_piece(ws.dA + (chat * wpb + q.warp) * kPiece, q.lane, regs.dA);
+  // the threads' channel sums: rows of threads that share channels, in order
 #pragma unroll
-    for (int j = 0; j < V; ++j) sh[q.tid / lpr * K::cw + vc + j] = w ? sbias[j] : sD[j];
+  for (int w = 0; w < 2; ++w) {
+    float* sh = s.dt;  // [dr][cw]
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sh[q.tid / kGroups * cw + vc + j] = w ? sbias[j] : sD[j];
     __syncthreads();
-    for (int c = q.tid; c < K::cw; c += blockDim.x) {
+    for (int c = q.tid; c < cw; c += S::threads) {
       float v = 0.f;
-      for (int i = 0; i < (int)blockDim.x / lpr; ++i) v += sh[i * K::cw + c];
-      ws.dD[(chat * 2 + w) * K::cw + c] = v;
+      for (int i = 0; i < dr; ++i) v += sh[i * cw + c];
+      ws.dD[(chat * 2 + w) * cw + c] = v;
     }
     __syncthreads();
   }
@@ -586,15 +663,17 @@ cudaError_t bwd(const ScanBwdArgs& ga, cudaStream_t s) {
   if (a.T > 0) {
     e = for_warps(p.warps, [&](auto w) {
       constexpr int W = decltype(w)::value;
-      const size_t sh = smem_bytes(p, false);
-      const cudaError_t r =
-          cudaFuncSetAttribute(main_kernel<T, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sh);
+      using First = Shared<W, true>;
+      using All = Shared<W, false>;
+      cudaError_t r = cudaFuncSetAttribute(pre_kernel<T, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(First));
+      if (r != cudaSuccess) return r;
+      r = cudaFuncSetAttribute(main_kernel<T, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(All));
       if (r != cudaSuccess) return r;
       const dim3 grid((unsigned)p.blocks, p.chunks);
-      pre_kernel<T, W><<<grid, 32 * nw, smem_bytes(p, true), s>>>(ga, p, ws);
+      pre_kernel<T, W><<<grid, 32 * nw, sizeof(First), s>>>(ga, p, ws);
       const int64_t n = p.blocks * nw * kPiece;
       join_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(a, p, ws);
-      main_kernel<T, W><<<grid, 32 * nw, sh, s>>>(ga, p, ws);
+      main_kernel<T, W><<<grid, 32 * nw, sizeof(All), s>>>(ga, p, ws);
       const int64_t bc = (int64_t)a.B * a.G * a.T * 2 * p.warps * kNB;
       put_bc_kernel<T><<<(unsigned)((bc + 255) / 256), 256, 0, s>>>(ga, p, ws.dBC);
       return cudaGetLastError();
