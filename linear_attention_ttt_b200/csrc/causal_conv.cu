@@ -63,84 +63,154 @@ __device__ __forceinline__ bool next_piece(const Seqs& q, const Run& r, int T, i
   return false;
 }
 
-// win[i] = the input K-1-i tokens before t (i < K-1), from the sequence or the
-// state before it.
-template <typename T, int K, int V>
-__device__ __forceinline__ void fill_window(const T* x, int64_t st, const TokView& state0, const Run& r,
-                                            const Piece& p, int t, bool wide, float (&win)[K][V]) {
-#pragma unroll
-  for (int i = 0; i < K - 1; ++i) {
-    const int src = t - (K - 1) + i;
-    if (src >= p.lo) {
-      load_row<T, V>(x + src * st, r.n, wide, win[i]);
-    } else if (state0.p) {
-      const T* s0 = static_cast<const T*>(state0.p) + p.seq * state0.sb + r.h * state0.sh + r.c;
-      load_row<T, V>(s0 + (int64_t)(K - 1 + src - p.lo) * state0.st, r.n, wide, win[i]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < V; ++j) win[i][j] = 0.f;
+// Four channels of a token row as they lie in memory, and as two fp32 pairs.
+constexpr int kV = 4;
+template <typename T>
+struct Raw {
+  using type = uint2;
+};
+template <>
+struct Raw<float> {
+  using type = uint4;
+};
+// kWhole: all four exist and are aligned (see read_row).
+template <bool kWhole, typename T>
+__device__ __forceinline__ typename Raw<T>::type raw_row(const T* p, int n, bool wide) {
+  if constexpr (kWhole) {
+    return *reinterpret_cast<const typename Raw<T>::type*>(p);
+  } else {
+    float f[kV];
+    load_row<T, kV>(p, n, wide, f);
+    if constexpr (sizeof(T) == 4) {
+      return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    } else {  // exact: the values came from bf16
+      return make_uint2(__float_as_uint(f[0]) >> 16 | (__float_as_uint(f[1]) & 0xffff0000u),
+                        __float_as_uint(f[2]) >> 16 | (__float_as_uint(f[3]) & 0xffff0000u));
     }
   }
 }
+__device__ __forceinline__ void pairs_of(uint4 r, f2 (&v)[2]) {
+  v[0] = mk2(__uint_as_float(r.x), __uint_as_float(r.y));
+  v[1] = mk2(__uint_as_float(r.z), __uint_as_float(r.w));
+}
+__device__ __forceinline__ void pairs_of(uint2 r, f2 (&v)[2]) {
+  v[0] = mk2(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u));
+  v[1] = mk2(__uint_as_float(r.y << 16), __uint_as_float(r.y & 0xffff0000u));
+}
+__device__ __forceinline__ void floats_of(const f2 (&v)[2], float (&f)[kV]) {
+  un2(v[0], f[0], f[1]);
+  un2(v[1], f[2], f[3]);
+}
+__device__ __forceinline__ void pairs_of(const float (&f)[kV], f2 (&v)[2]) {
+  v[0] = mk2(f[0], f[1]);
+  v[1] = mk2(f[2], f[3]);
+}
 
-template <int K, int V>
-__device__ __forceinline__ void load_taps(const float* w, const float* bias, int d, const Run& r,
-                                          float (&taps)[K][V], float (&b)[V]) {
+// win[i] = the input K-1-i tokens before t (i < K-1), from the sequence or the
+// state before it.
+template <typename T, int K>
+__device__ __forceinline__ void fill_window(const T* x, int64_t st, const TokView& state0, const Run& r,
+                                            const Piece& p, int t, bool wide, f2 (&win)[K][2]) {
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int64_t c = (int64_t)r.h * d + r.c + j;
-    const bool in = j < r.n;
-    b[j] = in && bias ? bias[c] : 0.f;
-#pragma unroll
-    for (int i = 0; i < K; ++i) taps[i][j] = in ? w[c * K + i] : 0.f;
+  for (int i = 0; i < K - 1; ++i) {
+    const int src = t - (K - 1) + i;
+    float f[kV] = {0.f, 0.f, 0.f, 0.f};
+    if (src >= p.lo) {
+      load_row<T, kV>(x + src * st, r.n, wide, f);
+    } else if (state0.p) {
+      const T* s0 = static_cast<const T*>(state0.p) + p.seq * state0.sb + r.h * state0.sh + r.c;
+      load_row<T, kV>(s0 + (int64_t)(K - 1 + src - p.lo) * state0.st, r.n, wide, f);
+    }
+    pairs_of(f, win[i]);
   }
 }
 
-constexpr int kBatch = 4;  // rows loaded ahead of their use
+template <int K>
+__device__ __forceinline__ void load_taps(const float* w, const float* bias, int d, const Run& r, f2 (&taps)[K][2],
+                                          f2 (&b)[2]) {
+  float f[kV], g[K][kV];
+#pragma unroll
+  for (int j = 0; j < kV; ++j) {
+    const int64_t c = (int64_t)r.h * d + r.c + j;
+    const bool in = j < r.n;
+    f[j] = in && bias ? bias[c] : 0.f;
+#pragma unroll
+    for (int i = 0; i < K; ++i) g[i][j] = in ? w[c * K + i] : 0.f;
+  }
+  pairs_of(f, b);
+#pragma unroll
+  for (int i = 0; i < K; ++i) pairs_of(g[i], taps[i]);
+}
+template <int K>
+__device__ __forceinline__ void shift(f2 (&win)[K][2]) {
+#pragma unroll
+  for (int k = 0; k < K - 1; ++k) win[k][0] = win[k + 1][0], win[k][1] = win[k + 1][1];
+}
+template <int K>
+__device__ __forceinline__ void convolve(const f2 (&taps)[K][2], const f2 (&win)[K][2], const f2 (&bias)[2],
+                                         float (&y)[kV]) {
+  f2 v[2] = {bias[0], bias[1]};
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    v[0] = fma2(taps[k][0], win[k][0], v[0]);
+    v[1] = fma2(taps[k][1], win[k][1], v[1]);
+  }
+  floats_of(v, y);
+}
 
-template <typename T, int K>
-__global__ void __launch_bounds__(kThreads) conv_fwd_kernel(ConvArgs a, int len) {
-  constexpr int V = Vec<T>::n;
-  const Run r = run_of<V>((int64_t)blockIdx.x * kThreads + threadIdx.x, a.B, a.H, a.T, a.d, len);
-  if (!r.live) return;
-  float taps[K][V], bias[V];
-  load_taps<K, V>(a.w, a.bias, a.d, r, taps, bias);
+constexpr int kBatch = 8;  // rows in flight a thread
+
+template <typename T, int K, bool kWhole>
+__device__ __forceinline__ void conv_run(const ConvArgs& a, const Run& r) {
+  f2 taps[K][2], bias[2];
+  load_taps<K>(a.w, a.bias, a.d, r, taps, bias);
   const T* x = static_cast<const T*>(a.x.p) + r.b * a.x.sb + r.h * a.x.sh + r.c;
   T* out = static_cast<T*>(a.out.p) + r.b * a.out.sb + r.h * a.out.sh + r.c;
   Piece p;
   if (!first_piece(a.seqs, r, a.T, a.status, &p)) return;
   do {
     const int t0 = max(p.lo, r.r0), t1 = min(p.hi, r.r1);
-    float win[K][V];
-    fill_window<T, K, V>(x, a.x.st, a.state0, r, p, t0, a.wide, win);
-    for (int tb = t0; tb < t1; tb += kBatch) {
-      Vec<T> in[kBatch];
+    f2 win[K][2];
+    fill_window<T, K>(x, a.x.st, a.state0, r, p, t0, a.wide, win);
+    auto row = [&](int t, typename Raw<T>::type in) {
+      float y[kV];
+      pairs_of(in, win[K - 1]);
+      convolve<K>(taps, win, bias, y);
+      if (a.silu) {
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        if (tb + i < t1) in[i] = load_vec(x + (tb + i) * a.x.st, r.n, a.wide);
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        if (tb + i >= t1) break;
-        unpack<T>(in[i], win[K - 1]);
-        float y[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          y[j] = bias[j];
-#pragma unroll
-          for (int k = 0; k < K; ++k) y[j] = fmaf(taps[k][j], win[k][j], y[j]);
-          if (a.silu) y[j] = silu_f(y[j]);
-#pragma unroll
-          for (int k = 0; k < K - 1; ++k) win[k][j] = win[k + 1][j];
-        }
-        store_vec<T>(out + (tb + i) * a.out.st, r.n, a.wide, y);
+        for (int j = 0; j < kV; ++j) y[j] = silu_f(y[j]);
       }
+      write_row<kWhole, T, kV>(out + t * a.out.st, r.n, a.wide, y);
+      shift<K>(win);
+    };
+    int t = t0;
+    for (; t + kBatch <= t1; t += kBatch) {
+      typename Raw<T>::type in[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) in[i] = raw_row<kWhole, T>(x + (t + i) * a.x.st, r.n, a.wide);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) row(t + i, in[i]);
     }
+#pragma unroll 1
+    for (; t < t1; ++t) row(t, raw_row<kWhole, T>(x + t * a.x.st, r.n, a.wide));
     if (a.fin.p && t1 == p.hi) {
       T* f = static_cast<T*>(a.fin.p) + p.seq * a.fin.sb + r.h * a.fin.sh + r.c;
 #pragma unroll
-      for (int k = 0; k < K - 1; ++k) store_vec<T>(f + k * a.fin.st, r.n, a.wide, win[k]);
+      for (int k = 0; k < K - 1; ++k) {
+        float v[kV];
+        floats_of(win[k], v);
+        store_row<T, kV>(f + k * a.fin.st, r.n, a.wide, v);
+      }
     }
   } while (next_piece(a.seqs, r, a.T, a.status, &p));
+}
+
+template <typename T, int K>
+__global__ void __launch_bounds__(kThreads) conv_fwd_kernel(const __grid_constant__ ConvArgs a, int len) {
+  const Run r = run_of<kV>((int64_t)blockIdx.x * kThreads + threadIdx.x, a.B, a.H, a.T, a.d, len);
+  if (!r.live) return;
+  if (a.wide && r.n >= kV) conv_run<T, K, true>(a, r);
+  else conv_run<T, K, false>(a, r);
 }
 
 // dst[i] (dst may be null) = src[i] (zeros where src is null) for every sequence
@@ -175,21 +245,13 @@ cudaError_t copy_empty(const Seqs& q, int T_, int H, int d, int K, const TokView
 // needs dp up to s+K-1, and dp is computed again there rather than exchanged.
 // dp of tokens behind the sequence is zero. The run's shares of dweight and
 // dbias go to ws[run][K+1][channels].
-constexpr int kBwdV = 4;
-template <typename T, int K>
-__global__ void __launch_bounds__(kThreads) conv_bwd_kernel(ConvBwdArgs a, int len, int64_t cols) {
-  constexpr int V = kBwdV;
-  const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const Run r = run_of<V>(id, a.B, a.H, a.T, a.d, len);
-  if (!r.live) return;
-  float taps[K][V], bias[V], dw[K][V], db[V];
-  load_taps<K, V>(a.w, a.bias, a.d, r, taps, bias);
+constexpr int kBwdBatch = 4;
+template <typename T, int K, bool kWhole>
+__device__ __forceinline__ void conv_back(const ConvBwdArgs& a, const Run& r, float* dst, int64_t cols) {
+  f2 taps[K][2], bias[2], dw[K][2], db[2] = {0, 0};
+  load_taps<K>(a.w, a.bias, a.d, r, taps, bias);
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    db[j] = 0.f;
-#pragma unroll
-    for (int k = 0; k < K; ++k) dw[k][j] = 0.f;
-  }
+  for (int k = 0; k < K; ++k) dw[k][0] = dw[k][1] = 0;
   const T* x = static_cast<const T*>(a.x.p) + r.b * a.x.sb + r.h * a.x.sh + r.c;
   const T* dy = static_cast<const T*>(a.dy.p) + r.b * a.dy.sb + r.h * a.dy.sh + r.c;
   T* dx = static_cast<T*>(a.dx.p) + r.b * a.dx.sb + r.h * a.dx.sh + r.c;
@@ -197,74 +259,115 @@ __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(ConvBwdArgs a, int l
   if (first_piece(a.seqs, r, a.T, a.status, &p)) do {
     const int t0 = max(p.lo, r.r0), t1 = min(p.hi, r.r1);
     const int first = t0 == p.lo ? p.lo - (K - 1) : t0;  // the state's inputs belong to the first run
-    float win[K][V], dp[K][V];
-    fill_window<T, K, V>(x, a.x.st, a.state0, r, p, t0, a.wide, win);
+    f2 win[K][2], dp[K][2];  // dp[k] = dp of token t-K+1+k
+    fill_window<T, K>(x, a.x.st, a.state0, r, p, t0, a.wide, win);
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+    for (int k = 0; k < K; ++k) dp[k][0] = dp[k][1] = 0;
+    // dp of token t from its rows; own: the token is the run's
+    auto token = [&](typename Raw<T>::type xr, typename Raw<T>::type gr, bool own) {
+      pairs_of(xr, win[K - 1]);
+      pairs_of(gr, dp[K - 1]);
+      if (a.silu) {
+        float y[kV];
+        convolve<K>(taps, win, bias, y);
 #pragma unroll
-      for (int j = 0; j < V; ++j) dp[k][j] = 0.f;
-    for (int t = t0; t < t1 + K - 1; ++t) {
-      // dp[k] = dp of token t-K+1+k
+        for (int j = 0; j < kV; ++j) y[j] = dsilu_f(y[j]);
+        f2 v[2];
+        pairs_of(y, v);
+        dp[K - 1][0] = mul2(dp[K - 1][0], v[0]);
+        dp[K - 1][1] = mul2(dp[K - 1][1], v[1]);
+      }
+      if (own) {
 #pragma unroll
-      for (int k = 0; k < K - 1; ++k)
+        for (int i = 0; i < 2; ++i) {
+          db[i] = add2(db[i], dp[K - 1][i]);
 #pragma unroll
-        for (int j = 0; j < V; ++j) dp[k][j] = dp[k + 1][j];
-      if (t < p.hi) {
-        float g[V];
-        load_row<T, V>(x + t * a.x.st, r.n, a.wide, win[K - 1]);
-        load_row<T, V>(dy + t * a.dy.st, r.n, a.wide, g);
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          if (a.silu) {
-            float y = bias[j];
-#pragma unroll
-            for (int k = 0; k < K; ++k) y = fmaf(taps[k][j], win[k][j], y);
-            g[j] *= dsilu_f(y);
-          }
-          dp[K - 1][j] = g[j];
-          if (t < t1) {
-            db[j] += g[j];
-#pragma unroll
-            for (int k = 0; k < K; ++k) dw[k][j] = fmaf(g[j], win[k][j], dw[k][j]);
-          }
-#pragma unroll
-          for (int k = 0; k < K - 1; ++k) win[k][j] = win[k + 1][j];
+          for (int k = 0; k < K; ++k) dw[k][i] = fma2(dp[K - 1][i], win[k][i], dw[k][i]);
         }
-      } else {
+      }
+      shift<K>(win);
+    };
+    // dx of the token K-1 before the last dp
+    auto gradient = [&](float (&o)[kV]) {
+      f2 v[2] = {0, 0};
 #pragma unroll
-        for (int j = 0; j < V; ++j) dp[K - 1][j] = 0.f;
+      for (int k = 0; k < K; ++k) {
+        v[0] = fma2(taps[k][0], dp[K - 1 - k][0], v[0]);
+        v[1] = fma2(taps[k][1], dp[K - 1 - k][1], v[1]);
+      }
+      floats_of(v, o);
+    };
+    int t = t0;
+    // One by one up to the first token whose dx is the run's and the sequence's
+    // own, then in whole batches (none of those dx is state_final's), then one
+    // by one to the end.
+    bool batches = false;
+#pragma unroll 1
+    for (; t < t1 + K - 1; ++t) {
+      if (!batches && t - (K - 1) >= max(first, p.lo) && t + kBwdBatch <= t1) {
+        batches = true;
+#pragma unroll 1
+        for (; t + kBwdBatch <= t1; t += kBwdBatch) {
+          typename Raw<T>::type xr[kBwdBatch], gr[kBwdBatch];
+#pragma unroll
+          for (int i = 0; i < kBwdBatch; ++i) {
+            xr[i] = raw_row<kWhole, T>(x + (t + i) * a.x.st, r.n, a.wide);
+            gr[i] = raw_row<kWhole, T>(dy + (t + i) * a.dy.st, r.n, a.wide);
+          }
+#pragma unroll
+          for (int i = 0; i < kBwdBatch; ++i) {
+            shift<K>(dp);
+            token(xr[i], gr[i], true);
+            float o[kV];
+            gradient(o);
+            write_row<kWhole, T, kV>(dx + (t + i - (K - 1)) * a.dx.st, r.n, a.wide, o);
+          }
+        }
+      }
+      shift<K>(dp);
+      if (t < p.hi) {
+        token(raw_row<kWhole, T>(x + t * a.x.st, r.n, a.wide), raw_row<kWhole, T>(dy + t * a.dy.st, r.n, a.wide), t < t1);
+      } else {
+        dp[K - 1][0] = dp[K - 1][1] = 0;
       }
       const int s = t - (K - 1);
       if (s < first || s >= t1) continue;
-      float o[V];
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        o[j] = 0.f;
-#pragma unroll
-        for (int k = 0; k < K; ++k) o[j] = fmaf(taps[k][j], dp[K - 1 - k][j], o[j]);
-      }
+      float o[kV];
+      gradient(o);
       if (a.dfin.p && s >= p.hi - (K - 1)) {  // state_final holds this input
-        float f[V];
+        float f[kV];
         const T* df = static_cast<const T*>(a.dfin.p) + p.seq * a.dfin.sb + r.h * a.dfin.sh + r.c;
-        load_row<T, V>(df + (int64_t)(K - 1 + s - p.hi) * a.dfin.st, r.n, a.wide, f);
+        load_row<T, kV>(df + (int64_t)(K - 1 + s - p.hi) * a.dfin.st, r.n, a.wide, f);
 #pragma unroll
-        for (int j = 0; j < V; ++j) o[j] += f[j];
+        for (int j = 0; j < kV; ++j) o[j] += f[j];
       }
       if (s >= p.lo) {
-        store_row<T, V>(dx + s * a.dx.st, r.n, a.wide, o);
+        write_row<kWhole, T, kV>(dx + s * a.dx.st, r.n, a.wide, o);
       } else if (a.dstate0.p) {
         T* d0 = static_cast<T*>(a.dstate0.p) + p.seq * a.dstate0.sb + r.h * a.dstate0.sh + r.c;
-        store_row<T, V>(d0 + (int64_t)(K - 1 + s - p.lo) * a.dstate0.st, r.n, a.wide, o);
+        store_row<T, kV>(d0 + (int64_t)(K - 1 + s - p.lo) * a.dstate0.st, r.n, a.wide, o);
       }
     }
   } while (next_piece(a.seqs, r, a.T, a.status, &p));
-  const int64_t nv = cols / V;
-  float* dst = a.ws + (id / nv) * (K + 1) * cols + (id % nv) * V;
 #pragma unroll
-  for (int k = 0; k <= K; ++k)
-    *reinterpret_cast<float4*>(dst + k * cols) =
-        k < K ? make_float4(dw[k < K ? k : 0][0], dw[k < K ? k : 0][1], dw[k < K ? k : 0][2], dw[k < K ? k : 0][3])
-              : make_float4(db[0], db[1], db[2], db[3]);
+  for (int k = 0; k <= K; ++k) {
+    float f[kV];
+    if (k < K) floats_of(dw[k < K ? k : 0], f);
+    else floats_of(db, f);
+    *reinterpret_cast<float4*>(dst + k * cols) = make_float4(f[0], f[1], f[2], f[3]);
+  }
+}
+
+template <typename T, int K>
+__global__ void __launch_bounds__(kThreads)
+    conv_bwd_kernel(const __grid_constant__ ConvBwdArgs a, int len, int64_t cols) {
+  const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const Run r = run_of<kV>(id, a.B, a.H, a.T, a.d, len);
+  if (!r.live) return;
+  const int64_t nv = cols / kV;
+  float* dst = a.ws + (id / nv) * (K + 1) * cols + (id % nv) * kV;
+  if (a.wide && r.n >= kV) conv_back<T, K, true>(a, r, dst, cols);
+  else conv_back<T, K, false>(a, r, dst, cols);
 }
 
 struct ConvDw {
@@ -283,35 +386,39 @@ struct ConvDw {
 
 template <typename T, int K>
 __global__ void __launch_bounds__(kThreads) conv_step_kernel(ConvStepArgs a) {
-  constexpr int V = Vec<T>::n;
   SlotRows rows;
   if (!rows.begin(a.slots, blockIdx.y, a.B, a.S, a.status)) return;
-  Run r = run_of<V>((int64_t)blockIdx.x * kThreads + threadIdx.x, 1, a.H, 1, a.d, 1);
+  Run r = run_of<kV>((int64_t)blockIdx.x * kThreads + threadIdx.x, 1, a.H, 1, a.d, 1);
   if (!r.live) r.n = 0, r.h = 0, r.c = 0;  // stays for the block's barriers
-  float taps[K][V], bias[V];
-  load_taps<K, V>(a.w, a.bias, a.d, r, taps, bias);
+  f2 taps[K][2], bias[2], win[K][2];
   T* st = static_cast<T*>(a.state.p) + rows.slot * a.state.sb + r.h * a.state.sh + r.c;
-  float win[K][V];
 #pragma unroll
-  for (int k = 0; k < K - 1; ++k) load_row<T, V>(st + k * a.state.st, r.n, a.wide, win[k]);
+  for (int k = 0; k < K - 1; ++k) {
+    float f[kV];
+    load_row<T, kV>(st + k * a.state.st, r.n, a.wide, f);
+    pairs_of(f, win[k]);
+  }
+  load_taps<K>(a.w, a.bias, a.d, r, taps, bias);
   do {
     const T* x = static_cast<const T*>(a.x.p) + rows.b * a.x.sb + r.h * a.x.sh + r.c;
     T* out = static_cast<T*>(a.out.p) + rows.b * a.out.sb + r.h * a.out.sh + r.c;
-    load_row<T, V>(x, r.n, a.wide, win[K - 1]);
-    float y[V];
+    float y[kV];
+    load_row<T, kV>(x, r.n, a.wide, y);
+    pairs_of(y, win[K - 1]);
+    convolve<K>(taps, win, bias, y);
+    if (a.silu) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      y[j] = bias[j];
-#pragma unroll
-      for (int k = 0; k < K; ++k) y[j] = fmaf(taps[k][j], win[k][j], y[j]);
-      if (a.silu) y[j] = silu_f(y[j]);
-#pragma unroll
-      for (int k = 0; k < K - 1; ++k) win[k][j] = win[k + 1][j];
+      for (int j = 0; j < kV; ++j) y[j] = silu_f(y[j]);
     }
-    store_row<T, V>(out, r.n, a.wide, y);
+    shift<K>(win);
+    store_row<T, kV>(out, r.n, a.wide, y);
   } while (rows.next_row());
 #pragma unroll
-  for (int k = 0; k < K - 1; ++k) store_row<T, V>(st + k * a.state.st, r.n, a.wide, win[k]);
+  for (int k = 0; k < K - 1; ++k) {
+    float f[kV];
+    floats_of(win[k], f);
+    store_row<T, kV>(st + k * a.state.st, r.n, a.wide, f);
+  }
 }
 
 // f(integral constant K) for the call's K.
@@ -339,13 +446,13 @@ int run_length(int64_t vecs, int B, int T, int least, int most) {
   return len;
 }
 
-int fwd_run(const ConvArgs& a, int V) {
-  return run_length((int64_t)a.H * ((a.d + V - 1) / V), a.B, a.T, 8, 64);
+int fwd_run(const ConvArgs& a) {
+  return run_length((int64_t)a.H * ((a.d + kV - 1) / kV), a.B, a.T, 8, 64);
 }
 int bwd_run(const ConvBwdArgs& a) {
-  return run_length((int64_t)a.H * ((a.d + kBwdV - 1) / kBwdV), a.B, a.T, 16, 128);
+  return run_length((int64_t)a.H * ((a.d + kV - 1) / kV), a.B, a.T, 16, 128);
 }
-int64_t bwd_cols(const ConvBwdArgs& a) { return (int64_t)a.H * ((a.d + kBwdV - 1) / kBwdV) * kBwdV; }
+int64_t bwd_cols(const ConvBwdArgs& a) { return (int64_t)a.H * ((a.d + kV - 1) / kV) * kV; }
 int64_t bwd_runs(const ConvBwdArgs& a) {
   const int len = bwd_run(a);
   return (int64_t)a.B * ((a.T + len - 1) / len);
@@ -355,9 +462,8 @@ template <typename T>
 cudaError_t fwd(const ConvArgs& a, cudaStream_t s) {
   cudaError_t e = copy_empty<T>(a.seqs, a.T, a.H, a.d, a.K, a.state0, a.fin, a.status, s);
   if (e != cudaSuccess || a.T == 0) return e;
-  constexpr int V = Vec<T>::n;
-  const int len = fwd_run(a, V);
-  const int64_t n = (int64_t)a.H * ((a.d + V - 1) / V) * a.B * ((a.T + len - 1) / len);
+  const int len = fwd_run(a);
+  const int64_t n = (int64_t)a.H * ((a.d + kV - 1) / kV) * a.B * ((a.T + len - 1) / len);
   const int64_t blocks = (n + kThreads - 1) / kThreads;
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   return for_taps(a.K, [&](auto k) {
@@ -373,7 +479,7 @@ cudaError_t bwd(const ConvBwdArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int len = bwd_run(a);
   const int64_t cols = bwd_cols(a), runs = bwd_runs(a);
-  const int64_t blocks = (cols / kBwdV * runs + kThreads - 1) / kThreads;
+  const int64_t blocks = (cols / kV * runs + kThreads - 1) / kThreads;
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   if (runs > 0) {
     e = for_taps(a.K, [&](auto k) {
@@ -382,14 +488,13 @@ cudaError_t bwd(const ConvBwdArgs& a, cudaStream_t s) {
     });
     if (e != cudaSuccess) return e;
   }
-  const int per_head = (a.d + kBwdV - 1) / kBwdV * kBwdV;
+  const int per_head = (a.d + kV - 1) / kV * kV;
   return sum_parts(a.ws, runs, (a.K + 1) * cols, ConvDw{a.dw, a.dbias, cols, per_head, a.d, a.K}, s);
 }
 
 template <typename T>
 cudaError_t step(const ConvStepArgs& a, cudaStream_t s) {
-  constexpr int V = Vec<T>::n;
-  const int64_t n = (int64_t)a.H * ((a.d + V - 1) / V);
+  const int64_t n = (int64_t)a.H * ((a.d + kV - 1) / kV);
   if (a.B > 65535) return cudaErrorInvalidConfiguration;
   const dim3 g((unsigned)((n + kThreads - 1) / kThreads), a.B);
   return for_taps(a.K, [&](auto k) {

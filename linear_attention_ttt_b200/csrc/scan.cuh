@@ -6,39 +6,6 @@
 namespace ttt {
 namespace scan {
 
-// ---- two fp32 in one 64-bit register (the packed fp32 instructions of sm_100
-// do two operations an issue slot) -------------------------------------------
-
-using f2 = unsigned long long;
-__device__ __forceinline__ f2 mk2(float lo, float hi) {
-  f2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void un2(f2 v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-  f2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-  f2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-  f2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ f2 ex2_pair(f2 x) {
-  float a, b;
-  un2(x, a, b);
-  return mk2(ex2(a), ex2(b));
-}
-
 constexpr int kNB = 16;    // states a warp holds
 constexpr int kPart = 32;  // tokens staged at once: one 32-bit mask
 
