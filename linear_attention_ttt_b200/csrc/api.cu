@@ -1034,6 +1034,7 @@ ttt_status rms_norm_fwd(const ttt_tensor* x, const ttt_tensor* residual,
   a.x = view(x);
   a.r = view_or_null(residual);
   a.w = ptr<const float>(weight);
+  a.wide = a.wide && aligned16(a.w) && n.d % 4 == 0;
   a.eps = eps;
   a.out = rows_view(out);
   a.rout = rows_view(residual_out);
@@ -1065,6 +1066,7 @@ ttt_status rms_norm_bwd(const ttt_tensor* h, const ttt_tensor* weight, const ttt
   a.dy = view(dy);
   a.dres = view_or_null(dres);
   a.w = ptr<const float>(weight);
+  a.wide = a.wide && aligned16(a.w) && n.d % 4 == 0;
   a.eps = eps;
   a.dh = view_mut(dh);
   a.dw = ptr(dweight);
@@ -1379,16 +1381,15 @@ ttt_status selective_scan_step(const ttt_tensor* x, const ttt_tensor* dt, const 
   Dims n;
   int64_t N, G;
   ttt::ScanStepArgs a;
-  bool rows_wide;  // single values are read: no difference
   ttt_status st;
   if ((st = scan_check(x, dt, A, Bm, Cm, D, z, dt_bias, softplus, &n, &N, &G,
-                       &rows_wide)) != TTT_OK) return st;
+                       &a.rows_wide)) != TTT_OK) return st;
   if (n.T != 1 || state->ndim != 4 || state->shape[0] < 1) return TTT_ERR_SHAPE;
   const int64_t S = state->shape[0];
   if ((st = check_slots(slots, n, S, &a.slots)) != TTT_OK) return st;
   const int64_t hs[4] = {S, n.H, n.d, N};
   if ((st = check_f32(state, 4, hs, false)) != TTT_OK) return st;
-  if ((st = check_out_rows(out, n, n.d, x->dtype, &rows_wide)) != TTT_OK) return st;
+  if ((st = check_out_rows(out, n, n.d, x->dtype, &a.rows_wide)) != TTT_OK) return st;
   const ttt_tensor* const ins[] = {x, dt, A, Bm, Cm, D, z, dt_bias, slots};
   const ttt_tensor* const outs[] = {out, state};
   if (clash(ins, outs)) return TTT_ERR_ARG;

@@ -22,7 +22,7 @@ struct NormArgs {
   float* scale;            // non-null: out is e4m3
   int64_t sc_sb, sc_sh, sc_st;
   int B, H, T, d;
-  bool wide;               // every token tensor's rows are 16-byte aligned
+  bool wide;               // token rows are 16-byte aligned, and so is the weight's every row
 };
 cudaError_t launch_rms_norm_fwd(const NormArgs& a, bool bf16, cudaStream_t s);
 
@@ -115,6 +115,7 @@ struct ScanStepArgs {
   TokViewMut out;
   int B, S, H, d, N, G, softplus;
   bool wide;               // state and A are 16-byte aligned
+  bool rows_wide;          // and so are the token rows
   int* status;
 };
 cudaError_t launch_selective_scan_step(const ScanStepArgs& a, bool bf16, cudaStream_t s);
@@ -413,10 +414,10 @@ struct SlotRows {
   }
 };
 
-// out(col, sum over p of ws[p * cols + col]): 32 columns a block, 16 threads a
-// column, each summing every 16th part in order, then the 16 in order: the
-// result does not depend on scheduling.
-constexpr int kSumCols = 32, kSumRows = 16;
+// out(col, sum over p of ws[p * cols + col]): 8 columns a block (a sector of
+// memory), 64 threads a column, each summing every 64th part in order, then a
+// fixed tree: the result does not depend on scheduling.
+constexpr int kSumCols = 8, kSumRows = 64;
 template <typename Out>
 __global__ void __launch_bounds__(kSumCols * kSumRows)
     sum_parts_kernel(const float* __restrict__ ws, int64_t parts, int64_t cols, Out out) {
@@ -424,14 +425,16 @@ __global__ void __launch_bounds__(kSumCols * kSumRows)
   const int c = threadIdx.x % kSumCols, r = threadIdx.x / kSumCols;
   const int64_t col = (int64_t)blockIdx.x * kSumCols + c;
   float s = 0.f;
-  if (col < cols)
+  if (col < cols) {
+#pragma unroll 8
     for (int64_t p = r; p < parts; p += kSumRows) s += ws[p * cols + col];
-  part[r][c] = s;
-  __syncthreads();
-  if (r == 0 && col < cols) {
-    for (int i = 1; i < kSumRows; ++i) s += part[i][c];
-    out(col, s);
   }
+  part[r][c] = s;
+  for (int h = kSumRows / 2; h; h /= 2) {
+    __syncthreads();
+    if (r < h) part[r][c] += part[r + h][c];
+  }
+  if (r == 0 && col < cols) out(col, part[0][c]);
 }
 template <typename Out>
 cudaError_t sum_parts(const float* ws, int64_t parts, int64_t cols, Out out, cudaStream_t s) {

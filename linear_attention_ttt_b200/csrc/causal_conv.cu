@@ -158,7 +158,9 @@ __device__ __forceinline__ void convolve(const f2 (&taps)[K][2], const f2 (&win)
   floats_of(v, y);
 }
 
-constexpr int kBatch = 8;  // rows in flight a thread
+// Rows a thread has in flight: while one batch is computed the next arrives.
+template <typename T>
+constexpr int kBatch = sizeof(T) == 2 ? 8 : 4;
 
 template <typename T, int K, bool kWhole>
 __device__ __forceinline__ void conv_run(const ConvArgs& a, const Run& r) {
@@ -183,13 +185,22 @@ __device__ __forceinline__ void conv_run(const ConvArgs& a, const Run& r) {
       write_row<kWhole, T, kV>(out + t * a.out.st, r.n, a.wide, y);
       shift<K>(win);
     };
+    constexpr int n = kBatch<T>;
     int t = t0;
-    for (; t + kBatch <= t1; t += kBatch) {
-      typename Raw<T>::type in[kBatch];
+    typename Raw<T>::type in[n], ahead[n];
+    if (t + n <= t1) {
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) in[i] = raw_row<kWhole, T>(x + (t + i) * a.x.st, r.n, a.wide);
+      for (int i = 0; i < n; ++i) in[i] = raw_row<kWhole, T>(x + (t + i) * a.x.st, r.n, a.wide);
+    }
+#pragma unroll 1
+    for (; t + n <= t1; t += n) {
+      const int64_t next = t + 2 * n <= t1 ? t + n : t;  // the last batch reads itself again
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) row(t + i, in[i]);
+      for (int i = 0; i < n; ++i) ahead[i] = raw_row<kWhole, T>(x + (next + i) * a.x.st, r.n, a.wide);
+#pragma unroll
+      for (int i = 0; i < n; ++i) row(t + i, in[i]);
+#pragma unroll
+      for (int i = 0; i < n; ++i) in[i] = ahead[i];
     }
 #pragma unroll 1
     for (; t < t1; ++t) row(t, raw_row<kWhole, T>(x + t * a.x.st, r.n, a.wide));
@@ -206,7 +217,7 @@ __device__ __forceinline__ void conv_run(const ConvArgs& a, const Run& r) {
 }
 
 template <typename T, int K>
-__global__ void __launch_bounds__(kThreads) conv_fwd_kernel(const __grid_constant__ ConvArgs a, int len) {
+__global__ void __launch_bounds__(kThreads, K <= 4 ? 5 : 3) conv_fwd_kernel(const __grid_constant__ ConvArgs a, int len) {
   const Run r = run_of<kV>((int64_t)blockIdx.x * kThreads + threadIdx.x, a.B, a.H, a.T, a.d, len);
   if (!r.live) return;
   if (a.wide && r.n >= kV) conv_run<T, K, true>(a, r);
@@ -245,7 +256,8 @@ cudaError_t copy_empty(const Seqs& q, int T_, int H, int d, int K, const TokView
 // needs dp up to s+K-1, and dp is computed again there rather than exchanged.
 // dp of tokens behind the sequence is zero. The run's shares of dweight and
 // dbias go to ws[run][K+1][channels].
-constexpr int kBwdBatch = 4;
+template <typename T>
+constexpr int kBwdBatch = sizeof(T) == 2 ? 4 : 2;
 template <typename T, int K, bool kWhole>
 __device__ __forceinline__ void conv_back(const ConvBwdArgs& a, const Run& r, float* dst, int64_t cols) {
   f2 taps[K][2], bias[2], dw[K][2], db[2] = {0, 0};
@@ -304,24 +316,32 @@ __device__ __forceinline__ void conv_back(const ConvBwdArgs& a, const Run& r, fl
     bool batches = false;
 #pragma unroll 1
     for (; t < t1 + K - 1; ++t) {
-      if (!batches && t - (K - 1) >= max(first, p.lo) && t + kBwdBatch <= t1) {
+      if (!batches && t - (K - 1) >= max(first, p.lo) && t + kBwdBatch<T> <= t1) {
         batches = true;
-#pragma unroll 1
-        for (; t + kBwdBatch <= t1; t += kBwdBatch) {
-          typename Raw<T>::type xr[kBwdBatch], gr[kBwdBatch];
+        typename Raw<T>::type xr[kBwdBatch<T>], gr[kBwdBatch<T>], xa[kBwdBatch<T>], ga[kBwdBatch<T>];
 #pragma unroll
-          for (int i = 0; i < kBwdBatch; ++i) {
-            xr[i] = raw_row<kWhole, T>(x + (t + i) * a.x.st, r.n, a.wide);
-            gr[i] = raw_row<kWhole, T>(dy + (t + i) * a.dy.st, r.n, a.wide);
+        for (int i = 0; i < kBwdBatch<T>; ++i) {
+          xr[i] = raw_row<kWhole, T>(x + (t + i) * a.x.st, r.n, a.wide);
+          gr[i] = raw_row<kWhole, T>(dy + (t + i) * a.dy.st, r.n, a.wide);
+        }
+#pragma unroll 1
+        for (; t + kBwdBatch<T> <= t1; t += kBwdBatch<T>) {
+          const int64_t next = t + 2 * kBwdBatch<T> <= t1 ? t + kBwdBatch<T> : t;  // the last batch reads itself again
+#pragma unroll
+          for (int i = 0; i < kBwdBatch<T>; ++i) {
+            xa[i] = raw_row<kWhole, T>(x + (next + i) * a.x.st, r.n, a.wide);
+            ga[i] = raw_row<kWhole, T>(dy + (next + i) * a.dy.st, r.n, a.wide);
           }
 #pragma unroll
-          for (int i = 0; i < kBwdBatch; ++i) {
+          for (int i = 0; i < kBwdBatch<T>; ++i) {
             shift<K>(dp);
             token(xr[i], gr[i], true);
             float o[kV];
             gradient(o);
             write_row<kWhole, T, kV>(dx + (t + i - (K - 1)) * a.dx.st, r.n, a.wide, o);
           }
+#pragma unroll
+          for (int i = 0; i < kBwdBatch<T>; ++i) xr[i] = xa[i], gr[i] = ga[i];
         }
       }
       shift<K>(dp);
@@ -359,7 +379,7 @@ __device__ __forceinline__ void conv_back(const ConvBwdArgs& a, const Run& r, fl
 }
 
 template <typename T, int K>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, K > 4 ? 2 : sizeof(T) == 2 ? 4 : 3)
     conv_bwd_kernel(const __grid_constant__ ConvBwdArgs a, int len, int64_t cols) {
   const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   const Run r = run_of<kV>(id, a.B, a.H, a.T, a.d, len);
@@ -437,20 +457,21 @@ cudaError_t for_taps(int K, F f) {
   return cudaErrorInvalidValue;
 }
 
-// Tokens a thread walks: long enough to make the K-1 rows read twice cheap,
-// short enough to give every SM 1024 threads.
-int run_length(int64_t vecs, int B, int T, int least, int most) {
-  const int64_t want = (int64_t)148 * 1024;
+// Tokens a thread walks: as many as leave `want` threads, to make the rows read
+// twice (K-1 a run, and in the backward pass computed twice, with K+1 partial
+// sums a run) cheap. B2 T4096 d4096 K4 backward: 96 us in runs of 32, 81 in 64,
+// 74 in 128.
+int run_length(int64_t vecs, int B, int T, int64_t want, int least, int most) {
   int len = most;
   while (len > least && vecs * B * ((T + len - 1) / len) < want) len /= 2;
   return len;
 }
 
 int fwd_run(const ConvArgs& a) {
-  return run_length((int64_t)a.H * ((a.d + kV - 1) / kV), a.B, a.T, 8, 64);
+  return run_length((int64_t)a.H * ((a.d + kV - 1) / kV), a.B, a.T, 148 * 1024, 8, 64);
 }
 int bwd_run(const ConvBwdArgs& a) {
-  return run_length((int64_t)a.H * ((a.d + kV - 1) / kV), a.B, a.T, 16, 128);
+  return run_length((int64_t)a.H * ((a.d + kV - 1) / kV), a.B, a.T, 148 * 256, 16, 128);
 }
 int64_t bwd_cols(const ConvBwdArgs& a) { return (int64_t)a.H * ((a.d + kV - 1) / kV) * kV; }
 int64_t bwd_runs(const ConvBwdArgs& a) {

@@ -12,7 +12,7 @@
 namespace ttt {
 namespace {
 
-constexpr int kThreads = 256;   // of a block that holds several rows
+constexpr int kThreads = 128;   // of a block that holds several rows
 constexpr int kVpt = 4;         // vectors a lane holds where a warp has a row
 constexpr int kMaxThreads = 512;  // a block of one row; 128 registers a thread
 
@@ -45,31 +45,42 @@ RowPlan plan_rows(int d) {
   return p;
 }
 
-// Sum (or maximum, kMax) of v over the `lanes` threads of a row, to all of
-// them. `red` holds a value a warp; blocks of one row only. The maximum
-// keeps NaN.
+// Sums (or maxima, kMax) of v[0..n) over the `lanes` threads of a row, to all of
+// them. `red` holds n values a warp; blocks of one row only. The maximum keeps NaN.
 template <bool kMax>
 __device__ __forceinline__ float join(float a, float b) {
   if (!kMax) return a + b;
-  return a > b || a != a ? a : b;
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
-template <bool kMax>
-__device__ __forceinline__ float row_reduce(float v, int lanes, float* red) {
-  for (int o = min(lanes, 32) / 2; o; o >>= 1) v = join<kMax>(v, __shfl_xor_sync(0xffffffffu, v, o));
+template <bool kMax, int n>
+__device__ __forceinline__ void row_reduce(float (&v)[n], int lanes, float* red) {
+  for (int o = min(lanes, 32) / 2; o; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < n; ++i) v[i] = join<kMax>(v[i], __shfl_xor_sync(0xffffffffu, v[i], o));
   if (lanes > 32) {
     __syncthreads();  // the last use of `red` is over
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    if ((threadIdx.x & 31) == 0)
+#pragma unroll
+      for (int i = 0; i < n; ++i) red[(threadIdx.x >> 5) * n + i] = v[i];
     __syncthreads();
-    v = red[0];
-    for (int i = 1; i < lanes / 32; ++i) v = join<kMax>(v, red[i]);
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      v[i] = red[i];
+      for (int k = 1; k < lanes / 32; ++k) v[i] = join<kMax>(v[i], red[k * n + i]);
+    }
   }
-  return v;
 }
 
 struct RowAt {
   int b, h, t;
 };
 __device__ __forceinline__ RowAt row_at(int64_t r, int H, int T) {
+  if (r < 0x7fffffff) {  // the common case, without 64-bit division
+    const unsigned bh = (unsigned)r / (unsigned)T;
+    return {(int)(bh / H), (int)(bh % H), (int)((unsigned)r - bh * T)};
+  }
   const int64_t bh = r / T;
   return {(int)(bh / H), (int)(bh % H), (int)(r % T)};
 }
@@ -80,176 +91,257 @@ __device__ __forceinline__ float inv_rms(float sumsq, int d, float eps) {
   return m > 0.f || m != m ? rsqrtf(m) : 0.f;
 }
 
-__device__ __forceinline__ void store_e4m3(uint8_t* p, int n, bool wide, const float* y, int count) {
+// V quotients as 8-bit values, n of them to memory.
+template <int V>
+__device__ __forceinline__ void store_e4m3(uint8_t* p, int n, bool wide, const float (&y)[8]) {
+  uint32_t w[V / 4];
 #pragma unroll
-  for (int i = 0; i < 8; i += 4) {
-    if (i >= count) break;
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[i], y[i + 1]), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi =
-        __nv_cvt_float2_to_fp8x2(make_float2(y[i + 2], y[i + 3]), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t w = lo | hi << 16;
-    if (wide && i + 4 <= n) {
-      *reinterpret_cast<uint32_t*>(p + i) = w;
-    } else {
+  for (int i = 0; i < V / 4; ++i) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * i], y[4 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * i + 2], y[4 * i + 3]), __NV_SATFINITE, __NV_E4M3);
+    w[i] = lo | hi << 16;
+  }
+  if (wide && n >= V) {
+    if constexpr (V == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t*>(p) = w[0];
+  } else {
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (i + k < n) p[i + k] = (uint8_t)(w >> (8 * k));
+    for (int k = 0; k < V; ++k)
+      if (k < n) p[k] = (uint8_t)(w[k / 4] >> (8 * (k % 4)));
+  }
+}
+
+// V weights of a row's piece at column c (zeros behind the row's end).
+template <bool kWhole, int V>
+__device__ __forceinline__ void weights(const float* w, int c, int d, float (&f)[V]) {
+  if constexpr (kWhole) {
+#pragma unroll
+    for (int j = 0; j < V; j += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(w + c + j);
+      f[j] = v.x, f[j + 1] = v.y, f[j + 2] = v.z, f[j + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) f[j] = c + j < d ? w[c + j] : 0.f;
+  }
+}
+
+// R tokens of a head beside one another, each by the same threads. kWhole:
+// every vector of every thread is a whole one of the row's (see read_row).
+template <typename T, int VPT, int R, bool kWhole>
+__device__ __forceinline__ void norm_rows(const NormArgs& a, int lanes, float* red) {
+  constexpr int V = Vec<T>::n;
+  const int lane = threadIdx.x % lanes, groups = (a.T + R - 1) / R;
+  const int64_t all = (int64_t)a.B * a.H * groups;
+  const int64_t g = (int64_t)blockIdx.x * (blockDim.x / lanes) + threadIdx.x / lanes;
+  const RowAt at = row_at(min(g, all - 1), a.H, groups);
+  const int t0 = at.t * R, n = g < all ? min(R, a.T - t0) : 0;  // tokens that are this thread's
+  const T* x = static_cast<const T*>(a.x.p) + at.b * a.x.sb + at.h * a.x.sh;
+  const float* w = a.w + at.h * a.w_sh;
+  float s[R][VPT][V], q[R][VPT][V];
+#pragma unroll
+  for (int k = 0; k < R; ++k)
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = (i * lanes + lane) * V;
+      read_row<kWhole, T, V>(x + min(t0 + k, a.T - 1) * a.x.st + c, a.d - c, a.wide, s[k][i]);
+    }
+  if (a.r.p) {
+    const T* res = static_cast<const T*>(a.r.p) + at.b * a.r.sb + at.h * a.r.sh;
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int c = (i * lanes + lane) * V;
+        read_row<kWhole, T, V>(res + min(t0 + k, a.T - 1) * a.r.st + c, a.d - c, a.wide, q[k][i]);
+      }
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) s[k][i][j] += q[k][i][j];
+  }
+  float sum[R];
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    sum[k] = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+      for (int j = 0; j < V; ++j) sum[k] = fmaf(s[k][i][j], s[k][i][j], sum[k]);
+  }
+  if (a.rout.p) {
+    T* ro = static_cast<T*>(a.rout.p) + at.b * a.rout.sb + at.h * a.rout.sh;
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int c = (i * lanes + lane) * V;
+        if (k < n) write_row<kWhole, T, V>(ro + (t0 + k) * a.rout.st + c, a.d - c, a.wide, s[k][i]);
+      }
+  }
+  row_reduce<false>(sum, lanes, red);
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    float f[V];
+    weights<kWhole, V>(w, (i * lanes + lane) * V, a.d, f);
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const float rs = inv_rms(sum[k], a.d, a.eps);
+#pragma unroll
+      for (int j = 0; j < V; ++j) s[k][i][j] = s[k][i][j] * rs * f[j];
+    }
+  }
+  if (!a.scale) {
+    T* o = static_cast<T*>(a.out.p) + at.b * a.out.sb + at.h * a.out.sh;
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int c = (i * lanes + lane) * V;
+        if (k < n) write_row<kWhole, T, V>(o + (t0 + k) * a.out.st + c, a.d - c, a.wide, s[k][i]);
+      }
+    return;
+  }
+  float top[R];
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    top[k] = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+      for (int j = 0; j < V; ++j) top[k] = join<true>(top[k], fabsf(s[k][i][j]));
+  }
+  row_reduce<true>(top, lanes, red);
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    if (k >= n) break;
+    const float scale = top[k] / 448.f;
+    if (lane == 0) a.scale[at.b * a.sc_sb + at.h * a.sc_sh + (t0 + k) * a.sc_st] = scale;
+    // the quotient by the reciprocal is at most an fp32 step off, well within
+    // e4m3's; tiny scales have none and keep the division
+    const float inv = 1.f / scale;
+    const bool tiny = scale < 1e-36f;
+    uint8_t* o = static_cast<uint8_t*>(a.out.p) + at.b * a.out.sb + at.h * a.out.sh + (t0 + k) * a.out.st;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = (i * lanes + lane) * V;
+      float y[8];
+      if (tiny) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) y[j] = scale == 0.f ? s[k][i][j] : s[k][i][j] / scale;
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) y[j] = s[k][i][j] * inv;
+      }
+      store_e4m3<V>(o + c, kWhole ? V : a.d - c, kWhole || a.wide, y);
     }
   }
 }
 
-template <typename T, int VPT>
-__global__ void __launch_bounds__(kMaxThreads) norm_fwd_kernel(NormArgs a, int lanes) {
-  constexpr int V = Vec<T>::n;
+// Whether every thread's vectors are whole ones of the row's.
+template <typename T>
+__host__ __device__ __forceinline__ bool whole_rows(bool wide, int d, int lanes, int vpt) {
+  return wide && d == lanes * vpt * Vec<T>::n;
+}
+
+template <typename T, int VPT, int R>
+__global__ void __launch_bounds__(kMaxThreads, 1) norm_fwd_kernel(const __grid_constant__ NormArgs a, int lanes) {
   __shared__ float red[32];
-  const int lane = threadIdx.x % lanes;
-  const int64_t rows = (int64_t)a.B * a.H * a.T;
-  const int64_t r = (int64_t)blockIdx.x * (blockDim.x / lanes) + threadIdx.x / lanes;
-  const bool live = r < rows;
-  const RowAt at = row_at(live ? r : rows - 1, a.H, a.T);
-  const T* x = static_cast<const T*>(a.x.p) + at.b * a.x.sb + at.h * a.x.sh + at.t * a.x.st;
-  const float* w = a.w + at.h * a.w_sh;
-  float s[VPT][V];
-  float sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < VPT; ++i) unpack<T>(load_vec(x + (i * lanes + lane) * V, a.d - (i * lanes + lane) * V, a.wide), s[i]);
-  if (a.r.p) {
-    const T* res = static_cast<const T*>(a.r.p) + at.b * a.r.sb + at.h * a.r.sh + at.t * a.r.st;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = (i * lanes + lane) * V;
-      float f[V];
-      unpack<T>(load_vec(res + c, a.d - c, a.wide), f);
-#pragma unroll
-      for (int j = 0; j < V; ++j) s[i][j] += f[j];
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < VPT; ++i)
-#pragma unroll
-    for (int j = 0; j < V; ++j) sum = fmaf(s[i][j], s[i][j], sum);
-  if (a.rout.p && live) {
-    T* ro = static_cast<T*>(a.rout.p) + at.b * a.rout.sb + at.h * a.rout.sh + at.t * a.rout.st;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = (i * lanes + lane) * V;
-      store_vec<T>(ro + c, a.d - c, a.wide, s[i]);
-    }
-  }
-  const float rs = inv_rms(row_reduce<false>(sum, lanes, red), a.d, a.eps);
-#pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int c = (i * lanes + lane) * V;
-#pragma unroll
-    for (int j = 0; j < V; ++j) s[i][j] = c + j < a.d ? s[i][j] * rs * w[c + j] : 0.f;
-  }
-  if (!a.scale) {
-    if (!live) return;
-    T* o = static_cast<T*>(a.out.p) + at.b * a.out.sb + at.h * a.out.sh + at.t * a.out.st;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = (i * lanes + lane) * V;
-      store_vec<T>(o + c, a.d - c, a.wide, s[i]);
-    }
-    return;
-  }
-  float top = 0.f;
-#pragma unroll
-  for (int i = 0; i < VPT; ++i)
-#pragma unroll
-    for (int j = 0; j < V; ++j) top = join<true>(top, fabsf(s[i][j]));
-  top = row_reduce<true>(top, lanes, red);
-  if (!live) return;
-  const float scale = top / 448.f;
-  if (lane == 0) a.scale[at.b * a.sc_sb + at.h * a.sc_sh + at.t * a.sc_st] = scale;
-  const float by = scale == 0.f ? 1.f : scale;
-  uint8_t* o = static_cast<uint8_t*>(a.out.p) + at.b * a.out.sb + at.h * a.out.sh + at.t * a.out.st;
-#pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int c = (i * lanes + lane) * V;
-    float q[8];
-#pragma unroll
-    for (int j = 0; j < V; ++j) q[j] = s[i][j] / by;
-    store_e4m3(o + c, a.d - c, a.wide, q, V);
-  }
+  if (whole_rows<T>(a.wide, a.d, lanes, VPT)) norm_rows<T, VPT, R, true>(a, lanes, red);
+  else norm_rows<T, VPT, R, false>(a, lanes, red);
 }
 
 // Rows of one weight: all of them, or those of head blockIdx.y. Every block
-// walks rows worker, worker + workers, ... and keeps its share of dweight in
-// registers; the shares go to ws[block][d padded to the row's vectors].
-template <typename T, int VPT>
-__global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(NormBwdArgs a, int lanes, int64_t rows, int cols) {
+// walks rows worker, worker + workers, ... , reading the next row while it works
+// on one, and keeps its share of dweight in registers; the shares go to
+// ws[block][d padded to the row's vectors].
+template <typename T, int VPT, bool kWhole>
+__device__ __forceinline__ void norm_back(const NormBwdArgs& a, int lanes, int64_t rows, int cols, float* share,
+                                          float* red) {
   constexpr int V = Vec<T>::n;
-  extern __shared__ float share[];  // [rows a block][cols]
-  __shared__ float red[32];
   const int lane = threadIdx.x % lanes, sub = threadIdx.x / lanes, subs = blockDim.x / lanes;
   const int64_t workers = (int64_t)gridDim.x * subs;
   const int head = blockIdx.y;
-  const float* w = a.w + head * a.w_sh;
-  float dw[VPT][V];
+  // long rows leave no registers for the weights and the next row
+  constexpr bool kAhead = VPT * V <= 16;
+  const float* wp = a.w + head * a.w_sh;
+  float w[kAhead ? VPT : 1][V], dw[VPT][V];
 #pragma unroll
-  for (int i = 0; i < VPT; ++i)
+  for (int i = 0; i < VPT; ++i) {
+    if (kAhead) weights<kWhole, V>(wp, (i * lanes + lane) * V, a.d, w[kAhead ? i : 0]);
 #pragma unroll
     for (int j = 0; j < V; ++j) dw[i][j] = 0.f;
+  }
   // every thread of a block makes the same number of turns (row_reduce synchronises)
   const int64_t turns = (rows + workers - 1) / workers;
+  Vec<T> hv[VPT], gv[VPT], rv[VPT];
+  RowAt at = {0, 0, 0}, ahead = {0, 0, 0};
+  auto fetch = [&](int64_t k) {
+    const int64_t r = min(k * workers + (int64_t)blockIdx.x * subs + sub, rows - 1);
+    if (a.w_sh) {
+      ahead = row_at(r, 1, a.T);
+      ahead.h = head;
+    } else {
+      ahead = row_at(r, a.H, a.T);
+    }
+    const T* hp = static_cast<const T*>(a.h.p) + ahead.b * a.h.sb + ahead.h * a.h.sh + ahead.t * a.h.st;
+    const T* gp = static_cast<const T*>(a.dy.p) + ahead.b * a.dy.sb + ahead.h * a.dy.sh + ahead.t * a.dy.st;
+    // without it the gradient stands in its place and is not used
+    const T* rp = a.dres.p ? static_cast<const T*>(a.dres.p) + ahead.b * a.dres.sb + ahead.h * a.dres.sh + ahead.t * a.dres.st
+                           : gp;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = (i * lanes + lane) * V, n = kWhole ? V : a.d - c;
+      hv[i] = kWhole ? Vec<T>{*reinterpret_cast<const uint4*>(hp + c)} : load_vec(hp + c, n, a.wide);
+      gv[i] = kWhole ? Vec<T>{*reinterpret_cast<const uint4*>(gp + c)} : load_vec(gp + c, n, a.wide);
+      rv[i] = kWhole ? Vec<T>{*reinterpret_cast<const uint4*>(rp + c)} : load_vec(rp + c, n, a.wide);
+    }
+  };
+  if (kAhead && turns > 0) fetch(0);
   for (int64_t k = 0; k < turns; ++k) {
-    const int64_t r = k * workers + (int64_t)blockIdx.x * subs + sub;
-    const bool live = r < rows;
-    RowAt at = {0, 0, 0};
-    if (live) {
-      if (a.w_sh) {
-        at = {(int)(r / a.T), head, (int)(r % a.T)};
-      } else {
-        at = row_at(r, a.H, a.T);
-      }
-    }
-    const T* hp = static_cast<const T*>(a.h.p) + at.b * a.h.sb + at.h * a.h.sh + at.t * a.h.st;
-    const T* gp = static_cast<const T*>(a.dy.p) + at.b * a.dy.sb + at.h * a.dy.sh + at.t * a.dy.st;
-    Vec<T> hv[VPT], gv[VPT];
+    const bool live = k * workers + (int64_t)blockIdx.x * subs + sub < rows;
+    if (!kAhead) fetch(k);
+    at = ahead;
+    float h[VPT][V], g[VPT][V];
+    Vec<T> res[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = (i * lanes + lane) * V;
-      hv[i] = load_vec(hp + c, live ? a.d - c : 0, a.wide);
-      gv[i] = load_vec(gp + c, live ? a.d - c : 0, a.wide);
+      unpack<T>(hv[i], h[i]);
+      unpack<T>(gv[i], g[i]);
+      res[i] = rv[i];
     }
-    float sum = 0.f, dot = 0.f;
+    if (kAhead && k + 1 < turns) fetch(k + 1);
+    float sums[2] = {0.f, 0.f};  // of h^2 and of dy w h
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = (i * lanes + lane) * V;
-      float h[V], g[V];
-      unpack<T>(hv[i], h);
-      unpack<T>(gv[i], g);
+      float(&f)[V] = w[kAhead ? i : 0];
+      if (!kAhead) weights<kWhole, V>(wp, (i * lanes + lane) * V, a.d, f);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        sum = fmaf(h[j], h[j], sum);
-        dot = fmaf(c + j < a.d ? g[j] * w[c + j] : 0.f, h[j], dot);
+        sums[0] = fmaf(h[i][j], h[i][j], sums[0]);
+        sums[1] = fmaf(g[i][j] * f[j], h[i][j], sums[1]);
       }
     }
-    const float rs = inv_rms(row_reduce<false>(sum, lanes, red), a.d, a.eps);
-    const float m = row_reduce<false>(dot, lanes, red) / (float)a.d * rs * rs;
+    row_reduce<false>(sums, lanes, red);
+    const float rs = inv_rms(sums[0], a.d, a.eps);
+    const float m = sums[1] / (float)a.d * rs * rs;
     if (!live) continue;  // the block's last turn
-    const T* rp = a.dres.p ? static_cast<const T*>(a.dres.p) + at.b * a.dres.sb + at.h * a.dres.sh + at.t * a.dres.st
-                           : nullptr;
     T* op = static_cast<T*>(a.dh.p) + at.b * a.dh.sb + at.h * a.dh.sh + at.t * a.dh.st;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = (i * lanes + lane) * V;
-      float h[V], g[V], o[V];
-      unpack<T>(hv[i], h);
-      unpack<T>(gv[i], g);
+      float(&f)[V] = w[kAhead ? i : 0];
+      if (!kAhead) weights<kWhole, V>(wp, c, a.d, f);
+      float o[V];
+      unpack<T>(res[i], o);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        dw[i][j] = fmaf(g[j], h[j] * rs, dw[i][j]);
-        o[j] = rs * ((c + j < a.d ? g[j] * w[c + j] : 0.f) - h[j] * m);
+        dw[i][j] = fmaf(g[i][j], h[i][j] * rs, dw[i][j]);
+        o[j] = fmaf(rs, fmaf(g[i][j], f[j], -h[i][j] * m), a.dres.p ? o[j] : 0.f);
       }
-      if (rp) {
-        float f[V];
-        unpack<T>(load_vec(rp + c, a.d - c, a.wide), f);
-#pragma unroll
-        for (int j = 0; j < V; ++j) o[j] += f[j];
-      }
-      store_vec<T>(op + c, a.d - c, a.wide, o);
+      write_row<kWhole, T, V>(op + c, a.d - c, a.wide, o);
     }
   }
   float* dst = a.ws + ((int64_t)blockIdx.x * gridDim.y + head) * cols;
@@ -257,7 +349,9 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(NormBwdArgs a, in
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
-      for (int j = 0; j < V; ++j) dst[(i * lanes + lane) * V + j] = dw[i][j];
+      for (int j = 0; j < V; j += 4)
+        *reinterpret_cast<float4*>(dst + (i * lanes + lane) * V + j) =
+            make_float4(dw[i][j], dw[i][j + 1], dw[i][j + 2], dw[i][j + 3]);
     return;
   }
 #pragma unroll
@@ -270,6 +364,15 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(NormBwdArgs a, in
     for (int k = 1; k < subs; ++k) s += share[k * cols + c];
     dst[c] = s;
   }
+}
+
+template <typename T, int VPT>
+__global__ void __launch_bounds__(kMaxThreads, 1)
+    norm_bwd_kernel(const __grid_constant__ NormBwdArgs a, int lanes, int64_t rows, int cols) {
+  extern __shared__ float share[];  // [rows a block][cols]
+  __shared__ float red[32];
+  if (whole_rows<T>(a.wide, a.d, lanes, VPT)) norm_back<T, VPT, true>(a, lanes, rows, cols, share, red);
+  else norm_back<T, VPT, false>(a, lanes, rows, cols, share, red);
 }
 
 struct NormDw {
@@ -290,21 +393,27 @@ int bwd_blocks(const NormBwdArgs& a) {
   const int64_t rows = (int64_t)a.B * a.T * (a.w_sh ? 1 : a.H);
   const int subs = p.block / p.lanes;
   const int64_t want = (rows + subs - 1) / subs;
-  const int64_t cap = (int64_t)148 * (2048 / p.block) / (a.w_sh ? a.H : 1);
+  const int64_t cap = (int64_t)148 * (512 / p.block) / (a.w_sh ? a.H : 1);
   return (int)(want < 1 ? 1 : want < cap ? want : cap < 1 ? 1 : cap);
 }
+
+// Short rows (a vector a thread) go four tokens a thread: their places and
+// weights are found once, and four loads are in flight.
+constexpr int kShortRows = 4;
 
 template <typename T>
 cudaError_t fwd(const NormArgs& a, cudaStream_t s) {
   const RowPlan p = plan_rows<T>(a.d);
-  const int64_t rows = (int64_t)a.B * a.H * a.T, per = p.block / p.lanes;
-  const int64_t blocks = (rows + per - 1) / per;
+  const int R = p.vpt == 1 && a.T >= kShortRows ? kShortRows : 1;
+  const int64_t groups = (int64_t)a.B * a.H * ((a.T + R - 1) / R), per = p.block / p.lanes;
+  const int64_t blocks = (groups + per - 1) / per;
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   const dim3 g((unsigned)blocks), b(p.block);
-  if (p.vpt == 1) norm_fwd_kernel<T, 1><<<g, b, 0, s>>>(a, p.lanes);
-  else if (p.vpt == 2) norm_fwd_kernel<T, 2><<<g, b, 0, s>>>(a, p.lanes);
-  else if (p.vpt == 4) norm_fwd_kernel<T, 4><<<g, b, 0, s>>>(a, p.lanes);
-  else if constexpr (Vec<T>::n == 4) norm_fwd_kernel<T, 8><<<g, b, 0, s>>>(a, p.lanes);
+  if (R > 1) norm_fwd_kernel<T, 1, kShortRows><<<g, b, 0, s>>>(a, p.lanes);
+  else if (p.vpt == 1) norm_fwd_kernel<T, 1, 1><<<g, b, 0, s>>>(a, p.lanes);
+  else if (p.vpt == 2) norm_fwd_kernel<T, 2, 1><<<g, b, 0, s>>>(a, p.lanes);
+  else if (p.vpt == 4) norm_fwd_kernel<T, 4, 1><<<g, b, 0, s>>>(a, p.lanes);
+  else if constexpr (Vec<T>::n == 4) norm_fwd_kernel<T, 8, 1><<<g, b, 0, s>>>(a, p.lanes);
   return cudaGetLastError();
 }
 

@@ -308,75 +308,110 @@ __global__ void copy_empty_kernel(Seqs q, int T, int64_t n, const float* src, fl
     dst[blockIdx.x * n + i] = src ? src[blockIdx.x * n + i] : 0.f;
 }
 
-// One token: a lane has four states of a channel, and a channel has 2^k lanes.
-// Bound by memory: the states are read and written once, in 16-byte pieces.
-constexpr int kStepThreads = 256;
-template <typename T>
-__global__ void __launch_bounds__(kStepThreads) step_kernel(ScanStepArgs a, int lanes, int cts) {
-  SlotRows rows;
-  if (!rows.begin(a.slots, blockIdx.y, a.B, a.S, a.status)) return;
-  const int per = kStepThreads / lanes, n0 = threadIdx.x % lanes * 4;
-  const int h = blockIdx.x / cts, c = blockIdx.x % cts * per + threadIdx.x / lanes;
-  const bool live = c < a.d;
-  const int64_t ch = (int64_t)h * a.d + (live ? c : 0);
-  const int left = live ? a.N - n0 : 0;
-  const bool whole = a.wide && left >= 4 && a.N % 4 == 0;
-  float A[4], s[4];
-  float* sp = a.state + ((int64_t)rows.slot * a.H * a.d + ch) * a.N + n0;
-  const float* ap = a.A + ch * a.N + n0;
-  if (whole) {
-    const float4 v = *reinterpret_cast<const float4*>(sp), w = *reinterpret_cast<const float4*>(ap);
-    s[0] = v.x, s[1] = v.y, s[2] = v.z, s[3] = v.w;
-    A[0] = w.x, A[1] = w.y, A[2] = w.z, A[3] = w.w;
-  } else {
+// One token. A channel's states lie on 2^k lanes, four a lane, and a lane has
+// them of four channels: places and slots are found once for 16 states. What a
+// channel needs once (its step size, the gate) one of its lanes computes for
+// the others. Bound by memory: the states are read and written once, in
+// 16-byte pieces.
+constexpr int kStepThreads = 128, kStepCh = 4;
+
+// kWhole: N is 4 kLanes, the block's channels all exist and every row is
+// aligned (see read_row).
+template <typename T, int kLanes, bool kWhole>
+__device__ __forceinline__ void step_rows(const ScanStepArgs& a, SlotRows& rows, int h, int first) {
+  constexpr int groups = kStepThreads / kLanes;
+  constexpr int kOwn = kLanes >= kStepCh ? 1 : kStepCh / kLanes;  // channels a lane computes for the others
+  const int me = threadIdx.x % kLanes, n0 = me * 4, c0 = first + threadIdx.x / kLanes;
+  const int64_t ch0 = (int64_t)h * a.d;
+  const int left = a.N - n0, g = h / (a.H / a.G), base = threadIdx.x & 31 & ~(kLanes - 1);
+  const bool whole = a.wide && a.N % 4 == 0;
+  float A[kStepCh][4], s[kStepCh][4], bias[kOwn], D[kOwn];
+  int own[kOwn];
+  float* sp = a.state + ((int64_t)rows.slot * a.H * a.d + ch0) * a.N + n0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      s[k] = k < left ? sp[k] : 0.f;
-      A[k] = k < left ? ap[k] : 0.f;
-    }
+  for (int i = 0; i < kStepCh; ++i) {
+    const int c = c0 + i * groups, n = c < a.d ? left : 0;
+    read_row<kWhole, float, 4>(sp + (int64_t)c * a.N, n, whole, s[i]);
+    read_row<kWhole, float, 4>(a.A + (ch0 + c) * a.N + n0, n, whole, A[i]);
   }
-  const float bias = a.dt_bias && live ? a.dt_bias[ch] : 0.f;
-  const float dskip = a.D && live ? a.D[ch] : 0.f;
-  const int g = h / (a.H / a.G);
-  do {
-    float x = 0.f, raw = 0.f, z = 0.f, y = 0.f;
-    if (live) {
-      x = to_f32(static_cast<const T*>(a.x.p)[rows.b * a.x.sb + h * a.x.sh + c]);
-      raw = to_f32(static_cast<const T*>(a.dt.p)[rows.b * a.dt.sb + h * a.dt.sh + c]);
-      if (a.z.p) z = to_f32(static_cast<const T*>(a.z.p)[rows.b * a.z.sb + h * a.z.sh + c]);
-    }
-    const T* bp = static_cast<const T*>(a.Bm.p) + rows.b * a.Bm.sb + g * a.Bm.sh + n0;
-    const T* cp = static_cast<const T*>(a.Cm.p) + rows.b * a.Cm.sb + g * a.Cm.sh + n0;
-    const float dt = step_of(raw + bias, a.softplus);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (k >= left) break;
-      s[k] = fmaf(ex2(dt * (A[k] * kLog2e)), s[k], dt * x * to_f32(bp[k]));
-      y = fmaf(s[k], to_f32(cp[k]), y);
+  for (int j = 0; j < kOwn; ++j) {
+    own[j] = c0 + ((me & (kStepCh - 1)) + j * kLanes) * groups;
+    bias[j] = a.dt_bias && (kWhole || own[j] < a.d) ? a.dt_bias[ch0 + own[j]] : 0.f;
+    D[j] = a.D && (kWhole || own[j] < a.d) ? a.D[ch0 + own[j]] : 0.f;
+  }
+  do {
+    const T* xp = static_cast<const T*>(a.x.p) + rows.b * a.x.sb + h * a.x.sh;
+    const T* dp = static_cast<const T*>(a.dt.p) + rows.b * a.dt.sb + h * a.dt.sh;
+    // without a gate the input stands in its place and is not used
+    const T* zp = a.z.p ? static_cast<const T*>(a.z.p) + rows.b * a.z.sb + h * a.z.sh : xp;
+    float Bv[4], Cv[4], x[kOwn], dt[kOwn], z[kOwn], y[kOwn];
+    read_row<kWhole, T, 4>(static_cast<const T*>(a.Bm.p) + rows.b * a.Bm.sb + g * a.Bm.sh + n0, left, a.rows_wide, Bv);
+    read_row<kWhole, T, 4>(static_cast<const T*>(a.Cm.p) + rows.b * a.Cm.sb + g * a.Cm.sh + n0, left, a.rows_wide, Cv);
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) {
+      const bool in = kWhole || own[j] < a.d;
+      x[j] = in ? to_f32(xp[own[j]]) : 0.f;
+      dt[j] = in ? to_f32(dp[own[j]]) : 0.f;
+      z[j] = in ? to_f32(zp[own[j]]) : 0.f;
     }
-    for (int o = lanes / 2; o; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-    if (live && n0 == 0) {
-      y = fmaf(dskip, x, y);
-      if (a.z.p) y *= silu_f(z);
-      static_cast<T*>(a.out.p)[rows.b * a.out.sb + h * a.out.sh + c] = from_f32<T>(y);
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) dt[j] = step_of(dt[j] + bias[j], a.softplus);
+#pragma unroll
+    for (int i = 0; i < kStepCh; ++i) {
+      constexpr int kDiv = kLanes < kStepCh ? kLanes : kStepCh;
+      const int from = base + i % kDiv, j = kOwn == 1 ? 0 : i / kLanes;
+      const float d = __shfl_sync(0xffffffffu, dt[j], from);
+      const float u = __shfl_sync(0xffffffffu, dt[j] * x[j], from);
+      float v = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        s[i][k] = fmaf(ex2(d * (A[i][k] * kLog2e)), s[i][k], u * Bv[k]);
+        v = fmaf(s[i][k], Cv[k], v);
+      }
+#pragma unroll
+      for (int o = kLanes / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (me % kDiv == i % kDiv) y[j] = v;
+    }
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) {
+      y[j] = fmaf(D[j], x[j], y[j]);
+      if (a.z.p) y[j] *= silu_f(z[j]);
+      if ((kLanes <= kStepCh || me < kStepCh) && (kWhole || own[j] < a.d))
+        static_cast<T*>(a.out.p)[rows.b * a.out.sb + h * a.out.sh + own[j]] = from_f32<T>(y[j]);
     }
   } while (rows.next_row());
-  if (whole) {
-    *reinterpret_cast<float4*>(sp) = make_float4(s[0], s[1], s[2], s[3]);
-  } else {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (k < left) sp[k] = s[k];
+  for (int i = 0; i < kStepCh; ++i) {
+    const int c = c0 + i * groups;
+    if (kWhole || c < a.d) write_row<kWhole, float, 4>(sp + (int64_t)c * a.N, left, whole, s[i]);
   }
 }
 
+template <typename T, int kLanes>
+__global__ void __launch_bounds__(kStepThreads) step_kernel(const __grid_constant__ ScanStepArgs a, int cts) {
+  constexpr int per = kStepThreads / kLanes * kStepCh;
+  SlotRows rows;
+  if (!rows.begin(a.slots, blockIdx.y, a.B, a.S, a.status)) return;
+  const int h = blockIdx.x / cts, first = blockIdx.x % cts * per;
+  if (a.wide && a.rows_wide && a.N == 4 * kLanes && first + per <= a.d) step_rows<T, kLanes, true>(a, rows, h, first);
+  else step_rows<T, kLanes, false>(a, rows, h, first);
+}
+
+template <typename T, int kLanes>
+cudaError_t step_as(const ScanStepArgs& a, cudaStream_t s) {
+  constexpr int per = kStepThreads / kLanes * kStepCh;
+  const int cts = (a.d + per - 1) / per;
+  step_kernel<T, kLanes><<<dim3((unsigned)(a.H * cts), a.B), kStepThreads, 0, s>>>(a, cts);
+  return cudaGetLastError();
+}
 template <typename T>
 cudaError_t step(const ScanStepArgs& a, cudaStream_t s) {
-  int lanes = 1;
-  while (lanes * 4 < a.N) lanes *= 2;
-  const int per = kStepThreads / lanes, cts = (a.d + per - 1) / per;
-  step_kernel<T><<<dim3((unsigned)(a.H * cts), a.B), kStepThreads, 0, s>>>(a, lanes, cts);
-  return cudaGetLastError();
+  if (a.N <= 4) return step_as<T, 1>(a, s);
+  if (a.N <= 8) return step_as<T, 2>(a, s);
+  if (a.N <= 16) return step_as<T, 4>(a, s);
+  if (a.N <= 32) return step_as<T, 8>(a, s);
+  return step_as<T, 16>(a, s);
 }
 
 }  // namespace
