@@ -7,11 +7,14 @@
 // C function's address (from the loaded library), `tensors` a tuple of tensors
 // or None, the scalar argument goes behind the first `split` of them. `stream`
 // is None for the tensors' device's current stream, or a stream's handle.
+#include <ATen/ATen.h>
+#include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
+#include <array>
 #include <utility>
 
 #include "../../include/ttt.h"
@@ -122,7 +125,42 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   return PyLong_FromLong(st);
 }
 
+// A new token tensor [B,H,T,d] in x's order of storage (heads before or behind
+// tokens), its rows a multiple of 16 bytes apart.
+PyObject* like_tokens(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+  if (nargs != 4 || !THPVariable_Check(args[0]) || !THPDtype_Check(args[2])) {
+    PyErr_SetString(PyExc_TypeError, "like_tokens(x, d, dtype, zero)");
+    return nullptr;
+  }
+  const at::Tensor& x = THPVariable_Unpack(args[0]);
+  const int64_t d = PyLong_AsLongLong(args[1]);
+  const auto type = reinterpret_cast<THPDtype*>(args[2])->scalar_type;
+  const int zero = PyObject_IsTrue(args[3]);
+  if (PyErr_Occurred()) return nullptr;
+  if (x.dim() != 4 || d < 0) {
+    PyErr_SetString(PyExc_ValueError, "tokens are [B,H,T,d]");
+    return nullptr;
+  }
+  try {
+    const int64_t B = x.size(0), H = x.size(1), T = x.size(2);
+    const int64_t per = 16 / (int64_t)c10::elementSize(type), row = (d + per - 1) / per * per;
+    const bool behind = H > 1 && T > 1 && x.stride(1) < x.stride(2);
+    const auto opt = x.options().dtype(type).requires_grad(false);
+    const std::array<int64_t, 4> size = {B, H, T, row};
+    const std::array<int64_t, 4> stride = {H * T * row, behind ? row : T * row, behind ? H * row : row, 1};
+    at::Tensor t = at::empty_strided(size, stride, opt);
+    if (zero) t.zero_();
+    if (row != d) t = t.slice(3, 0, d);
+    return THPVariable_Wrap(t);
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+    return nullptr;
+  }
+}
+
 PyMethodDef methods[] = {
+    {"like_tokens", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(like_tokens)), METH_FASTCALL,
+     "like_tokens(x, d, dtype, zero) -> tensor"},
     {"call", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(call)), METH_FASTCALL,
      "call(function, tensors, split, scalar, stream, name) -> status"},
     {nullptr, nullptr, 0, nullptr}};

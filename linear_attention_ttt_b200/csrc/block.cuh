@@ -414,23 +414,24 @@ struct SlotRows {
   }
 };
 
-// out(col, sum over p of ws[p * cols + col]): 8 columns a block (a sector of
-// memory), 64 threads a column, each summing every 64th part in order, then a
-// fixed tree: the result does not depend on scheduling.
-constexpr int kSumCols = 8, kSumRows = 64;
-template <typename Out>
-__global__ void __launch_bounds__(kSumCols * kSumRows)
+// out(col, sum over p of ws[p * cols + col]): kRows threads a column, each
+// summing every kRows-th part in order, then a fixed tree: the result does not
+// depend on scheduling. Few columns go 8 a block (a sector of memory) with 64
+// threads each, many (from 16384, where 8 a block would leave blocks too short)
+// 32 with 16.
+template <int kCols, int kRows, typename Out>
+__global__ void __launch_bounds__(kCols * kRows)
     sum_parts_kernel(const float* __restrict__ ws, int64_t parts, int64_t cols, Out out) {
-  __shared__ float part[kSumRows][kSumCols];
-  const int c = threadIdx.x % kSumCols, r = threadIdx.x / kSumCols;
-  const int64_t col = (int64_t)blockIdx.x * kSumCols + c;
+  __shared__ float part[kRows][kCols];
+  const int c = threadIdx.x % kCols, r = threadIdx.x / kCols;
+  const int64_t col = (int64_t)blockIdx.x * kCols + c;
   float s = 0.f;
   if (col < cols) {
 #pragma unroll 8
-    for (int64_t p = r; p < parts; p += kSumRows) s += ws[p * cols + col];
+    for (int64_t p = r; p < parts; p += kRows) s += ws[p * cols + col];
   }
   part[r][c] = s;
-  for (int h = kSumRows / 2; h; h /= 2) {
+  for (int h = kRows / 2; h; h /= 2) {
     __syncthreads();
     if (r < h) part[r][c] += part[r + h][c];
   }
@@ -438,8 +439,10 @@ __global__ void __launch_bounds__(kSumCols * kSumRows)
 }
 template <typename Out>
 cudaError_t sum_parts(const float* ws, int64_t parts, int64_t cols, Out out, cudaStream_t s) {
-  sum_parts_kernel<<<(unsigned)((cols + kSumCols - 1) / kSumCols), kSumCols * kSumRows, 0, s>>>(
-      ws, parts, cols, out);
+  if (cols < 16384)
+    sum_parts_kernel<8, 64><<<(unsigned)((cols + 7) / 8), 512, 0, s>>>(ws, parts, cols, out);
+  else
+    sum_parts_kernel<32, 16><<<(unsigned)((cols + 31) / 32), 512, 0, s>>>(ws, parts, cols, out);
   return cudaGetLastError();
 }
 

@@ -131,11 +131,11 @@ __device__ __forceinline__ void load_taps(const float* w, const float* bias, int
   float f[kV], g[K][kV];
 #pragma unroll
   for (int j = 0; j < kV; ++j) {
-    const int64_t c = (int64_t)r.h * d + r.c + j;
-    const bool in = j < r.n;
-    f[j] = in && bias ? bias[c] : 0.f;
+    // channels behind the row's end read its last: nothing of theirs is kept
+    const int64_t c = (int64_t)r.h * d + min(r.c + j, d - 1);
+    f[j] = bias ? bias[c] : 0.f;
 #pragma unroll
-    for (int i = 0; i < K; ++i) g[i][j] = in ? w[c * K + i] : 0.f;
+    for (int i = 0; i < K; ++i) g[i][j] = w[c * K + i];
   }
   pairs_of(f, b);
 #pragma unroll
@@ -237,7 +237,7 @@ __global__ void conv_empty_kernel(Seqs q, int T_, int H, int d, int rows, TokVie
   const T* s = static_cast<const T*>(src.p);
   T* o = static_cast<T*>(dst.p);
   const int64_t n = (int64_t)H * rows * d;
-  for (int64_t i = threadIdx.x; i < n; i += blockDim.x) {
+  for (int64_t i = (int64_t)blockIdx.y * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.y * blockDim.x) {
     const int c = (int)(i % d), k = (int)(i / d % rows), h = (int)(i / d / rows);
     o[seq * dst.sb + h * dst.sh + k * dst.st + c] =
         s ? s[seq * src.sb + h * src.sh + k * src.st + c] : from_f32<T>(0.f);
@@ -248,7 +248,10 @@ template <typename T>
 cudaError_t copy_empty(const Seqs& q, int T_, int H, int d, int K, const TokView& src, const RowsView& dst,
                        int* status, cudaStream_t s) {
   if (!q.cu && (T_ > 0 || !dst.p)) return cudaSuccess;
-  conv_empty_kernel<T><<<q.S, 256, 0, s>>>(q, T_, H, d, K - 1, src, dst, status);
+  // mostly there is nothing to copy: a block for 1024 values, up to 16 a sequence
+  const int64_t n = (int64_t)H * (K - 1) * d, rows = (n + 1023) / 1024;
+  const dim3 g(q.S, (unsigned)(!dst.p || rows < 1 ? 1 : rows < 16 ? rows : 16));
+  conv_empty_kernel<T><<<g, 256, 0, s>>>(q, T_, H, d, K - 1, src, dst, status);
   return cudaGetLastError();
 }
 

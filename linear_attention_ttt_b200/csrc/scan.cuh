@@ -134,6 +134,15 @@ __device__ __forceinline__ void spread_part(float* dst, const T* src, int tid) {
   }
 }
 
+// Element (channel c of the block, state n) of a [H,d,N] array whose rows begin
+// at `row`; 0 where there is none. The read itself is always made (in bounds):
+// reads behind a choice would wait for one another.
+__device__ __forceinline__ float state_at(const ScanArgs& a, const Place& q, const float* p, int64_t row, int n, int c) {
+  const int cc = min(q.c0 + c, a.d - 1) - q.c0, nn = min(n, a.N - 1);
+  const float v = p[(row + q.ch0 + cc) * a.N + nn];
+  return nn == n && cc == c ? v : 0.f;
+}
+
 // The lane's decay rates, in powers of two.
 __device__ __forceinline__ void rates(const ScanArgs& a, const Place& q, f2 (&A2)[4]) {
 #pragma unroll
@@ -142,7 +151,7 @@ __device__ __forceinline__ void rates(const ScanArgs& a, const Place& q, f2 (&A2
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int n = q.wn * kNB + q.sg * 4 + k, c = q.wt * kCh + q.cg * 2 + i;
-      r[i] = n < a.N && q.c0 + c < a.d ? a.A[(q.ch0 + c) * a.N + n] * kLog2e : 0.f;
+      r[i] = state_at(a, q, a.A, 0, n, c) * kLog2e;
     }
     A2[k] = mk2(r[0], r[1]);
   }
@@ -157,7 +166,7 @@ __device__ __forceinline__ void seq_state(const ScanArgs& a, const Place& q, con
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int n = q.wn * kNB + q.sg * 4 + k, c = q.wt * kCh + q.cg * 2 + i;
-      r[i] = p && n < a.N && q.c0 + c < a.d ? p[((int64_t)seq * a.H * a.d + q.ch0 + c) * a.N + n] : 0.f;
+      r[i] = p ? state_at(a, q, p, (int64_t)seq * a.H * a.d, n, c) : 0.f;
     }
     s[k] = mk2(r[0], r[1]);
   }

@@ -81,8 +81,9 @@ __global__ void __launch_bounds__(128, sizeof(T) == 2 ? 4 : 3)
   float bias[4], skip[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    bias[j] = a.dt_bias && j < vn ? a.dt_bias[q.ch0 + vc + j] : 0.f;
-    skip[j] = !kPre && a.D && j < vn ? a.D[q.ch0 + vc + j] : 0.f;
+    const int64_t c = (int64_t)q.h * a.d + min(q.c0 + vc + j, a.d - 1);
+    bias[j] = a.dt_bias ? a.dt_bias[c] : 0.f;
+    skip[j] = !kPre && a.D ? a.D[c] : 0.f;
   }
   const T* xp = static_cast<const T*>(a.x.p) + q.b * a.x.sb + q.h * a.x.sh + q.c0;
   const T* dp = static_cast<const T*>(a.dt.p) + q.b * a.dt.sb + q.h * a.dt.sh + q.c0;
@@ -258,10 +259,11 @@ __global__ void join_kernel(ScanArgs a, Plan p, float* states, const float* __re
     bool cut[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      const bool in = i0 + j + 1 < p.chunks;  // the last chunk passes nothing on
-      local[j] = in ? states[(i0 + j) * per + e] : 0.f;
-      dec[j] = in ? ex2(A2 * sum[(i0 + j) * row]) : 0.f;
-      cut[j] = in && cuts[i0 + j];
+      // the last chunk passes nothing on; its place reads the one before
+      const int i = min(i0 + j, p.chunks - 2);
+      local[j] = states[i * per + e];
+      dec[j] = ex2(A2 * sum[i * row]);
+      cut[j] = cuts[i];
     }
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
@@ -304,7 +306,7 @@ __global__ void copy_empty_kernel(Seqs q, int T, int64_t n, const float* src, fl
   int lo = 0, hi = T;
   if (q.cu) packed_seq(q.cu, blockIdx.x, T, status, &lo, &hi);
   if (hi > lo || !dst) return;
-  for (int64_t i = threadIdx.x; i < n; i += blockDim.x)
+  for (int64_t i = (int64_t)blockIdx.y * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.y * blockDim.x)
     dst[blockIdx.x * n + i] = src ? src[blockIdx.x * n + i] : 0.f;
 }
 
@@ -419,7 +421,10 @@ cudaError_t step(const ScanStepArgs& a, cudaStream_t s) {
 cudaError_t copy_empty_states(const Seqs& q, int T, int64_t n, const float* src, float* dst, int* status,
                               cudaStream_t s) {
   if (!q.cu && (T > 0 || !dst)) return cudaSuccess;
-  copy_empty_kernel<<<q.S, 256, 0, s>>>(q, T, n, src, dst, status);
+  // mostly there is nothing to copy: a block for 2048 values, up to 16 a sequence
+  const int64_t rows = (n + 2047) / 2048;
+  const dim3 g(q.S, (unsigned)(!dst || rows < 1 ? 1 : rows < 16 ? rows : 16));
+  copy_empty_kernel<<<g, 256, 0, s>>>(q, T, n, src, dst, status);
   return cudaGetLastError();
 }
 

@@ -179,9 +179,10 @@ __device__ __forceinline__ void stage(const ScanArgs& a, const TokView& dy, cons
   else stage_as<false, T>(a, dy, q, tb, live, bias, s);
 }
 
-__device__ __forceinline__ void four_of(const float* p, int n, float (&f)[4]) {
+// Four parameters of the channels from c on (head h), zeros for null.
+__device__ __forceinline__ void four_of(const float* p, const ScanArgs& a, int h, int c, float (&f)[4]) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) f[j] = p && j < n ? p[j] : 0.f;
+  for (int j = 0; j < 4; ++j) f[j] = p ? p[(int64_t)h * a.d + min(c + j, a.d - 1)] : 0.f;
 }
 
 // First pass over a chunk: start states of its parts from a zero start, sums
@@ -203,7 +204,7 @@ __global__ void __launch_bounds__(128, 4) pre_kernel(ScanBwdArgs ga, Plan p, Ws 
   float bias[4];
   {
     const int vc = q.tid % (S::cw / 4) * 4;
-    four_of(a.dt_bias ? a.dt_bias + q.ch0 + vc : nullptr, a.d - q.c0 - vc, bias);
+    four_of(a.dt_bias, a, q.h, q.c0 + vc, bias);
   }
   bool open = true;  // the sequence that enters the chunk has not ended
   const int lane_c = q.wt * kCh + q.cg * 2, lane_s = q.wn * 2 * kNB + q.sg * 8;
@@ -294,10 +295,10 @@ __global__ void join_kernel(ScanArgs a, Plan p, Ws ws) {
       float local[kAhead], dec[kAhead];
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
-        const int64_t i = way ? p.chunks - 1 - (i0 + j) : i0 + j;
-        const bool in = i0 + j < p.chunks;
-        local[j] = in ? x[i * per] : 0.f;
-        dec[j] = in ? ex2(A2 * total[i * row]) : 0.f;
+        const int k = min(i0 + j, p.chunks - 1);
+        const int64_t i = way ? p.chunks - 1 - k : k;
+        local[j] = x[i * per];
+        dec[j] = ex2(A2 * total[i * row]);
       }
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
@@ -439,8 +440,8 @@ __global__ void __launch_bounds__(128, 3) main_kernel(const __grid_constant__ Sc
   const int vc = q.tid % kGroups * 4, vn = a.d - q.c0 - vc;
   float bias[4], sD[4] = {0.f, 0.f, 0.f, 0.f}, sbias[4] = {0.f, 0.f, 0.f, 0.f};
   float dskip[4];
-  four_of(a.dt_bias ? a.dt_bias + q.ch0 + vc : nullptr, vn, bias);
-  four_of(a.D ? a.D + q.ch0 + vc : nullptr, vn, dskip);
+  four_of(a.dt_bias, a, q.h, q.c0 + vc, bias);
+  four_of(a.D, a, q.h, q.c0 + vc, dskip);
   const float ln2 = 0.6931471805599453f;
   const int lane_c = q.wt * kCh + q.cg * 2, lane_s = q.wn * 2 * kNB + q.sg * 8;
   WarpMem mem;

@@ -315,7 +315,16 @@ def lact_swiglu_window_fwd(q, k, v, eta, W1, W2, W3, chunk: int, update_rule: in
 
 # ---- the recurrent block: RMS norm, short convolution, selective scan ---------
 
-_ADDRESS = {}  # of the loaded library's functions
+_ADDRESS = {}  # of the loaded library's functions, by name; and the native binding's two
+
+
+def _load_binding():
+    try:
+        from . import _binding
+    except ImportError as e:
+        raise OSError(f"{_PKG}/_binding.so is missing or does not load: run "
+                      f"`python -m linear_attention_ttt_b200.build`") from e
+    _ADDRESS["call"], _ADDRESS["like_tokens"] = _binding.call, _binding.like_tokens
 
 
 def _block_call(name, tensors, split, scalar, stream):
@@ -325,13 +334,12 @@ def _block_call(name, tensors, split, scalar, stream):
     stream. csrc/binding.cpp does the marshalling."""
     address = _ADDRESS.get(name)
     if address is None:
-        from . import _binding
-        _ADDRESS[""] = _binding.call
+        _load_binding()
         address = ctypes.cast(getattr(load(), name), ctypes.c_void_p).value
         _ADDRESS[name] = address
     if stream is not None:
         stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    code = _ADDRESS[""](address, tensors, split, scalar, stream, name)
+    code = _ADDRESS["call"](address, tensors, split, scalar, stream, name)
     if code != 0:
         raise TTTError(code, name)
 
@@ -339,18 +347,9 @@ def _block_call(name, tensors, split, scalar, stream):
 def _like_tokens(x, d=None, dtype=None, zero=False):
     """A new token tensor [B,H,T,d] with x's order of storage (heads before or behind
     tokens) and rows of a multiple of 16 bytes."""
-    if not zero and d is None and x.is_contiguous() and x.shape[3] * (dtype or x.dtype).itemsize % 16 == 0:
-        return torch.empty_like(x, dtype=dtype)
-    B, H, T = x.shape[:3]
-    d = x.shape[3] if d is None else d
-    dtype = dtype or x.dtype
-    pad = -d % (16 // dtype.itemsize)
-    make = torch.zeros if zero else torch.empty
-    if H > 1 and T > 1 and x.stride(1) < x.stride(2):
-        t = make((B, T, H, d + pad), dtype=dtype, device=x.device).transpose(1, 2)
-    else:
-        t = make((B, H, T, d + pad), dtype=dtype, device=x.device)
-    return t[..., :d] if pad else t
+    if not _ADDRESS:
+        _load_binding()
+    return _ADDRESS["like_tokens"](x, x.shape[3] if d is None else d, dtype or x.dtype, zero)
 
 
 def _conv_state(x, S, K):
