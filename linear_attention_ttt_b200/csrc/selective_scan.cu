@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(128, sizeof(T) == 2 ? 4 : 3)
       }
     };
     if (nt == kPart && !(now.begin | now.end)) {
-#pragma unroll 1
+#pragma unroll 4
       for (int t = 0; t < kPart; t += 4) block(t, false);
     } else {
 #pragma unroll 1
