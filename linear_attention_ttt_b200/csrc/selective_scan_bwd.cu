@@ -41,7 +41,7 @@ Plan plan(const ScanArgs& a) {
   // Measured against this, chunks of 1 to 64 parts: B4 T2048 d4096 takes 1327 us
   // at its best (3 parts; 4 parts, which this picks, 1351; 1 part 1457, 64 parts
   // 1816), B1 T2048 d4096 394 us (3 parts; 2, picked, 424; 64 parts 1396).
-  const double slots = 148 * 3;
+  const double slots = 148 * 2;
   double best = 0;
   p.chunk = 1;
   for (int c = 1; c <= p.parts && c <= 1024; ++c) {
@@ -101,7 +101,7 @@ struct Shared {
   // A warp's states before every block but the last; a block's dB, dC [4][32]
   // take the place of its states, the last block's have room of their own.
   float keep[kPre ? 4 : wpb * ((kBlocks - 1) * kPiece + kBlk * 32)];
-  float red[kPre ? 4 : wpb * 256];                     // a token's dB, dC on their way over lanes
+  float red[kPre ? 4 : wpb * kBlk * 256];              // a block's dB, dC on their way over lanes
   int seq[kPart];
 };
 
@@ -389,17 +389,21 @@ __device__ __forceinline__ void back_block(const ScanBwdArgs& ga, Shared<W, fals
       dC[k] = lo + hi;
     }
     if (kEvents && (m.begin >> t & 1) && ga.dh0) put_state(a, q, ga.dh0, s.seq[t], gs);
-    // dB, dC over the warp's 8 channel lanes, through memory: a value a lane
-    // (which = lane / 16 of state lane % 16)
-    *reinterpret_cast<float4*>(red + q.cg * 32 + q.sg * 4) = make_float4(dB[0], dB[1], dB[2], dB[3]);
-    *reinterpret_cast<float4*>(red + q.cg * 32 + 16 + q.sg * 4) = make_float4(dC[0], dC[1], dC[2], dC[3]);
-    __syncwarp();
-    float v = red[q.lane];
-#pragma unroll
-    for (int c = 1; c < 8; ++c) v += red[c * 32 + q.lane];
-    out[i * 32 + q.lane] = v;
-    __syncwarp();
+    // dB, dC on their way over the warp's 8 channel lanes
+    *reinterpret_cast<float4*>(red + i * 256 + q.cg * 32 + q.sg * 4) = make_float4(dB[0], dB[1], dB[2], dB[3]);
+    *reinterpret_cast<float4*>(red + i * 256 + q.cg * 32 + 16 + q.sg * 4) = make_float4(dC[0], dC[1], dC[2], dC[3]);
   }
+  // a value a lane of every token: which = lane / 16 of state lane % 16
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < kBlk; ++i) {
+    if (kEvents && blk * kBlk + i >= nt) continue;
+    float v[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) v[c] = red[i * 256 + c * 32 + q.lane];
+    out[i * 32 + q.lane] = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+  }
+  __syncwarp();
   // the four tokens' sums over the tile's state lanes: halve twice, a token a lane is left
   const bool up = q.sg & 1, up2 = q.sg & 2;
   const int t = blk * kBlk + (up ? 2 : 0) + (up2 ? 1 : 0);
@@ -421,7 +425,7 @@ __device__ __noinline__ void back_block_events(const ScanBwdArgs& ga, Shared<W, 
 }
 
 template <typename T, int W>
-__global__ void __launch_bounds__(128, 3) main_kernel(const __grid_constant__ ScanBwdArgs ga, Plan p, Ws ws) {
+__global__ void __launch_bounds__(128, 2) main_kernel(const __grid_constant__ ScanBwdArgs ga, Plan p, Ws ws) {
   using S = Shared<W, false>;
   constexpr int cw = S::cw, ns = S::ns, wpb = S::wpb;
   constexpr int kGroups = cw / 4, dr = S::threads / kGroups;
@@ -449,7 +453,7 @@ __global__ void __launch_bounds__(128, 3) main_kernel(const __grid_constant__ Sc
   mem.r = W == 1 ? s.u + q.wt * kCh : s.ry + q.warp * kPart * kCh;
   mem.y = W == 1 ? s.e + q.wt * kCh : s.ry + (wpb + q.warp) * kPart * kCh;
   mem.keep = s.keep + q.warp * ((S::kBlocks - 1) * kPiece + kBlk * 32);
-  mem.red = s.red + q.warp * 256;
+  mem.red = s.red + q.warp * kBlk * 256;
 
   const int part0 = chunk * p.chunk, part1 = min(p.parts, part0 + p.chunk);
   for (int part = part1 - 1; part >= part0; --part) {
@@ -524,51 +528,69 @@ __global__ void __launch_bounds__(128, 3) main_kernel(const __grid_constant__ Sc
     const float* y0 = W == 1 ? s.e : s.ry + wpb * kPart * kCh;
     auto finish = [&](auto whole) {
       constexpr bool kWhole = decltype(whole)::value;
+      constexpr int kTurns = (kPart + dr - 1) / dr;
+      const int64_t t0 = tb;
+      const T* xp = static_cast<const T*>(a.x.p) + q.b * a.x.sb + q.h * a.x.sh + q.c0 + vc;
+      const T* dp = static_cast<const T*>(a.dt.p) + q.b * a.dt.sb + q.h * a.dt.sh + q.c0 + vc;
+      const T* gp = static_cast<const T*>(ga.dy.p) + q.b * ga.dy.sb + q.h * ga.dy.sh + q.c0 + vc;
+      // without a gate the gradient stands in its place and is not used
+      const bool gate = a.z.p != nullptr;
+      const T* zp = gate ? static_cast<const T*>(a.z.p) + q.b * a.z.sb + q.h * a.z.sh + q.c0 + vc : gp;
+      const int64_t zs = gate ? a.z.st : ga.dy.st;
+      float x[kTurns][4], w[kTurns][4], e[kTurns][4], z[kTurns][4];
 #pragma unroll
-      for (int r = 0; r < kPart; r += dr) {
-        const int row = r + q.tid / kGroups;
+      for (int i = 0; i < kTurns; ++i) {
+        const int row = min(i * dr + q.tid / kGroups, kPart - 1);
+        const int n = kWhole || m.live >> row & 1 ? vn : 0;
+        const int64_t t = t0 + row;
+        read_row<kWhole, T, 4>(xp + t * a.x.st, n, a.wide, x[i]);
+        read_row<kWhole, T, 4>(dp + t * a.dt.st, n, a.wide, w[i]);
+        read_row<kWhole, T, 4>(gp + t * ga.dy.st, n, a.wide, e[i]);
+        read_row<kWhole, T, 4>(zp + t * zs, n, a.wide, z[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < kTurns; ++i) {
+        const int row = i * dr + q.tid / kGroups;
         if (kPart % dr != 0 && row >= kPart) break;
         if (!kWhole && (!(m.live >> row & 1) || vn <= 0)) continue;
-        const int64_t t = tb + row;
+        const int64_t t = t0 + row;
         auto joined = [&](const float* base, float (&v)[4]) {  // over a tile's warps
           const float* at = W == 1 ? base + row * cw + vc : base + (vc / kCh * W * kPart + row) * kCh + vc % kCh;
-          float4 x = *reinterpret_cast<const float4*>(at);
+          float4 f = *reinterpret_cast<const float4*>(at);
 #pragma unroll
-          for (int w = 1; w < W; ++w) {
-            const float4 o = *reinterpret_cast<const float4*>(at + w * kPart * kCh);
-            x.x += o.x, x.y += o.y, x.z += o.z, x.w += o.w;
+          for (int k = 1; k < W; ++k) {
+            const float4 o = *reinterpret_cast<const float4*>(at + k * kPart * kCh);
+            f.x += o.x, f.y += o.y, f.z += o.z, f.w += o.w;
           }
-          v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+          v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
         };
-        float x[4], w[4], e[4], z[4], gb[4], gr[4], y[4], o[4];
-        read_row<kWhole, T, 4>(static_cast<const T*>(a.x.p) + q.b * a.x.sb + q.h * a.x.sh + q.c0 + vc + t * a.x.st, vn, a.wide, x);
-        read_row<kWhole, T, 4>(static_cast<const T*>(a.dt.p) + q.b * a.dt.sb + q.h * a.dt.sh + q.c0 + vc + t * a.dt.st, vn, a.wide, w);
-        read_row<kWhole, T, 4>(static_cast<const T*>(ga.dy.p) + q.b * ga.dy.sb + q.h * ga.dy.sh + q.c0 + vc + t * ga.dy.st, vn, a.wide, e);
-        if (a.z.p)
-          read_row<kWhole, T, 4>(static_cast<const T*>(a.z.p) + q.b * a.z.sb + q.h * a.z.sh + q.c0 + vc + t * a.z.st, vn, a.wide, z);
+        float gb[4], gr[4], y[4], o[4];
         joined(q0, gb);
         joined(r0, gr);
-        if (a.z.p) {
+        if (gate) {
           joined(y0, y);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            o[j] = e[j] * fmaf(dskip[j], x[j], y[j]) * dsilu_f(z[j]);
-            e[j] *= silu_f(z[j]);
+            o[j] = e[i][j] * fmaf(dskip[j], x[i][j], y[j]) * dsilu_f(z[i][j]);
+            e[i][j] *= silu_f(z[i][j]);
           }
-          write_row<kWhole, T, 4>(static_cast<T*>(ga.dz.p) + q.b * ga.dz.sb + q.h * ga.dz.sh + q.c0 + vc + t * ga.dz.st, vn, a.wide, o);
+          write_row<kWhole, T, 4>(static_cast<T*>(ga.dz.p) + q.b * ga.dz.sb + q.h * ga.dz.sh + q.c0 + vc + t * ga.dz.st, vn,
+                                  a.wide, o);
         }
         const float4 d = *reinterpret_cast<const float4*>(s.dt + row * cw + vc);
-        o[0] = fmaf(dskip[0], e[0], d.x * gb[0]), o[1] = fmaf(dskip[1], e[1], d.y * gb[1]);
-        o[2] = fmaf(dskip[2], e[2], d.z * gb[2]), o[3] = fmaf(dskip[3], e[3], d.w * gb[3]);
-        write_row<kWhole, T, 4>(static_cast<T*>(ga.dx.p) + q.b * ga.dx.sb + q.h * ga.dx.sh + q.c0 + vc + t * ga.dx.st, vn, a.wide, o);
+        o[0] = fmaf(dskip[0], e[i][0], d.x * gb[0]), o[1] = fmaf(dskip[1], e[i][1], d.y * gb[1]);
+        o[2] = fmaf(dskip[2], e[i][2], d.z * gb[2]), o[3] = fmaf(dskip[3], e[i][3], d.w * gb[3]);
+        write_row<kWhole, T, 4>(static_cast<T*>(ga.dx.p) + q.b * ga.dx.sb + q.h * ga.dx.sh + q.c0 + vc + t * ga.dx.st, vn,
+                                a.wide, o);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          o[j] = fmaf(x[j], gb[j], gr[j] * ln2);  // the rates are in powers of two
-          if (a.softplus) o[j] *= sigmoid_f(w[j] + bias[j]);
-          sD[j] = fmaf(e[j], x[j], sD[j]);
+          o[j] = fmaf(x[i][j], gb[j], gr[j] * ln2);  // the rates are in powers of two
+          if (a.softplus) o[j] *= sigmoid_f(w[i][j] + bias[j]);
+          sD[j] = fmaf(e[i][j], x[i][j], sD[j]);
           sbias[j] += o[j];
         }
-        write_row<kWhole, T, 4>(static_cast<T*>(ga.ddt.p) + q.b * ga.ddt.sb + q.h * ga.ddt.sh + q.c0 + vc + t * ga.ddt.st, vn, a.wide, o);
+        write_row<kWhole, T, 4>(static_cast<T*>(ga.ddt.p) + q.b * ga.ddt.sb + q.h * ga.ddt.sh + q.c0 + vc + t * ga.ddt.st, vn,
+                                a.wide, o);
       }
     };
     if (is_whole<S>(a, q, m.live)) finish(std::true_type());
