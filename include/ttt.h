@@ -387,7 +387,7 @@ ttt_status lact_swiglu_window_fwd(const ttt_tensor* q, const ttt_tensor* k, cons
  * device) B is 1 and sequence i is the tokens cu_seqlens[i] ..
  * cu_seqlens[i+1]-1 of the T packed ones; it may be empty. Sequences share
  * nothing: each starts from its own row of the [S,...] state tensors. Token
- * rows behind the last sequence are neither read nor written. The offsets
+ * rows behind the last sequence are not used and not written. The offsets
  * must not decrease and lie in [0, T]. Where they break this nothing outside
  * the tensors is touched and ttt_get_device_status reports TTT_ERR_BOUNDS,
  * but which of the call's sequences are computed is not specified.

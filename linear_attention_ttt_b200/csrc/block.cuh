@@ -342,6 +342,86 @@ __device__ __forceinline__ f2 ex2_pair(f2 x) {
   return mk2(ex2(a), ex2(b));
 }
 
+// Four channels of a token row as they lie in memory, and as two fp32 pairs.
+constexpr int kV = 4;
+template <typename T>
+struct Raw {
+  using type = uint2;
+};
+template <>
+struct Raw<float> {
+  using type = uint4;
+};
+// kWhole: all four exist and are aligned (see read_row).
+template <bool kWhole, typename T>
+__device__ __forceinline__ typename Raw<T>::type raw_row(const T* p, int n, bool wide) {
+  if constexpr (kWhole) {
+    return *reinterpret_cast<const typename Raw<T>::type*>(p);
+  } else {
+    float f[kV];
+    load_row<T, kV>(p, n, wide, f);
+    if constexpr (sizeof(T) == 4) {
+      return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    } else {  // exact: the values came from bf16
+      return make_uint2(__float_as_uint(f[0]) >> 16 | (__float_as_uint(f[1]) & 0xffff0000u),
+                        __float_as_uint(f[2]) >> 16 | (__float_as_uint(f[3]) & 0xffff0000u));
+    }
+  }
+}
+__device__ __forceinline__ void pairs_of(uint4 r, f2 (&v)[2]) {
+  v[0] = mk2(__uint_as_float(r.x), __uint_as_float(r.y));
+  v[1] = mk2(__uint_as_float(r.z), __uint_as_float(r.w));
+}
+__device__ __forceinline__ void pairs_of(uint2 r, f2 (&v)[2]) {
+  v[0] = mk2(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u));
+  v[1] = mk2(__uint_as_float(r.y << 16), __uint_as_float(r.y & 0xffff0000u));
+}
+__device__ __forceinline__ void floats_of(const f2 (&v)[2], float (&f)[kV]) {
+  un2(v[0], f[0], f[1]);
+  un2(v[1], f[2], f[3]);
+}
+__device__ __forceinline__ void pairs_of(const float (&f)[kV], f2 (&v)[2]) {
+  v[0] = mk2(f[0], f[1]);
+  v[1] = mk2(f[2], f[3]);
+}
+
+// The same where a piece may be missing or ragged: first all of a thread's
+// reads by predicated instructions (whole: the piece is whole and aligned), so
+// that they are in flight together; then raw_rest() for each, which reads the
+// pieces that are neither whole nor empty one element after another.
+template <typename T>
+__device__ __forceinline__ typename Raw<T>::type raw_whole(const T* p, bool whole) {
+  typename Raw<T>::type r;
+  if constexpr (sizeof(T) == 2) {
+    r = make_uint2(0, 0);
+    asm volatile("{\n .reg .pred p;\n setp.ne.s32 p, %3, 0;\n @p ld.global.v2.u32 {%0, %1}, [%2];\n}\n"
+                 : "+r"(r.x), "+r"(r.y)
+                 : "l"(p), "r"((int)whole));
+  } else {
+    r = make_uint4(0, 0, 0, 0);
+    asm volatile("{\n .reg .pred p;\n setp.ne.s32 p, %5, 0;\n @p ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n}\n"
+                 : "+r"(r.x), "+r"(r.y), "+r"(r.z), "+r"(r.w)
+                 : "l"(p), "r"((int)whole));
+  }
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void raw_rest(typename Raw<T>::type& r, const T* p, int n, bool wide) {
+  if (n > 0 && !(wide && n >= kV)) r = raw_row<false, T>(p, n, false);
+}
+__device__ __forceinline__ void floats_of(uint2 r, float (&f)[kV]) {
+  f[0] = __uint_as_float(r.x << 16);
+  f[1] = __uint_as_float(r.x & 0xffff0000u);
+  f[2] = __uint_as_float(r.y << 16);
+  f[3] = __uint_as_float(r.y & 0xffff0000u);
+}
+__device__ __forceinline__ void floats_of(uint4 r, float (&f)[kV]) {
+  f[0] = __uint_as_float(r.x);
+  f[1] = __uint_as_float(r.y);
+  f[2] = __uint_as_float(r.z);
+  f[3] = __uint_as_float(r.w);
+}
+
 // Sequence i of a packed call, its offsets clamped into [0, T]; empty (lo =
 // hi) where they decrease or leave the range, which is recorded.
 __device__ __forceinline__ void packed_seq(const int32_t* cu, int i, int T, int* status, int* lo,

@@ -63,61 +63,21 @@ __device__ __forceinline__ bool next_piece(const Seqs& q, const Run& r, int T, i
   return false;
 }
 
-// Four channels of a token row as they lie in memory, and as two fp32 pairs.
-constexpr int kV = 4;
-template <typename T>
-struct Raw {
-  using type = uint2;
-};
-template <>
-struct Raw<float> {
-  using type = uint4;
-};
-// kWhole: all four exist and are aligned (see read_row).
-template <bool kWhole, typename T>
-__device__ __forceinline__ typename Raw<T>::type raw_row(const T* p, int n, bool wide) {
-  if constexpr (kWhole) {
-    return *reinterpret_cast<const typename Raw<T>::type*>(p);
-  } else {
-    float f[kV];
-    load_row<T, kV>(p, n, wide, f);
-    if constexpr (sizeof(T) == 4) {
-      return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-    } else {  // exact: the values came from bf16
-      return make_uint2(__float_as_uint(f[0]) >> 16 | (__float_as_uint(f[1]) & 0xffff0000u),
-                        __float_as_uint(f[2]) >> 16 | (__float_as_uint(f[3]) & 0xffff0000u));
-    }
-  }
-}
-__device__ __forceinline__ void pairs_of(uint4 r, f2 (&v)[2]) {
-  v[0] = mk2(__uint_as_float(r.x), __uint_as_float(r.y));
-  v[1] = mk2(__uint_as_float(r.z), __uint_as_float(r.w));
-}
-__device__ __forceinline__ void pairs_of(uint2 r, f2 (&v)[2]) {
-  v[0] = mk2(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u));
-  v[1] = mk2(__uint_as_float(r.y << 16), __uint_as_float(r.y & 0xffff0000u));
-}
-__device__ __forceinline__ void floats_of(const f2 (&v)[2], float (&f)[kV]) {
-  un2(v[0], f[0], f[1]);
-  un2(v[1], f[2], f[3]);
-}
-__device__ __forceinline__ void pairs_of(const float (&f)[kV], f2 (&v)[2]) {
-  v[0] = mk2(f[0], f[1]);
-  v[1] = mk2(f[2], f[3]);
-}
-
 // win[i] = the input K-1-i tokens before t (i < K-1), from the sequence or the
 // state before it.
-template <typename T, int K>
+template <typename T, int K, bool kWhole>
 __device__ __forceinline__ void fill_window(const T* x, int64_t st, const TokView& state0, const Run& r,
                                             const Piece& p, int t, bool wide, f2 (&win)[K][2]) {
 #pragma unroll
+  for (int i = 0; i < K - 1; ++i)  // tokens that are not there read the first
+    pairs_of(raw_row<kWhole, T>(x + max(t - (K - 1) + i, p.lo) * st, r.n, wide), win[i]);
+  if (t - (K - 1) >= p.lo) return;
+#pragma unroll
   for (int i = 0; i < K - 1; ++i) {
     const int src = t - (K - 1) + i;
+    if (src >= p.lo) continue;
     float f[kV] = {0.f, 0.f, 0.f, 0.f};
-    if (src >= p.lo) {
-      load_row<T, kV>(x + src * st, r.n, wide, f);
-    } else if (state0.p) {
+    if (state0.p) {
       const T* s0 = static_cast<const T*>(state0.p) + p.seq * state0.sb + r.h * state0.sh + r.c;
       load_row<T, kV>(s0 + (int64_t)(K - 1 + src - p.lo) * state0.st, r.n, wide, f);
     }
@@ -173,7 +133,7 @@ __device__ __forceinline__ void conv_run(const ConvArgs& a, const Run& r) {
   do {
     const int t0 = max(p.lo, r.r0), t1 = min(p.hi, r.r1);
     f2 win[K][2];
-    fill_window<T, K>(x, a.x.st, a.state0, r, p, t0, a.wide, win);
+    fill_window<T, K, kWhole>(x, a.x.st, a.state0, r, p, t0, a.wide, win);
     auto row = [&](int t, typename Raw<T>::type in) {
       float y[kV];
       pairs_of(in, win[K - 1]);
@@ -202,8 +162,13 @@ __device__ __forceinline__ void conv_run(const ConvArgs& a, const Run& r) {
 #pragma unroll
       for (int i = 0; i < n; ++i) in[i] = ahead[i];
     }
-#pragma unroll 1
-    for (; t < t1; ++t) row(t, raw_row<kWhole, T>(x + t * a.x.st, r.n, a.wide));
+    if (t < t1) {
+#pragma unroll
+      for (int i = 0; i < n; ++i) in[i] = raw_row<kWhole, T>(x + min(t + i, t1 - 1) * a.x.st, r.n, a.wide);
+#pragma unroll
+      for (int i = 0; i < n; ++i)
+        if (t + i < t1) row(t + i, in[i]);
+    }
     if (a.fin.p && t1 == p.hi) {
       T* f = static_cast<T*>(a.fin.p) + p.seq * a.fin.sb + r.h * a.fin.sh + r.c;
 #pragma unroll
@@ -275,7 +240,7 @@ __device__ __forceinline__ void conv_back(const ConvBwdArgs& a, const Run& r, fl
     const int t0 = max(p.lo, r.r0), t1 = min(p.hi, r.r1);
     const int first = t0 == p.lo ? p.lo - (K - 1) : t0;  // the state's inputs belong to the first run
     f2 win[K][2], dp[K][2];  // dp[k] = dp of token t-K+1+k
-    fill_window<T, K>(x, a.x.st, a.state0, r, p, t0, a.wide, win);
+    fill_window<T, K, kWhole>(x, a.x.st, a.state0, r, p, t0, a.wide, win);
 #pragma unroll
     for (int k = 0; k < K; ++k) dp[k][0] = dp[k][1] = 0;
     // dp of token t from its rows; own: the token is the run's
@@ -313,62 +278,59 @@ __device__ __forceinline__ void conv_back(const ConvBwdArgs& a, const Run& r, fl
       floats_of(v, o);
     };
     int t = t0;
-    // One by one up to the first token whose dx is the run's and the sequence's
-    // own, then in whole batches (none of those dx is state_final's), then one
-    // by one to the end.
-    bool batches = false;
+    // The walk goes in batches, the rows of the next one on their way. A batch
+    // of the run's own tokens whose dx are all the run's and the sequence's own
+    // (none of those is state_final's) needs no further look at its tokens.
+    constexpr int n = kBwdBatch<T>;
+    typename Raw<T>::type xr[n], gr[n], xa[n], ga[n];
+    auto fetch = [&](int t) {  // tokens behind the sequence read its last
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        const int64_t at = min(t + i, p.hi - 1);
+        xa[i] = raw_row<kWhole, T>(x + at * a.x.st, r.n, a.wide);
+        ga[i] = raw_row<kWhole, T>(dy + at * a.dy.st, r.n, a.wide);
+      }
+    };
+    fetch(t0);
 #pragma unroll 1
-    for (; t < t1 + K - 1; ++t) {
-      if (!batches && t - (K - 1) >= max(first, p.lo) && t + kBwdBatch<T> <= t1) {
-        batches = true;
-        typename Raw<T>::type xr[kBwdBatch<T>], gr[kBwdBatch<T>], xa[kBwdBatch<T>], ga[kBwdBatch<T>];
+    for (int t = t0; t < t1 + K - 1; t += n) {
 #pragma unroll
-        for (int i = 0; i < kBwdBatch<T>; ++i) {
-          xr[i] = raw_row<kWhole, T>(x + (t + i) * a.x.st, r.n, a.wide);
-          gr[i] = raw_row<kWhole, T>(dy + (t + i) * a.dy.st, r.n, a.wide);
+      for (int i = 0; i < n; ++i) xr[i] = xa[i], gr[i] = ga[i];
+      fetch(t + n);
+      if (t + n <= t1 && t - (K - 1) >= max(first, p.lo)) {
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+          shift<K>(dp);
+          token(xr[i], gr[i], true);
+          float o[kV];
+          gradient(o);
+          write_row<kWhole, T, kV>(dx + (t + i - (K - 1)) * a.dx.st, r.n, a.wide, o);
         }
-#pragma unroll 1
-        for (; t + kBwdBatch<T> <= t1; t += kBwdBatch<T>) {
-          const int64_t next = t + 2 * kBwdBatch<T> <= t1 ? t + kBwdBatch<T> : t;  // the last batch reads itself again
+        continue;
+      }
 #pragma unroll
-          for (int i = 0; i < kBwdBatch<T>; ++i) {
-            xa[i] = raw_row<kWhole, T>(x + (next + i) * a.x.st, r.n, a.wide);
-            ga[i] = raw_row<kWhole, T>(dy + (next + i) * a.dy.st, r.n, a.wide);
-          }
+      for (int i = 0; i < n; ++i) {
+        const int ti = t + i, s = ti - (K - 1);
+        if (ti >= t1 + K - 1) break;
+        shift<K>(dp);
+        if (ti < p.hi) token(xr[i], gr[i], ti < t1);
+        else dp[K - 1][0] = dp[K - 1][1] = 0;
+        if (s < first || s >= t1) continue;
+        float o[kV];
+        gradient(o);
+        if (a.dfin.p && s >= p.hi - (K - 1)) {  // state_final holds this input
+          float f[kV];
+          const T* df = static_cast<const T*>(a.dfin.p) + p.seq * a.dfin.sb + r.h * a.dfin.sh + r.c;
+          load_row<T, kV>(df + (int64_t)(K - 1 + s - p.hi) * a.dfin.st, r.n, a.wide, f);
 #pragma unroll
-          for (int i = 0; i < kBwdBatch<T>; ++i) {
-            shift<K>(dp);
-            token(xr[i], gr[i], true);
-            float o[kV];
-            gradient(o);
-            write_row<kWhole, T, kV>(dx + (t + i - (K - 1)) * a.dx.st, r.n, a.wide, o);
-          }
-#pragma unroll
-          for (int i = 0; i < kBwdBatch<T>; ++i) xr[i] = xa[i], gr[i] = ga[i];
+          for (int j = 0; j < kV; ++j) o[j] += f[j];
         }
-      }
-      shift<K>(dp);
-      if (t < p.hi) {
-        token(raw_row<kWhole, T>(x + t * a.x.st, r.n, a.wide), raw_row<kWhole, T>(dy + t * a.dy.st, r.n, a.wide), t < t1);
-      } else {
-        dp[K - 1][0] = dp[K - 1][1] = 0;
-      }
-      const int s = t - (K - 1);
-      if (s < first || s >= t1) continue;
-      float o[kV];
-      gradient(o);
-      if (a.dfin.p && s >= p.hi - (K - 1)) {  // state_final holds this input
-        float f[kV];
-        const T* df = static_cast<const T*>(a.dfin.p) + p.seq * a.dfin.sb + r.h * a.dfin.sh + r.c;
-        load_row<T, kV>(df + (int64_t)(K - 1 + s - p.hi) * a.dfin.st, r.n, a.wide, f);
-#pragma unroll
-        for (int j = 0; j < kV; ++j) o[j] += f[j];
-      }
-      if (s >= p.lo) {
-        write_row<kWhole, T, kV>(dx + s * a.dx.st, r.n, a.wide, o);
-      } else if (a.dstate0.p) {
-        T* d0 = static_cast<T*>(a.dstate0.p) + p.seq * a.dstate0.sb + r.h * a.dstate0.sh + r.c;
-        store_row<T, kV>(d0 + (int64_t)(K - 1 + s - p.lo) * a.dstate0.st, r.n, a.wide, o);
+        if (s >= p.lo) {
+          write_row<kWhole, T, kV>(dx + s * a.dx.st, r.n, a.wide, o);
+        } else if (a.dstate0.p) {
+          T* d0 = static_cast<T*>(a.dstate0.p) + p.seq * a.dstate0.sb + r.h * a.dstate0.sh + r.c;
+          store_row<T, kV>(d0 + (int64_t)(K - 1 + s - p.lo) * a.dstate0.st, r.n, a.wide, o);
+        }
       }
     }
   } while (next_piece(a.seqs, r, a.T, a.status, &p));
@@ -382,7 +344,7 @@ __device__ __forceinline__ void conv_back(const ConvBwdArgs& a, const Run& r, fl
 }
 
 template <typename T, int K>
-__global__ void __launch_bounds__(kThreads, K > 4 ? 2 : sizeof(T) == 2 ? 4 : 3)
+__global__ void __launch_bounds__(kThreads, K > 4 ? 2 : 3)
     conv_bwd_kernel(const __grid_constant__ ConvBwdArgs a, int len, int64_t cols) {
   const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   const Run r = run_of<kV>(id, a.B, a.H, a.T, a.d, len);

@@ -112,7 +112,35 @@ __device__ __forceinline__ void store_e4m3(uint8_t* p, int n, bool wide, const f
   }
 }
 
-// V weights of a row's piece at column c (zeros behind the row's end).
+// A thread's vectors of a row. Whole ones are read by predicated instructions,
+// all of them before any value is looked at; the rest (the row's last elements,
+// rows that are not aligned) follows one element after another.
+template <typename T, int VPT, bool kWhole>
+__device__ __forceinline__ void read_vecs(const T* row, int lane, int lanes, int d, bool wide, Vec<T> (&v)[VPT]) {
+  constexpr int V = Vec<T>::n;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = (i * lanes + lane) * V;
+    if constexpr (kWhole) {
+      v[i].v = *reinterpret_cast<const uint4*>(row + c);
+    } else {
+      v[i].v = make_uint4(0, 0, 0, 0);
+      asm volatile(
+          "{\n .reg .pred p;\n setp.ne.s32 p, %5, 0;\n @p ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n}\n"
+          : "+r"(v[i].v.x), "+r"(v[i].v.y), "+r"(v[i].v.z), "+r"(v[i].v.w)
+          : "l"(row + c), "r"((int)(wide && c + V <= d)));
+    }
+  }
+  if (!kWhole && (!wide || d % V != 0)) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = (i * lanes + lane) * V;
+      if (c < d && !(wide && c + V <= d)) v[i] = load_vec(row + c, d - c, false);
+    }
+  }
+}
+
+// V weights of a row's piece at column c.
 template <bool kWhole, int V>
 __device__ __forceinline__ void weights(const float* w, int c, int d, float (&f)[V]) {
   if constexpr (kWhole) {
@@ -123,7 +151,7 @@ __device__ __forceinline__ void weights(const float* w, int c, int d, float (&f)
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < V; ++j) f[j] = c + j < d ? w[c + j] : 0.f;
+    for (int j = 0; j < V; ++j) f[j] = w[min(c + j, d - 1)];  // nothing behind the row's end is kept
   }
 }
 
@@ -139,29 +167,32 @@ __device__ __forceinline__ void norm_rows(const NormArgs& a, int lanes, float* r
   const int t0 = at.t * R, n = g < all ? min(R, a.T - t0) : 0;  // tokens that are this thread's
   const T* x = static_cast<const T*>(a.x.p) + at.b * a.x.sb + at.h * a.x.sh;
   const float* w = a.w + at.h * a.w_sh;
-  float s[R][VPT][V], q[R][VPT][V];
+  float s[R][VPT][V];
+  Vec<T> xv[R][VPT];
 #pragma unroll
   for (int k = 0; k < R; ++k)
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = (i * lanes + lane) * V;
-      read_row<kWhole, T, V>(x + min(t0 + k, a.T - 1) * a.x.st + c, a.d - c, a.wide, s[k][i]);
-    }
+    read_vecs<T, VPT, kWhole>(x + min(t0 + k, a.T - 1) * a.x.st, lane, lanes, a.d, a.wide, xv[k]);
   if (a.r.p) {
     const T* res = static_cast<const T*>(a.r.p) + at.b * a.r.sb + at.h * a.r.sh;
+    Vec<T> rv[R][VPT];
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+      read_vecs<T, VPT, kWhole>(res + min(t0 + k, a.T - 1) * a.r.st, lane, lanes, a.d, a.wide, rv[k]);
 #pragma unroll
     for (int k = 0; k < R; ++k)
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
-        const int c = (i * lanes + lane) * V;
-        read_row<kWhole, T, V>(res + min(t0 + k, a.T - 1) * a.r.st + c, a.d - c, a.wide, q[k][i]);
+        float q[V];
+        unpack<T>(xv[k][i], s[k][i]);
+        unpack<T>(rv[k][i], q);
+#pragma unroll
+        for (int j = 0; j < V; ++j) s[k][i][j] += q[j];
       }
+  } else {
 #pragma unroll
     for (int k = 0; k < R; ++k)
 #pragma unroll
-      for (int i = 0; i < VPT; ++i)
-#pragma unroll
-        for (int j = 0; j < V; ++j) s[k][i][j] += q[k][i][j];
+      for (int i = 0; i < VPT; ++i) unpack<T>(xv[k][i], s[k][i]);
   }
   float sum[R];
 #pragma unroll
@@ -292,13 +323,9 @@ __device__ __forceinline__ void norm_back(const NormBwdArgs& a, int lanes, int64
     // without it the gradient stands in its place and is not used
     const T* rp = a.dres.p ? static_cast<const T*>(a.dres.p) + ahead.b * a.dres.sb + ahead.h * a.dres.sh + ahead.t * a.dres.st
                            : gp;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = (i * lanes + lane) * V, n = kWhole ? V : a.d - c;
-      hv[i] = kWhole ? Vec<T>{*reinterpret_cast<const uint4*>(hp + c)} : load_vec(hp + c, n, a.wide);
-      gv[i] = kWhole ? Vec<T>{*reinterpret_cast<const uint4*>(gp + c)} : load_vec(gp + c, n, a.wide);
-      rv[i] = kWhole ? Vec<T>{*reinterpret_cast<const uint4*>(rp + c)} : load_vec(rp + c, n, a.wide);
-    }
+    read_vecs<T, VPT, kWhole>(hp, lane, lanes, a.d, a.wide, hv);
+    read_vecs<T, VPT, kWhole>(gp, lane, lanes, a.d, a.wide, gv);
+    read_vecs<T, VPT, kWhole>(rp, lane, lanes, a.d, a.wide, rv);
   };
   if (kAhead && turns > 0) fetch(0);
   for (int64_t k = 0; k < turns; ++k) {

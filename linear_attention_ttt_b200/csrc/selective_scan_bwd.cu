@@ -61,7 +61,8 @@ Plan plan(const ScanArgs& a) {
 struct Ws {
   float *start, *sums;      // [parts][blocks][warps a block][kPiece], [parts][blocks][channels]
   float *hin, *gin, *total; // [chunks][blocks]... likewise; total: sum of D_t over a chunk
-  float *dA, *dD;           // [B*chunks][...] partial sums; dD: dD then ddt_bias
+  float* sums_of;           // [chunks * B][cols]: a batch row's partial sums of dA, then of dD and ddt_bias
+  int64_t cols;
   float *dBC;               // [blocks][T][2][states padded]
   int64_t floats;
 };
@@ -79,8 +80,8 @@ Ws carve(const ScanArgs& a, const Plan& p, float* base) {
   w.hin = take(p.chunks * p.blocks * wpb * kPiece);
   w.gin = take(p.chunks * p.blocks * wpb * kPiece);
   w.total = take(p.chunks * p.blocks * ch);
-  w.dA = take(p.chunks * p.blocks * wpb * kPiece);
-  w.dD = take(p.chunks * p.blocks * ch * 2);
+  w.cols = p.blocks / a.B * (wpb * kPiece + 2 * ch);
+  w.sums_of = take(p.chunks * (int64_t)a.B * w.cols);
   w.dBC = take(p.blocks * a.T * 2 * p.warps * kNB);
   w.floats = at;
   return w;
@@ -121,34 +122,51 @@ __device__ __forceinline__ void stage_as(const ScanArgs& a, const TokView& dy, c
   const bool gate = a.z.p != nullptr;
   const T* zp = gate ? static_cast<const T*>(a.z.p) + q.b * a.z.sb + q.h * a.z.sh + q.c0 + vc : gp;
   const int64_t zs = gate ? a.z.st : dy.st;
-  float x[kTurns][4], d[kTurns][4], e[kTurns][4], z[kTurns][4];
+  using R = typename Raw<T>::type;
+  R rx[kTurns], rd[kTurns], re[kTurns], rz[kTurns];
 #pragma unroll
-  for (int i = 0; i < kTurns; ++i) {
-    const int row = min(i * dr + q.tid / kGroups, kPart - 1);
-    const int n = kWhole || live >> row & 1 ? vn : 0;
-    const int64_t t = tb + row;
-    read_row<kWhole, T, 4>(xp + t * a.x.st, n, a.wide, x[i]);
-    read_row<kWhole, T, 4>(dp + t * a.dt.st, n, a.wide, d[i]);
-    read_row<kWhole, T, 4>(gp + t * dy.st, n, a.wide, e[i]);
-    read_row<kWhole, T, 4>(zp + t * zs, n, a.wide, z[i]);
+  for (int pass = 0; pass < (kWhole ? 1 : 2); ++pass) {
+    if (pass == 1 && a.wide && (vn >= kV || vn <= 0)) break;  // no ragged piece
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) {
+      const int row = min(i * dr + q.tid / kGroups, kPart - 1);
+      const int n = kWhole || live >> row & 1 ? vn : 0;
+      const bool whole = kWhole || (a.wide && n >= kV);
+      const int64_t t = tb + row;
+      if (pass == 0) {
+        rx[i] = raw_whole<T>(xp + t * a.x.st, whole);
+        rd[i] = raw_whole<T>(dp + t * a.dt.st, whole);
+        re[i] = raw_whole<T>(gp + t * dy.st, whole);
+        rz[i] = raw_whole<T>(zp + t * zs, whole);
+      } else {
+        raw_rest<T>(rx[i], xp + t * a.x.st, n, a.wide);
+        raw_rest<T>(rd[i], dp + t * a.dt.st, n, a.wide);
+        raw_rest<T>(re[i], gp + t * dy.st, n, a.wide);
+        raw_rest<T>(rz[i], zp + t * zs, n, a.wide);
+      }
+    }
   }
 #pragma unroll
   for (int i = 0; i < kTurns; ++i) {
     const int row = i * dr + q.tid / kGroups;
     if (kPart % dr != 0 && row >= kPart) break;
     const bool on = kWhole || live >> row & 1;
+    float x[4], d[4], e[4], z[4];
+    floats_of(rx[i], x);
+    floats_of(rd[i], d);
+    floats_of(re[i], e);
+    floats_of(rz[i], z);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      d[i][j] += bias[j];
-      if (a.softplus) d[i][j] = softplus_f(d[i][j]);
-      if (gate) e[i][j] *= silu_f(z[i][j]);
-      if (!on) d[i][j] = 0.f;
+      d[j] += bias[j];
+      if (a.softplus) d[j] = softplus_f(d[j]);
+      if (gate) e[j] *= silu_f(z[j]);
+      if (!on) d[j] = 0.f;
     }
     const int o = row * S::cw + vc;
-    *reinterpret_cast<float4*>(s.dt + o) = make_float4(d[i][0], d[i][1], d[i][2], d[i][3]);
-    *reinterpret_cast<float4*>(s.u + o) =
-        make_float4(d[i][0] * x[i][0], d[i][1] * x[i][1], d[i][2] * x[i][2], d[i][3] * x[i][3]);
-    *reinterpret_cast<float4*>(s.e + o) = make_float4(e[i][0], e[i][1], e[i][2], e[i][3]);
+    *reinterpret_cast<float4*>(s.dt + o) = make_float4(d[0], d[1], d[2], d[3]);
+    *reinterpret_cast<float4*>(s.u + o) = make_float4(d[0] * x[0], d[1] * x[1], d[2] * x[2], d[3] * x[3]);
+    *reinterpret_cast<float4*>(s.e + o) = make_float4(e[0], e[1], e[2], e[3]);
   }
   constexpr int per = S::ns / 2;  // two states a turn: consecutive threads write consecutive 16 bytes
 #pragma unroll
@@ -159,9 +177,11 @@ __device__ __forceinline__ void stage_as(const ScanArgs& a, const TokView& dy, c
     for (int i0 = 0; i0 < kPart * per; i0 += S::threads) {
       const int i = i0 + q.tid, row = i / per, n0 = i % per * 2;
       if (kPart * per % S::threads != 0 && i >= kPart * per) break;
+      // the reads are always made, in bounds; what is not there becomes zero
       const bool on = kWhole || live >> row & 1;
-      const T* at = p + (int64_t)(tb + row) * v.st + n0;
-      const float f0 = on && n0 < a.N ? to_f32(at[0]) : 0.f, f1 = on && n0 + 1 < a.N ? to_f32(at[1]) : 0.f;
+      const T* at = p + (int64_t)min(tb + row, a.T - 1) * v.st;
+      const float v0 = to_f32(at[min(n0, a.N - 1)]), v1 = to_f32(at[min(n0 + 1, a.N - 1)]);
+      const float f0 = on && n0 < a.N ? v0 : 0.f, f1 = on && n0 + 1 < a.N ? v1 : 0.f;
       reinterpret_cast<float4*>(w ? s.c : s.b)[i] = make_float4(f0, f0, f1, f1);
     }
   }
@@ -440,7 +460,12 @@ __global__ void __launch_bounds__(128, 2) main_kernel(const __grid_constant__ Sc
 #pragma unroll
   for (int k = 0; k < 4; ++k) regs.dA[k] = 0;
   rates(a, q, A2);
-  load_piece(ws.gin + (chat * wpb + q.warp) * kPiece, q.lane, regs.gs);
+  if (p.chunks > 1) {
+    load_piece(ws.gin + (chat * wpb + q.warp) * kPiece, q.lane, regs.gs);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) regs.gs[k] = 0;
+  }
   const int vc = q.tid % kGroups * 4, vn = a.d - q.c0 - vc;
   float bias[4], sD[4] = {0.f, 0.f, 0.f, 0.f}, sbias[4] = {0.f, 0.f, 0.f, 0.f};
   float dskip[4];
@@ -464,7 +489,12 @@ __global__ void __launch_bounds__(128, 2) main_kernel(const __grid_constant__ Sc
     stage<T>(a, ga.dy, q, tb, m.live, bias, s);
     // the state before the part
     f2(&hs)[4] = regs.hs;
-    load_piece(ws.hin + (chat * wpb + q.warp) * kPiece, q.lane, hs);
+    if (p.chunks > 1) {
+      load_piece(ws.hin + (chat * wpb + q.warp) * kPiece, q.lane, hs);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) hs[k] = 0;
+    }
     if (part > part0) {
       const int64_t at = (int64_t)part * p.blocks + blockIdx.x;
       f2 local[4];
@@ -537,16 +567,29 @@ __global__ void __launch_bounds__(128, 2) main_kernel(const __grid_constant__ Sc
       const bool gate = a.z.p != nullptr;
       const T* zp = gate ? static_cast<const T*>(a.z.p) + q.b * a.z.sb + q.h * a.z.sh + q.c0 + vc : gp;
       const int64_t zs = gate ? a.z.st : ga.dy.st;
-      float x[kTurns][4], w[kTurns][4], e[kTurns][4], z[kTurns][4];
+      using R = typename Raw<T>::type;
+      R rx[kTurns], rd[kTurns], re[kTurns], rz[kTurns];
 #pragma unroll
-      for (int i = 0; i < kTurns; ++i) {
-        const int row = min(i * dr + q.tid / kGroups, kPart - 1);
-        const int n = kWhole || m.live >> row & 1 ? vn : 0;
-        const int64_t t = t0 + row;
-        read_row<kWhole, T, 4>(xp + t * a.x.st, n, a.wide, x[i]);
-        read_row<kWhole, T, 4>(dp + t * a.dt.st, n, a.wide, w[i]);
-        read_row<kWhole, T, 4>(gp + t * ga.dy.st, n, a.wide, e[i]);
-        read_row<kWhole, T, 4>(zp + t * zs, n, a.wide, z[i]);
+      for (int pass = 0; pass < (kWhole ? 1 : 2); ++pass) {
+        if (pass == 1 && a.wide && (vn >= kV || vn <= 0)) break;  // no ragged piece
+#pragma unroll
+        for (int i = 0; i < kTurns; ++i) {
+          const int row = min(i * dr + q.tid / kGroups, kPart - 1);
+          const int n = kWhole || m.live >> row & 1 ? vn : 0;
+          const bool whole = kWhole || (a.wide && n >= kV);
+          const int64_t t = t0 + row;
+          if (pass == 0) {
+            rx[i] = raw_whole<T>(xp + t * a.x.st, whole);
+            rd[i] = raw_whole<T>(dp + t * a.dt.st, whole);
+            re[i] = raw_whole<T>(gp + t * ga.dy.st, whole);
+            rz[i] = raw_whole<T>(zp + t * zs, whole);
+          } else {
+            raw_rest<T>(rx[i], xp + t * a.x.st, n, a.wide);
+            raw_rest<T>(rd[i], dp + t * a.dt.st, n, a.wide);
+            raw_rest<T>(re[i], gp + t * ga.dy.st, n, a.wide);
+            raw_rest<T>(rz[i], zp + t * zs, n, a.wide);
+          }
+        }
       }
 #pragma unroll
       for (int i = 0; i < kTurns; ++i) {
@@ -564,29 +607,33 @@ __global__ void __launch_bounds__(128, 2) main_kernel(const __grid_constant__ Sc
           }
           v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
         };
-        float gb[4], gr[4], y[4], o[4];
+        float x[4], w[4], e[4], z[4], gb[4], gr[4], y[4], o[4];
+        floats_of(rx[i], x);
+        floats_of(rd[i], w);
+        floats_of(re[i], e);
+        floats_of(rz[i], z);
         joined(q0, gb);
         joined(r0, gr);
         if (gate) {
           joined(y0, y);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            o[j] = e[i][j] * fmaf(dskip[j], x[i][j], y[j]) * dsilu_f(z[i][j]);
-            e[i][j] *= silu_f(z[i][j]);
+            o[j] = e[j] * fmaf(dskip[j], x[j], y[j]) * dsilu_f(z[j]);
+            e[j] *= silu_f(z[j]);
           }
           write_row<kWhole, T, 4>(static_cast<T*>(ga.dz.p) + q.b * ga.dz.sb + q.h * ga.dz.sh + q.c0 + vc + t * ga.dz.st, vn,
                                   a.wide, o);
         }
         const float4 d = *reinterpret_cast<const float4*>(s.dt + row * cw + vc);
-        o[0] = fmaf(dskip[0], e[i][0], d.x * gb[0]), o[1] = fmaf(dskip[1], e[i][1], d.y * gb[1]);
-        o[2] = fmaf(dskip[2], e[i][2], d.z * gb[2]), o[3] = fmaf(dskip[3], e[i][3], d.w * gb[3]);
+        o[0] = fmaf(dskip[0], e[0], d.x * gb[0]), o[1] = fmaf(dskip[1], e[1], d.y * gb[1]);
+        o[2] = fmaf(dskip[2], e[2], d.z * gb[2]), o[3] = fmaf(dskip[3], e[3], d.w * gb[3]);
         write_row<kWhole, T, 4>(static_cast<T*>(ga.dx.p) + q.b * ga.dx.sb + q.h * ga.dx.sh + q.c0 + vc + t * ga.dx.st, vn,
                                 a.wide, o);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          o[j] = fmaf(x[i][j], gb[j], gr[j] * ln2);  // the rates are in powers of two
-          if (a.softplus) o[j] *= sigmoid_f(w[i][j] + bias[j]);
-          sD[j] = fmaf(e[i][j], x[i][j], sD[j]);
+          o[j] = fmaf(x[j], gb[j], gr[j] * ln2);  // the rates are in powers of two
+          if (a.softplus) o[j] *= sigmoid_f(w[j] + bias[j]);
+          sD[j] = fmaf(e[j], x[j], sD[j]);
           sbias[j] += o[j];
         }
         write_row<kWhole, T, 4>(static_cast<T*>(ga.ddt.p) + q.b * ga.ddt.sb + q.h * ga.ddt.sh + q.c0 + vc + t * ga.ddt.st, vn,
@@ -607,7 +654,9 @@ __global__ void __launch_bounds__(128, 2) main_kernel(const __grid_constant__ Sc
     }
     __syncthreads();
   }
-  store_piece(ws.dA + (chat * wpb + q.warp) * kPiece, q.lane, regs.dA);
+  const int64_t heads = (int64_t)a.H * p.per_head, in = blockIdx.x % heads;  // the block's place in its batch row
+  float* sums = ws.sums_of + ((int64_t)chunk * a.B + q.b) * ws.cols;
+  store_piece(sums + (in * wpb + q.warp) * kPiece, q.lane, regs.dA);
   // the threads' channel sums: rows of threads that share channels, in order
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
@@ -618,34 +667,30 @@ __global__ void __launch_bounds__(128, 2) main_kernel(const __grid_constant__ Sc
     for (int c = q.tid; c < cw; c += S::threads) {
       float v = 0.f;
       for (int i = 0; i < dr; ++i) v += sh[i * cw + c];
-      ws.dD[(chat * 2 + w) * cw + c] = v;
+      sums[heads * wpb * kPiece + (in * 2 + w) * cw + c] = v;
     }
     __syncthreads();
   }
 }
 
-// Destinations of the ordered sums over batch rows and chunks. A column is an
-// element of the block's layout for one (head, channel block).
-struct PutA {
-  float* dA;
+// Destinations of the ordered sums over batch rows and chunks.
+struct PutSums {
+  float *dA, *dD, *dbias;
   int d, N;
   Grid g;
+  int64_t first;  // columns of dA
   __device__ void operator()(int64_t col, float v) const {
-    const PieceAt at = piece_at(col, g);
-    const int64_t h = at.blk / g.per_head;
-    const int c = (int)(at.blk % g.per_head) * g.cw() + at.cb;
-    if (at.n < N && c < d) dA[(h * d + c) * N + at.n] = v;
-  }
-};
-struct PutD {
-  float *dD, *dbias;
-  int d, per_head, cw;
-  __device__ void operator()(int64_t col, float v) const {
-    const int c = (int)(col % cw), which = (int)(col / cw % 2);
-    const int64_t blk = col / cw / 2, h = blk / per_head;
-    const int ch = (int)(blk % per_head) * cw + c;
-    float* p = which ? dbias : dD;
-    if (p && ch < d) p[h * d + ch] = v;
+    if (col < first) {
+      const PieceAt at = piece_at(col, g);
+      const int64_t h = at.blk / g.per_head;
+      const int c = (int)(at.blk % g.per_head) * g.cw() + at.cb;
+      if (at.n < N && c < d) dA[(h * d + c) * N + at.n] = v;
+    } else {
+      const int64_t i = col - first, blk = i / (2 * g.cw()), h = blk / g.per_head;
+      const int c = (int)(blk % g.per_head) * g.cw() + (int)(i % g.cw());
+      float* p = i / g.cw() % 2 ? dbias : dD;
+      if (p && c < d) p[h * d + c] = v;
+    }
   }
 };
 
@@ -681,7 +726,7 @@ cudaError_t bwd(const ScanBwdArgs& ga, cudaStream_t s) {
   cudaError_t e =
       copy_empty_states(a.seqs, a.T, (int64_t)a.H * a.d * a.N, ga.dh_final, ga.dh0, a.status, s);
   if (e != cudaSuccess) return e;
-  const int nw = p.tpb * p.warps, cw = p.tpb * kCh;
+  const int nw = p.wpb();
   const int64_t heads = (int64_t)a.H * p.per_head;  // channel blocks of a batch row
   if (a.T > 0) {
     e = for_warps(p.warps, [&](auto w) {
@@ -693,9 +738,11 @@ cudaError_t bwd(const ScanBwdArgs& ga, cudaStream_t s) {
       r = cudaFuncSetAttribute(main_kernel<T, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(All));
       if (r != cudaSuccess) return r;
       const dim3 grid((unsigned)p.blocks, p.chunks);
-      pre_kernel<T, W><<<grid, 32 * nw, sizeof(First), s>>>(ga, p, ws);
+      // one chunk enters with nothing and passes nothing on; its first part
+      // starts from its own beginning
+      if (p.parts > 1) pre_kernel<T, W><<<grid, 32 * nw, sizeof(First), s>>>(ga, p, ws);
       const int64_t n = p.blocks * nw * kPiece;
-      join_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(a, p, ws);
+      if (p.chunks > 1) join_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(a, p, ws);
       main_kernel<T, W><<<grid, 32 * nw, sizeof(All), s>>>(ga, p, ws);
       const int64_t bc = (int64_t)a.B * a.G * a.T * 2 * p.warps * kNB;
       put_bc_kernel<T><<<(unsigned)((bc + 255) / 256), 256, 0, s>>>(ga, p, ws.dBC);
@@ -703,11 +750,8 @@ cudaError_t bwd(const ScanBwdArgs& ga, cudaStream_t s) {
     });
     if (e != cudaSuccess) return e;
   }
-  // [chunk][batch row][head block]: parts are (chunk, batch row) pairs
-  const int64_t parts = (int64_t)p.chunks * a.B;
-  e = sum_parts(ws.dA, parts, heads * nw * kPiece, PutA{ga.dA, a.d, a.N, p}, s);
-  if (e != cudaSuccess || (!ga.dD && !ga.ddt_bias)) return e;
-  return sum_parts(ws.dD, parts, heads * 2 * cw, PutD{ga.dD, ga.ddt_bias, a.d, p.per_head, cw}, s);
+  return sum_parts(ws.sums_of, (int64_t)p.chunks * a.B, ws.cols,
+                   PutSums{ga.dA, ga.dD, ga.ddt_bias, a.d, a.N, p, heads * nw * kPiece}, s);
 }
 
 }  // namespace
