@@ -16,6 +16,7 @@
 
 #include <array>
 #include <utility>
+#include <vector>
 
 #include "../../include/ttt.h"
 
@@ -125,8 +126,21 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   return PyLong_FromLong(st);
 }
 
-// A new token tensor [B,H,T,d] in x's order of storage (heads before or behind
-// tokens), its rows a multiple of 16 bytes apart.
+// Layout of a new token tensor [B,H,T,d]: x's order of storage (heads before or
+// behind tokens), its rows a multiple of 16 bytes apart.
+struct Rows {
+  std::array<int64_t, 4> size, stride;
+  int64_t count;
+  Rows(const at::Tensor& x, int64_t d, int64_t element) {
+    const int64_t B = x.size(0), H = x.size(1), T = x.size(2);
+    const int64_t per = 16 / element, row = (d + per - 1) / per * per;
+    const bool behind = H > 1 && T > 1 && x.stride(1) < x.stride(2);
+    size = {B, H, T, d};
+    stride = {H * T * row, behind ? row : T * row, behind ? H * row : row, 1};
+    count = B * H * T * row;
+  }
+};
+
 PyObject* like_tokens(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   if (nargs != 4 || !THPVariable_Check(args[0]) || !THPDtype_Check(args[2])) {
     PyErr_SetString(PyExc_TypeError, "like_tokens(x, d, dtype, zero)");
@@ -142,16 +156,56 @@ PyObject* like_tokens(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     return nullptr;
   }
   try {
-    const int64_t B = x.size(0), H = x.size(1), T = x.size(2);
-    const int64_t per = 16 / (int64_t)c10::elementSize(type), row = (d + per - 1) / per * per;
-    const bool behind = H > 1 && T > 1 && x.stride(1) < x.stride(2);
+    const Rows r(x, d, (int64_t)c10::elementSize(type));
     const auto opt = x.options().dtype(type).requires_grad(false);
-    const std::array<int64_t, 4> size = {B, H, T, row};
-    const std::array<int64_t, 4> stride = {H * T * row, behind ? row : T * row, behind ? H * row : row, 1};
-    at::Tensor t = at::empty_strided(size, stride, opt);
-    if (zero) t.zero_();
-    if (row != d) t = t.slice(3, 0, d);
-    return THPVariable_Wrap(t);
+    const at::Tensor t = zero ? at::zeros({r.count}, opt) : at::empty({r.count}, opt);
+    return THPVariable_Wrap(t.as_strided(r.size, r.stride));
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+    return nullptr;
+  }
+}
+
+// New zero tensors like each of a tuple of token tensors of one type (None gives
+// None), in one allocation with one fill.
+PyObject* zeros_like_tokens(PyObject*, PyObject* arg) {
+  if (!PyTuple_Check(arg)) {
+    PyErr_SetString(PyExc_TypeError, "zeros_like_tokens((x, ...))");
+    return nullptr;
+  }
+  const Py_ssize_t n = PyTuple_GET_SIZE(arg);
+  try {
+    std::vector<Rows> rows;
+    const at::Tensor* first = nullptr;
+    int64_t total = 0;
+    for (Py_ssize_t i = 0; i < n; ++i) {
+      PyObject* o = PyTuple_GET_ITEM(arg, i);
+      if (o == Py_None) continue;
+      if (!THPVariable_Check(o) || THPVariable_Unpack(o).dim() != 4) {
+        PyErr_SetString(PyExc_ValueError, "tokens are [B,H,T,d]");
+        return nullptr;
+      }
+      const at::Tensor& x = THPVariable_Unpack(o);
+      if (!first) first = &x;
+      rows.emplace_back(x, x.size(3), (int64_t)x.element_size());
+      total += rows.back().count;
+    }
+    PyObject* out = PyTuple_New(n);
+    if (!out) return nullptr;
+    at::Tensor all;
+    if (first) all = at::zeros({total}, first->options().requires_grad(false));
+    int64_t at_ = 0;
+    size_t k = 0;
+    for (Py_ssize_t i = 0; i < n; ++i) {
+      if (PyTuple_GET_ITEM(arg, i) == Py_None) {
+        Py_INCREF(Py_None);
+        PyTuple_SET_ITEM(out, i, Py_None);
+        continue;
+      }
+      PyTuple_SET_ITEM(out, i, THPVariable_Wrap(all.as_strided(rows[k].size, rows[k].stride, at_)));
+      at_ += rows[k++].count;
+    }
+    return out;
   } catch (const std::exception& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
     return nullptr;
@@ -161,6 +215,7 @@ PyObject* like_tokens(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
 PyMethodDef methods[] = {
     {"like_tokens", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(like_tokens)), METH_FASTCALL,
      "like_tokens(x, d, dtype, zero) -> tensor"},
+    {"zeros_like_tokens", zeros_like_tokens, METH_O, "zeros_like_tokens((x, ...)) -> tensors"},
     {"call", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(call)), METH_FASTCALL,
      "call(function, tensors, split, scalar, stream, name) -> status"},
     {nullptr, nullptr, 0, nullptr}};

@@ -315,7 +315,7 @@ def lact_swiglu_window_fwd(q, k, v, eta, W1, W2, W3, chunk: int, update_rule: in
 
 # ---- the recurrent block: RMS norm, short convolution, selective scan ---------
 
-_ADDRESS = {}  # of the loaded library's functions, by name; and the native binding's two
+_ADDRESS = {}  # of the loaded library's functions, by name; and the native binding's
 
 
 def _load_binding():
@@ -324,7 +324,8 @@ def _load_binding():
     except ImportError as e:
         raise OSError(f"{_PKG}/_binding.so is missing or does not load: run "
                       f"`python -m linear_attention_ttt_b200.build`") from e
-    _ADDRESS["call"], _ADDRESS["like_tokens"] = _binding.call, _binding.like_tokens
+    for f in (_binding.call, _binding.like_tokens, _binding.zeros_like_tokens):
+        _ADDRESS[f.__name__] = f
 
 
 def _block_call(name, tensors, split, scalar, stream):
@@ -453,13 +454,16 @@ def selective_scan_bwd(x, dt, A, Bm, Cm, dy, D=None, z=None, dt_bias=None, softp
     """Backward of selective_scan_fwd: returns (dx, ddt, dA, dBm, dCm, dD, dz, ddt_bias,
     dh0), None for the gradient of what was not given. The states are computed again
     from the inputs."""
-    packed = cu_seqlens is not None
     f32 = dict(dtype=torch.float32, device=x.device)
-    dx, ddt = _like_tokens(x, zero=packed), _like_tokens(x, zero=packed)
-    dBm, dCm = _like_tokens(Bm, zero=packed), _like_tokens(Cm, zero=packed)
+    like = (x, x, None if z is None else x, Bm, Cm)
+    if cu_seqlens is None:
+        dx, ddt, dz, dBm, dCm = (None if t is None else _like_tokens(t) for t in like)
+    else:  # rows behind the last sequence stay zero
+        if not _ADDRESS:
+            _load_binding()
+        dx, ddt, dz, dBm, dCm = _ADDRESS["zeros_like_tokens"](like)
     dA = torch.empty(A.shape, **f32)
     dD = None if D is None else torch.empty(D.shape, **f32)
-    dz = None if z is None else _like_tokens(x, zero=packed)
     dbias = None if dt_bias is None else torch.empty(dt_bias.shape, **f32)
     dh0 = None if h0 is None else torch.empty(h0.shape, **f32)
     _block_call("selective_scan_bwd", (x, dt, A, Bm, Cm, D, z, dt_bias, h0, cu_seqlens, dy,
