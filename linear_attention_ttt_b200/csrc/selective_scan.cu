@@ -75,7 +75,6 @@ __global__ void __launch_bounds__(128, sizeof(T) == 2 ? 4 : 3)
   f2 A2[4], hs[4] = {0, 0, 0, 0}, sum = 0;
   rates(a, q, A2);
   const int64_t piece = ((int64_t)chunk * p.blocks + blockIdx.x) * S::wpb + q.warp;
-  if (!kPre && chunk > 0) load_piece(states + piece * kPiece, q.lane, hs);
 
   const int vc = q.tid % kGroups * 4, vn = a.d - q.c0 - vc, row0 = q.tid / kGroups;
   float bias[4], skip[4];
@@ -113,6 +112,13 @@ __global__ void __launch_bounds__(128, sizeof(T) == 2 ? 4 : 3)
 
   fetch(t0);
   if (!kPre) fetch_z(t0, next.live);
+  // the join may be launched now, and waits; the main pass may have been launched
+  // before the joined states were there
+  if (kPre) pdl_trigger();
+  if (!kPre && p.chunks > 1) {
+    pdl_wait();
+    if (chunk > 0) load_piece(states + piece * kPiece, q.lane, hs);
+  }
   for (int tb = t0; tb < t1; tb += kPart) {
     const int nt = min(kPart, t1 - tb);
     const Marks now = next;
@@ -254,6 +260,8 @@ __global__ void join_kernel(ScanArgs a, Plan p, float* states, const float* __re
   const float A2 = at.n < a.N && c < a.d ? a.A[((int64_t)h * a.d + c) * a.N + at.n] * kLog2e : 0.f;
   const float* sum = sums + at.blk * p.cw() + at.cb;
   float carry = 0.f;
+  pdl_trigger();
+  pdl_wait();
   for (int i0 = 0; i0 < p.chunks; i0 += kAhead) {
     float local[kAhead], dec[kAhead];
     bool cut[kAhead];
@@ -295,7 +303,11 @@ cudaError_t fwd(const ScanArgs& a, cudaStream_t s) {
     if (p.chunks > 1) {
       scan_kernel<T, W, true><<<first, threads, sizeof(First), s>>>(a, p, states, sums, cuts);
       const int64_t n = p.blocks * p.wpb() * kPiece;
-      join_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(a, p, states, sums, cuts);
+      r = cudaGetLastError();
+      if (r != cudaSuccess) return r;
+      r = launch_pdl(join_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a, p, states, (const float*)sums, (const int*)cuts);
+      if (r != cudaSuccess) return r;
+      return launch_pdl(scan_kernel<T, W, false>, all, dim3(threads), sizeof(All), s, a, p, states, sums, cuts);
     }
     scan_kernel<T, W, false><<<all, threads, sizeof(All), s>>>(a, p, states, sums, cuts);
     return cudaGetLastError();

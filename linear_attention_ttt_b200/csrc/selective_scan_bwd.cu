@@ -29,6 +29,8 @@ namespace {
 
 constexpr int kBlk = 4;     // tokens held in registers
 
+constexpr int kMostChunks = 8192;
+
 struct Plan : Grid {
   int parts, chunk, chunks;  // parts in all, parts a chunk, chunks
 };
@@ -47,12 +49,12 @@ Plan plan(const ScanArgs& a) {
   for (int c = 1; c <= p.parts && c <= 1024; ++c) {
     const double rounds = (double)p.blocks * ((p.parts + c - 1) / c) / slots;
     const double cost = ((rounds > 1 ? rounds : 1) + 0.8) * (c + 0.6);
-    if ((p.parts + c - 1) / c <= 65535 && (best == 0 || cost < best)) {
+    if ((p.parts + c - 1) / c <= kMostChunks && (best == 0 || cost < best)) {
       best = cost;
       p.chunk = c;
     }
   }
-  if (p.parts / 65535 >= p.chunk) p.chunk = p.parts / 65535 + 1;
+  if (best == 0 && p.parts > 0) p.chunk = (p.parts + kMostChunks - 1) / kMostChunks;
   p.chunks = (p.parts + p.chunk - 1) / p.chunk;
   return p;
 }
@@ -227,6 +229,7 @@ __global__ void __launch_bounds__(128, 4) pre_kernel(ScanBwdArgs ga, Plan p, Ws 
     four_of(a.dt_bias, a, q.h, q.c0 + vc, bias);
   }
   bool open = true;  // the sequence that enters the chunk has not ended
+  pdl_trigger();     // the join may be launched now, and waits
   const int lane_c = q.wt * kCh + q.cg * 2, lane_s = q.wn * 2 * kNB + q.sg * 8;
   const int part1 = min(p.parts, (chunk + 1) * p.chunk);
   for (int part = chunk * p.chunk; part < part1; ++part) {
@@ -297,17 +300,31 @@ constexpr int kAhead = 8;  // chunks read before their use
 // sequence begins (or ends) passes nothing through, and nothing crosses a
 // border at which one begins.
 __global__ void join_kernel(ScanArgs a, Plan p, Ws ws) {
+  // packed sequences: bit 0 the sequence at a chunk's first token was there
+  // before it, bit 1 and before the chunk in front of it, bit 2 and it goes on
+  // behind the chunk
+  __shared__ uint8_t border[kMostChunks];
+  if (a.seqs.cu) {
+    const int span = p.chunk * kPart;
+    for (int i = threadIdx.x; i < p.chunks; i += blockDim.x) {
+      const TokenAt at = token_at(a.seqs, 0, a.T, i * span, a.status);
+      const bool on = at.live && at.lo < i * span;
+      border[i] = on | (on && at.lo < (i - 1) * span) << 1 | (on && at.hi > (i + 1) * span) << 2;
+    }
+    __syncthreads();
+  }
   const int64_t per = p.blocks * p.wpb() * kPiece, e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (e >= per) return;
   const PieceAt at = piece_at(e, p);
   const int n = at.n, cb = at.cb;
   const int64_t blk = at.blk;
   const int c = (int)(blk % p.per_head) * p.cw() + cb, h = (int)(blk / p.per_head % a.H);
-  const int b = (int)(blk / p.per_head / a.H);
   const float A2 = n < a.N && c < a.d ? a.A[((int64_t)h * a.d + c) * a.N + n] * kLog2e : 0.f;
   const int span = p.chunk * kPart;
   const int64_t row = p.blocks * p.cw();
   const float* total = ws.total + blk * p.cw() + cb;
+  pdl_trigger();
+  pdl_wait();
   for (int way = 0; way < 2; ++way) {  // forward: states, backward: gradients
     float* x = (way ? ws.gin : ws.hin) + e;
     float carry = 0.f;
@@ -327,11 +344,9 @@ __global__ void join_kernel(ScanArgs a, Plan p, Ws ws) {
         x[i * per] = carry;
         bool through = way ? i + 1 < p.chunks : i > 0, on = true;
         if (a.seqs.cu) {
-          // the token behind the border that the carry crosses, and its sequence
-          const int border = way ? i * span : (i + 1) * span;
-          const TokenAt at = token_at(a.seqs, b, a.T, border, a.status);
-          on = at.live && at.lo < border;
-          through = on && (way ? at.hi > (i + 1) * span : at.lo < i * span);
+          const int mark = border[way ? i : min(i + 1, p.chunks - 1)];
+          on = mark & 1;
+          through = way ? mark & 4 : mark & 2;
         }
         carry = !on ? 0.f : through ? fmaf(dec[j], carry, local[j]) : local[j];
       }
@@ -461,6 +476,7 @@ __global__ void __launch_bounds__(128, 2) main_kernel(const __grid_constant__ Sc
   for (int k = 0; k < 4; ++k) regs.dA[k] = 0;
   rates(a, q, A2);
   if (p.chunks > 1) {
+    pdl_wait();  // launched before the joined states were there
     load_piece(ws.gin + (chat * wpb + q.warp) * kPiece, q.lane, regs.gs);
   } else {
 #pragma unroll
@@ -742,8 +758,16 @@ cudaError_t bwd(const ScanBwdArgs& ga, cudaStream_t s) {
       // starts from its own beginning
       if (p.parts > 1) pre_kernel<T, W><<<grid, 32 * nw, sizeof(First), s>>>(ga, p, ws);
       const int64_t n = p.blocks * nw * kPiece;
-      if (p.chunks > 1) join_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(a, p, ws);
-      main_kernel<T, W><<<grid, 32 * nw, sizeof(All), s>>>(ga, p, ws);
+      r = cudaGetLastError();
+      if (r != cudaSuccess) return r;
+      if (p.chunks > 1) {
+        r = launch_pdl(join_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a, p, ws);
+        if (r != cudaSuccess) return r;
+        r = launch_pdl(main_kernel<T, W>, grid, dim3(32 * nw), sizeof(All), s, ga, p, ws);
+        if (r != cudaSuccess) return r;
+      } else {
+        main_kernel<T, W><<<grid, 32 * nw, sizeof(All), s>>>(ga, p, ws);
+      }
       const int64_t bc = (int64_t)a.B * a.G * a.T * 2 * p.warps * kNB;
       put_bc_kernel<T><<<(unsigned)((bc + 255) / 256), 256, 0, s>>>(ga, p, ws.dBC);
       return cudaGetLastError();
