@@ -22,6 +22,7 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -80,13 +81,17 @@ def build(force: bool = False, verbose: bool = False, extra=(), debug_bounds: bo
         extra = (*extra, "-DTTT_DEBUG_BOUNDS")
     os.makedirs(build_dir, exist_ok=True)
     hdr_time = max([os.path.getmtime(h) for h in _headers()] + [0])
-    objs = []
+    objs, stale = [], []
     for src in sorted(glob.glob(os.path.join(CSRC, "*.cu"))):
         obj = os.path.join(build_dir, os.path.basename(src)[:-3] + ".o")
         objs.append(obj)
         if (not force and os.path.exists(obj)
                 and os.path.getmtime(obj) >= max(os.path.getmtime(src), hdr_time)):
             continue
+        stale.append((src, obj))
+
+    def compile_unit(unit):
+        src, obj = unit
         cmd = [nvcc(), *ARCH, *FLAGS, *extra, "-c", src, "-o", obj]
         if verbose:
             cmd += ["-Xptxas", "-v"]
@@ -96,6 +101,9 @@ def build(force: bool = False, verbose: bool = False, extra=(), debug_bounds: bo
             sys.stderr.write(r.stdout + r.stderr)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed on {os.path.basename(src)}")
+
+    with ThreadPoolExecutor(max(1, os.cpu_count() or 1)) as pool:  # a unit takes up to minutes
+        list(pool.map(compile_unit, stale))
     newest = max(os.path.getmtime(o) for o in objs)
     if force or not os.path.exists(lib) or os.path.getmtime(lib) < newest:
         cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", *objs, "-o", lib, "-lcuda"]

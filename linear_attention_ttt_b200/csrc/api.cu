@@ -142,7 +142,7 @@ __global__ void selftest_bounds_kernel(int* status) {
 
 extern "C" {
 
-int32_t ttt_version(void) { return 200; }
+int32_t ttt_version(void) { return 300; }
 
 ttt_status ttt_selftest_bounds(void* stream) {
 #ifdef TTT_DEBUG_BOUNDS

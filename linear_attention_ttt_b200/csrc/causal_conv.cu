@@ -277,7 +277,6 @@ __device__ __forceinline__ void conv_back(const ConvBwdArgs& a, const Run& r, fl
       }
       floats_of(v, o);
     };
-    int t = t0;
     // The walk goes in batches, the rows of the next one on their way. A batch
     // of the run's own tokens whose dx are all the run's and the sequence's own
     // (none of those is state_final's) needs no further look at its tokens.

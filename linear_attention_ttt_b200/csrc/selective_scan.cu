@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(128, sizeof(T) == 2 ? 4 : 3)
     // A token's decays are computed while the token before it is scanned, and
     // the sums over states leave four tokens at a time, one block later: the
     // exponentials run beside everything else.
-    f2 dec[4], y[4];
+    f2 dec[4], y[4] = {0, 0, 0, 0};
     {
       const f2 dt = *reinterpret_cast<const f2*>(s.dt + lane_c);
 #pragma unroll

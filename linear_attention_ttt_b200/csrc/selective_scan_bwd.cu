@@ -320,7 +320,6 @@ __global__ void join_kernel(ScanArgs a, Plan p, Ws ws) {
   const int64_t blk = at.blk;
   const int c = (int)(blk % p.per_head) * p.cw() + cb, h = (int)(blk / p.per_head % a.H);
   const float A2 = n < a.N && c < a.d ? a.A[((int64_t)h * a.d + c) * a.N + n] * kLog2e : 0.f;
-  const int span = p.chunk * kPart;
   const int64_t row = p.blocks * p.cw();
   const float* total = ws.total + blk * p.cw() + cb;
   pdl_trigger();

@@ -8,6 +8,7 @@ library; if it is missing, loading fails with an error (there is no fallback).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -314,6 +315,8 @@ def lact_swiglu_window_fwd(q, k, v, eta, W1, W2, W3, chunk: int, update_rule: in
 
 
 # ---- the recurrent block: RMS norm, short convolution, selective scan ---------
+# Every function here also takes stream= (a torch stream or a handle): the call and
+# its outputs then belong to that stream instead of the current one.
 
 _ADDRESS = {}  # of the loaded library's functions, by name; and the native binding's
 
@@ -328,19 +331,33 @@ def _load_binding():
         _ADDRESS[f.__name__] = f
 
 
-def _block_call(name, tensors, split, scalar, stream):
+def _on_stream(op):
+    """With a stream given, the call and the outputs it makes belong to that stream: memory
+    that the current stream still uses is not handed to another one."""
+    @functools.wraps(op)
+    def call(x, *args, stream=None, **kwargs):
+        if stream is None:
+            return op(x, *args, **kwargs)
+        if not hasattr(stream, "cuda_stream"):
+            handle = int(stream)
+            stream = (torch.cuda.ExternalStream(handle, device=x.device) if handle
+                      else torch.cuda.default_stream(x.device))
+        with torch.cuda.stream(stream):
+            return op(x, *args, **kwargs)
+    return call
+
+
+def _block_call(name, tensors, split, scalar):
     """Calls entry point `name` with the descriptors of `tensors` (None -> NULL), the
     scalar argument behind the first `split` of them. All tensors have to be on one
-    CUDA device; the call is made with that device current, on `stream` or its current
-    stream. csrc/binding.cpp does the marshalling."""
+    CUDA device; the call is made with that device current, on its current stream.
+    csrc/binding.cpp does the marshalling."""
     address = _ADDRESS.get(name)
     if address is None:
         _load_binding()
         address = ctypes.cast(getattr(load(), name), ctypes.c_void_p).value
         _ADDRESS[name] = address
-    if stream is not None:
-        stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    code = _ADDRESS["call"](address, tensors, split, scalar, stream, name)
+    code = _ADDRESS["call"](address, tensors, split, scalar, None, name)
     if code != 0:
         raise TTTError(code, name)
 
@@ -363,8 +380,9 @@ def _sequences(x, cu_seqlens):
     return x.shape[0] if cu_seqlens is None else cu_seqlens.shape[0] - 1
 
 
+@_on_stream
 def rms_norm_fwd(x, weight, eps: float = 1e-6, residual=None, quant: bool = False, out=None,
-                 scale=None, residual_out=None, stream=None):
+                 scale=None, residual_out=None):
     """RMS norm over the last dimension of x [B,H,T,d], or of x + residual, times weight
     ([d] or [H,d], fp32). Returns (out, scale, summed): with quant=True out holds 8-bit
     (e4m3) values and scale [B,H,T] what they are multiplied with, else scale is None;
@@ -376,23 +394,24 @@ def rms_norm_fwd(x, weight, eps: float = 1e-6, residual=None, quant: bool = Fals
         scale = torch.empty(x.shape[:3], dtype=torch.float32, device=x.device)
     if residual is not None and residual_out is None:
         residual_out = _like_tokens(x)
-    _block_call("rms_norm_fwd", (x, residual, weight, out, scale, residual_out), 3, float(eps),
-                stream)
+    _block_call("rms_norm_fwd", (x, residual, weight, out, scale, residual_out), 3, float(eps))
     return out, scale, residual_out
 
 
-def rms_norm_bwd(h, weight, dy, eps: float = 1e-6, dres=None, stream=None):
+@_on_stream
+def rms_norm_bwd(h, weight, dy, eps: float = 1e-6, dres=None):
     """Backward of rms_norm_fwd from its normalised input h (its `summed`, or x): returns
     (dh, dweight). dres is the gradient that reaches h past the norm. dh is the gradient
     of x and of the residual alike."""
     dh = _like_tokens(h)
     dw = torch.empty(weight.shape, dtype=torch.float32, device=h.device)
-    _block_call("rms_norm_bwd", (h, weight, dy, dres, dh, dw), 4, float(eps), stream)
+    _block_call("rms_norm_bwd", (h, weight, dy, dres, dh, dw), 4, float(eps))
     return dh, dw
 
 
+@_on_stream
 def causal_conv_fwd(x, weight, bias=None, silu: bool = True, state0=None, cu_seqlens=None,
-                    out=None, state_final=None, want_final: bool = True, stream=None):
+                    out=None, state_final=None, want_final: bool = True):
     """Short causal depthwise convolution of x [B,H,T,d] along T (weight [H,d,K], bias
     [H,d]), followed by silu. Returns (out, state_final): the last K-1 inputs of every
     sequence [S,H,K-1,d], which state0 of a later call or causal_conv_step continues
@@ -402,12 +421,13 @@ def causal_conv_fwd(x, weight, bias=None, silu: bool = True, state0=None, cu_seq
     if state_final is None and want_final:
         state_final = _conv_state(x, _sequences(x, cu_seqlens), weight.shape[-1])
     _block_call("causal_conv_fwd", (x, weight, bias, state0, cu_seqlens, out, state_final), 5,
-                int(bool(silu)), stream)
+                int(bool(silu)))
     return out, state_final
 
 
+@_on_stream
 def causal_conv_bwd(x, weight, dy, bias=None, silu: bool = True, state0=None, dstate_final=None,
-                    cu_seqlens=None, stream=None):
+                    cu_seqlens=None):
     """Backward of causal_conv_fwd: returns (dx, dweight, dbias, dstate0), None for the
     gradient of what was not given."""
     dx = _like_tokens(x, zero=cu_seqlens is not None)
@@ -415,25 +435,24 @@ def causal_conv_bwd(x, weight, dy, bias=None, silu: bool = True, state0=None, ds
     db = None if bias is None else torch.empty(bias.shape, dtype=torch.float32, device=x.device)
     ds = None if state0 is None else _conv_state(x, state0.shape[0], weight.shape[-1])
     _block_call("causal_conv_bwd", (x, weight, bias, state0, cu_seqlens, dy, dstate_final, dx, dw,
-                                    db, ds), 5, int(bool(silu)), stream)
+                                    db, ds), 5, int(bool(silu)))
     return dx, dw, db, ds
 
 
-def causal_conv_step(x, state, weight, bias=None, silu: bool = True, slots=None, out=None,
-                     stream=None):
+@_on_stream
+def causal_conv_step(x, state, weight, bias=None, silu: bool = True, slots=None, out=None):
     """One token of causal_conv_fwd for each of B sequences: x [B,H,1,d]; state
     [S,H,K-1,d] is updated in place. slots (int32 [B]) names each row's place in the
     state pool (-1: a padded row, left alone). Returns out."""
     if out is None:
         out = _like_tokens(x, zero=slots is not None)
-    _block_call("causal_conv_step", (x, state, slots, weight, bias, out), 5, int(bool(silu)),
-                stream)
+    _block_call("causal_conv_step", (x, state, slots, weight, bias, out), 5, int(bool(silu)))
     return out
 
 
+@_on_stream
 def selective_scan_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, softplus: bool = True,
-                       h0=None, cu_seqlens=None, out=None, h_final=None, want_final: bool = True,
-                       stream=None):
+                       h0=None, cu_seqlens=None, out=None, h_final=None, want_final: bool = True):
     """Selective state space scan: per channel, with step = softplus(dt + dt_bias),
     s <- exp(step A) s + step x Bm, y = <Cm, s> + D x, out = y silu(z). x, dt, z
     [B,H,T,d]; A [H,d,N] fp32; Bm, Cm [B,G,T,N] shared by H/G heads each; D, dt_bias
@@ -445,12 +464,13 @@ def selective_scan_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, softplus:
         h_final = torch.empty((_sequences(x, cu_seqlens), *A.shape), dtype=torch.float32,
                               device=x.device)
     _block_call("selective_scan_fwd", (x, dt, A, Bm, Cm, D, z, dt_bias, h0, cu_seqlens, out,
-                                       h_final), 10, int(bool(softplus)), stream)
+                                       h_final), 10, int(bool(softplus)))
     return out, h_final
 
 
+@_on_stream
 def selective_scan_bwd(x, dt, A, Bm, Cm, dy, D=None, z=None, dt_bias=None, softplus: bool = True,
-                       h0=None, dh_final=None, cu_seqlens=None, stream=None):
+                       h0=None, dh_final=None, cu_seqlens=None):
     """Backward of selective_scan_fwd: returns (dx, ddt, dA, dBm, dCm, dD, dz, ddt_bias,
     dh0), None for the gradient of what was not given. The states are computed again
     from the inputs."""
@@ -468,19 +488,20 @@ def selective_scan_bwd(x, dt, A, Bm, Cm, dy, D=None, z=None, dt_bias=None, softp
     dh0 = None if h0 is None else torch.empty(h0.shape, **f32)
     _block_call("selective_scan_bwd", (x, dt, A, Bm, Cm, D, z, dt_bias, h0, cu_seqlens, dy,
                                        dh_final, dx, ddt, dA, dBm, dCm, dD, dz, dbias, dh0), 10,
-                int(bool(softplus)), stream)
+                int(bool(softplus)))
     return dx, ddt, dA, dBm, dCm, dD, dz, dbias, dh0
 
 
+@_on_stream
 def selective_scan_step(x, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None,
-                        softplus: bool = True, slots=None, out=None, stream=None):
+                        softplus: bool = True, slots=None, out=None):
     """One token of selective_scan_fwd for each of B sequences: x, dt, z [B,H,1,d], Bm, Cm
     [B,G,1,N]; state [S,H,d,N] (fp32) is updated in place; slots as in causal_conv_step.
     Returns out."""
     if out is None:
         out = _like_tokens(x, zero=slots is not None)
     _block_call("selective_scan_step", (x, dt, A, Bm, Cm, D, z, dt_bias, state, slots, out), 10,
-                int(bool(softplus)), stream)
+                int(bool(softplus)))
     return out
 
 

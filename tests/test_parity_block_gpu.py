@@ -733,6 +733,59 @@ def test_another_stream():
     clean()
 
 
+def test_stream_argument():
+    """stream= takes a torch stream or a handle; the outputs made by the call are that stream's."""
+    x, w = tokens(gen(36), 2, 1, 40, 256, BF16), torch.ones(256).cuda()
+    want, _, _ = ops.rms_norm_fwd(x, w)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream, 0):
+        got, _, _ = ops.rms_norm_fwd(x, w, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+    clean()
+
+
+FIRST_IN_A_GRAPH = """
+import torch
+from linear_attention_ttt_b200 import ops
+x = torch.randn(2, 1, 100, 96, device="cuda")
+A, B = -torch.rand(1, 96, 16, device="cuda"), torch.randn(2, 1, 100, 16, device="cuda")
+w = torch.randn(1, 96, 4, device="cuda")
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    y, _, _ = ops.rms_norm_fwd(x, A[0, :, 0].contiguous())
+    u, _ = ops.causal_conv_fwd(y, w)
+    got = [y, u, *ops.selective_scan_fwd(u, x, A, B, B), *ops.selective_scan_bwd(u, x, A, B, B, x)[:5],
+           *ops.causal_conv_bwd(y, w, x)[:2], *ops.rms_norm_bwd(x, A[0, :, 0].contiguous(), x)]
+g.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in got]
+y, _, _ = ops.rms_norm_fwd(x, A[0, :, 0].contiguous())
+u, _ = ops.causal_conv_fwd(y, w)
+want = [y, u, *ops.selective_scan_fwd(u, x, A, B, B), *ops.selective_scan_bwd(u, x, A, B, B, x)[:5],
+        *ops.causal_conv_bwd(y, w, x)[:2], *ops.rms_norm_bwd(x, A[0, :, 0].contiguous(), x)]
+assert all(torch.equal(p, q) for p, q in zip(got, want)) and ops.device_status() == 0
+print("same")
+"""
+
+
+def test_first_calls_of_a_process_inside_a_graph():
+    import subprocess
+    import sys
+    r = subprocess.run([sys.executable, "-c", FIRST_IN_A_GRAPH], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
+
+
+def test_norm_of_no_tokens():
+    x, w = torch.zeros(2, 3, 0, 64, device="cuda"), torch.ones(64).cuda()
+    y, s, _ = ops.rms_norm_fwd(x, w, quant=True)
+    assert y.shape == x.shape and s.shape == (2, 3, 0)
+    dh, dw = ops.rms_norm_bwd(x, w, x)
+    assert dh.numel() == 0 and (dw == 0).all()
+    clean()
+
+
 def test_two_streams_at_once():
     """Workspaces of calls in flight beside one another are their own."""
     calls, _ = every_call(gen(33))
