@@ -2,8 +2,11 @@
  * ttt.h - C ABI of libttt_b200.so: forward pass of chunked test-time-training
  * (TTT) layers with key->value binding, on one NVIDIA B200 (sm_100a).
  *
- * Three operations, each a per-(batch, head) scan over chunks of `chunk`
- * tokens with fast weights W kept in fp32:
+ * Beside them stand the operators of a recurrent block: rms_norm_*,
+ * causal_conv_* and selective_scan_*, described where they are declared.
+ *
+ * The TTT layers are three operations, each a per-(batch, head) scan over chunks
+ * of `chunk` tokens with fast weights W kept in fp32:
  *
  *  ttt_linear_fwd, loss = TTT_LOSS_MSE  (TTT-Linear, mini-batch GD)
  *    "Test-Time Training (TTT)" summary, sections "TTT 정의", "예시 2: DeltaNet

@@ -6,6 +6,11 @@
 // has at most 32 vectors (q/k heads of 64: 8 lanes, four rows a warp), to one
 // warp up to 256 vectors (128 in the backward pass), and to a block of its own
 // above that.
+//
+// B4 T4096 d2048 bf16: forward with residual and 8-bit output 42 us (36 at the
+// measured copy rate), backward 64 us (41) with the ordered sum of
+// dweight's shares; 16 heads of 64, B8 T2048: 20 us (10), waiting on its loads
+// with 5 blocks an SM.
 #include <cuda_fp8.h>
 
 #include "block.cuh"
@@ -429,7 +434,7 @@ int bwd_blocks(const NormBwdArgs& a) {
 // weights are found once, and four loads are in flight.
 constexpr int kShortRows = 4;
 // A warp a row, without barriers, up to 256 vectors: B4 T4096 d2048 with 8-bit
-// output takes 45 us, a block of 128 threads a row 58 us. The backward pass has
+// output takes 42 us (5.6 TB/s), a block of 128 threads a row 59 us. The backward pass has
 // no registers for that beside its share of dweight.
 constexpr int kFwdVpt = 8;
 

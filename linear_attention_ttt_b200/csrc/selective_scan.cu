@@ -2,15 +2,23 @@
 // selective_scan_step of include/ttt.h).
 //
 // A warp holds 16 states of 16 channels: a lane has 4 states of 2 channels, so
-// the sum over states takes two shuffles a token and the inputs of a token are
-// a few wide reads of shared memory. N > 16 gives a channel tile a warp per 16
+// the sums over states cross four lanes only, and the inputs of a token are a
+// few wide reads of shared memory. N > 16 gives a channel tile a warp per 16
 // states, which add their parts of y through shared memory. The tokens of a
 // part (32) are staged once: softplus, the products D_t x_t and the gate are
 // computed once per element, from 16-byte loads.
 //
 // What bounds it: one exponential and four fp32 operations per (channel,
-// state, token). The special-function unit gives 16 exponentials a clock and
-// SM, which at N = 16 takes three times as long as the memory traffic does.
+// state, token), and four special functions per element beside them. The
+// special-function unit gives 16 a clock and SM: at N = 16 that is 3.5 times the
+// memory traffic's time. B16 T1024 d4096 takes 482 us, 290 of them the unit's own
+// (60 % busy); B4 T4096 d4096, with two warps a scheduler and nothing to hide
+// their latencies behind, 637 (50 %).
+//
+// The raw rows of a part arrive by asynchronous copies while the part before is
+// scanned; a token's decays are computed while the token before is; the sums
+// over states leave four tokens at a time. Whole pieces have paths of their
+// own: loads behind a choice wait for one another.
 //
 // Where B x channels give too few warps, the tokens are split into chunks: a
 // first pass computes each chunk's end state from a zero start and its sum of
@@ -26,11 +34,11 @@ struct Plan : Grid {
   int chunks, len;  // len: tokens, a multiple of kPart
 };
 // Chunks cost a second pass, which only idle SMs pay for. Measured at N = 16,
-// bf16, gated: with 1024 warps and more one chunk wins (B4 T4096 d4096: 690 us
-// against 797 with four chunks a warp; B16 T1024 d4096: 490 against 670), with
-// 256 and fewer about 4096 warps in all do (B1 T4096 d4096: 541 us in one chunk,
-// 226 in 16; B1 T16384 d2048: 2135 in one, 436 in 32). Chunks below 64 tokens
-// gain nothing.
+// bf16, gated: from 1024 warps on one chunk wins (B4 T4096 d4096: 648 us in one
+// chunk, 759 in 4, 775 in 16; B16 T1024 d4096: 483, 733, 844), with 256 and fewer
+// about 4096 warps in all do (B1 T4096 d4096: 475 us in one, 217 in 16, 221 in 32;
+// B1 T16384 d2048: 1861 in one, 472 in 16, 416 in 32). Chunks below 64 tokens gain
+// nothing.
 Plan plan(const ScanArgs& a) {
   Plan p;
   static_cast<Grid&>(p) = grid_of(a);
@@ -325,8 +333,9 @@ __global__ void copy_empty_kernel(Seqs q, int T, int64_t n, const float* src, fl
 // One token. A channel's states lie on 2^k lanes, four a lane, and a lane has
 // them of four channels: places and slots are found once for 16 states. What a
 // channel needs once (its step size, the gate) one of its lanes computes for
-// the others. Bound by memory: the states are read and written once, in
-// 16-byte pieces.
+// the others. The states are read and written once, in 16-byte pieces:
+// 64 sequences, d4096 N16 bf16, take 9.2 us a call (5.5 at the measured copy
+// rate), waiting on their loads.
 constexpr int kStepThreads = 128, kStepCh = 4;
 
 // kWhole: N is 4 kLanes, the block's channels all exist and every row is

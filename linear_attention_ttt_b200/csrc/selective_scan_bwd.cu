@@ -4,10 +4,10 @@
 // block up to four warps: channel tiles of one head beside one another, or the
 // 16-state parts of one tile. The tokens are worked in parts of 32:
 //   - forward through the part, keeping the state before every fourth token in
-//     shared memory (and y, which the gate's gradient needs);
+//     shared memory;
 //   - backward through its blocks of four tokens: each is run forward once
 //     more from its kept state with the decays and states in registers, then
-//     backward, carrying g.
+//     backward, carrying g; y, which the gate's gradient needs, comes along.
 // So a part takes two exponentials per (channel, state, token), and states
 // never travel token by token through memory.
 //
@@ -20,7 +20,12 @@
 // leave a block as partial sums that a second kernel adds in order.
 //
 // What bounds it: three exponentials and about 21 fp32 operations per
-// (channel, state, token) in both passes together.
+// (channel, state, token) in both passes together, and the sums over channels:
+// every token leaves 32 sums over 16 channels a warp, which cost about as many
+// instructions as the recurrence. B2 T2048 d2048 N16 takes 369 us; in a
+// profile the main pass is 273 (two blocks an SM by registers and shared memory,
+// 40 % of the issue slots used) and the first pass 70. At the special-function
+// unit's rate alone both together would be 101 us.
 #include "scan.cuh"
 
 namespace ttt {
@@ -38,11 +43,11 @@ Plan plan(const ScanArgs& a) {
   Plan p;
   static_cast<Grid&>(p) = grid_of(a);
   p.parts = (a.T + kPart - 1) / kPart;
-  // Blocks run three an SM; a chunk costs its parts and about 0.6 of one for
+  // Blocks run two an SM; a chunk costs its parts and about 0.6 of one for
   // itself (rates, sums, the join), the last round of blocks 0.8 of a chunk.
-  // Measured against this, chunks of 1 to 64 parts: B4 T2048 d4096 takes 1327 us
-  // at its best (3 parts; 4 parts, which this picks, 1351; 1 part 1457, 64 parts
-  // 1816), B1 T2048 d4096 394 us (3 parts; 2, picked, 424; 64 parts 1396).
+  // Measured (N 16, bf16, gated) in chunks of 1, 2, 4, 8, 64 parts: B4 T2048 d4096
+  // 1319, 1278, 1244, 1229, 1449 us; B1 T8192 d2048 734, 672, 653, 673, 1370;
+  // B1 T200 d512 55, 58, 90, 129, 129.
   const double slots = 148 * 2;
   double best = 0;
   p.chunk = 1;
