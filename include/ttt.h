@@ -436,7 +436,8 @@ ttt_status rms_norm_fwd(const ttt_tensor* x, const ttt_tensor* residual,
  * dh is the gradient of x and of the residual alike.
  *  h, dy   [B,H,T,d]; dres NULL or [B,H,T,d]: the gradient that reaches h
  *          through residual_out; dh [B,H,T,d]; all of h's type
- *  dweight weight's shape, fp32 contiguous (summed over what shares it)
+ *  dweight weight's shape, fp32 contiguous (summed over what shares it); a weight
+ *          [H,d] has at most 65535 heads here
  */
 ttt_status rms_norm_bwd(const ttt_tensor* h, const ttt_tensor* weight, const ttt_tensor* dy,
                         const ttt_tensor* dres, float eps, const ttt_tensor* dh,

@@ -1058,6 +1058,8 @@ ttt_status rms_norm_bwd(const ttt_tensor* h, const ttt_tensor* weight, const ttt
   if (dres && (st = check_rows(dres, n.B, n.H, n.T, n.d, h->dtype, &a.wide)) != TTT_OK) return st;
   if ((st = check_out_rows(dh, n, n.d, h->dtype, &a.wide)) != TTT_OK) return st;
   if (dweight->ndim != weight->ndim) return TTT_ERR_SHAPE;
+  // a weight per head has a grid row per head
+  if (weight->ndim == 2 && n.H > 65535) return TTT_ERR_UNSUPPORTED;
   if ((st = check_f32(dweight, weight->ndim, weight->shape, false)) != TTT_OK) return st;
   const ttt_tensor* const ins[] = {h, weight, dy, dres};
   const ttt_tensor* const outs[] = {dh, dweight};

@@ -284,3 +284,19 @@ def test_new_token_tensors_have_aligned_rows():
     assert y.shape == x.shape and all(s * 2 % 16 == 0 for s in y.stride()[:3]) and y.stride(1) < y.stride(2)
     q = ops._like_tokens(x, dtype=torch.float8_e4m3fn)
     assert all(s % 16 == 0 for s in q.stride()[:3])
+
+
+@pytest.mark.parametrize("heads,shared,ok", [(65535, False, True), (65536, False, False), (65536, True, True)])
+def test_norm_backward_heads_of_a_weight(lib, heads, shared, ok):
+    """A weight per head takes a row of blocks per head, of which a launch has 65535 at
+    most; a shared weight has no such limit."""
+    w = (8,) if shared else (heads, 8)
+    new = dict(h=tok(1, heads, 1, 8), weight=dense(w, 0), dy=tok(1, heads, 1, 8), dres=tok(1, heads, 1, 8),
+               dh=tok(1, heads, 1, 8), dweight=dense(w, 0))
+    for i, t in enumerate(new.values()):
+        t.data = FAKE + i * GAP
+    st = NormBwd()(lib, **new)
+    if ok:
+        assert st in (ERR["TTT_ERR_CUDA"], ERR["TTT_ERR_ALLOC"])
+    else:
+        assert st == ERR["TTT_ERR_UNSUPPORTED"]
