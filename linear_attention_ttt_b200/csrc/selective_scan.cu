@@ -131,8 +131,10 @@ __global__ void __launch_bounds__(128, sizeof(T) == 2 ? 4 : 3)
     const int nt = min(kPart, t1 - tb);
     const Marks now = next;
     copy_wait<kPre ? 0 : 1>();
-    if (q.warp == 0) s.seq[q.lane] = seq;
     __syncthreads();
+    // Every warp has left the part before: the first pass has no barrier at a
+    // part's end, and a warp behind still reads the old sequences there.
+    if (q.warp == 0) s.seq[q.lane] = seq;
     // stage the part: step sizes, inputs, and D x where y is summed up
 #pragma unroll
     for (int r = 0; r < kPart; r += dr) {
