@@ -7,9 +7,15 @@
 // C function's address (from the loaded library), `tensors` a tuple of tensors
 // or None, the scalar argument goes behind the first `split` of them. `stream`
 // is None for the tensors' device's current stream, or a stream's handle.
+//
+// Whatever torch throws (a tensor without memory of its own, as inside
+// torch.func's transforms; an allocation that fails) becomes the Python
+// exception that torch itself raises for it.
 #include <ATen/ATen.h>
 #include <torch/csrc/Dtype.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/utils/object_ptr.h>
 
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -37,6 +43,7 @@ ttt_status invoke(void* f, ttt_tensor* const* t, S scalar, void* stream) {
 }
 
 PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+  HANDLE_TH_ERRORS
   if (nargs != 6 || !PyTuple_Check(args[1])) {
     PyErr_SetString(PyExc_TypeError, "call(function, tensors, split, scalar, stream, name)");
     return nullptr;
@@ -99,7 +106,7 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   }
   ttt_status st = TTT_ERR_ARG;
   bool known = true;
-  try {
+  {
     const c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, (c10::DeviceIndex)device));
     void* s = args[4] == Py_None ? (void*)c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream() : given;
     Py_BEGIN_ALLOW_THREADS
@@ -115,15 +122,13 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     else if (!real && split == 10 && n == 21) st = invoke<10, 11>(fn, t, k, s);
     else known = false;
     Py_END_ALLOW_THREADS
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
-    return nullptr;
   }
   if (!known) {
     PyErr_Format(PyExc_ValueError, "%s: no such call", name);
     return nullptr;
   }
   return PyLong_FromLong(st);
+  END_HANDLE_TH_ERRORS
 }
 
 // Layout of a new token tensor [B,H,T,d]: x's order of storage (heads before or
@@ -142,6 +147,7 @@ struct Rows {
 };
 
 PyObject* like_tokens(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+  HANDLE_TH_ERRORS
   if (nargs != 4 || !THPVariable_Check(args[0]) || !THPDtype_Check(args[2])) {
     PyErr_SetString(PyExc_TypeError, "like_tokens(x, d, dtype, zero)");
     return nullptr;
@@ -155,61 +161,54 @@ PyObject* like_tokens(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     PyErr_SetString(PyExc_ValueError, "tokens are [B,H,T,d]");
     return nullptr;
   }
-  try {
-    const Rows r(x, d, (int64_t)c10::elementSize(type));
-    const auto opt = x.options().dtype(type).requires_grad(false);
-    const at::Tensor t = zero ? at::zeros({r.count}, opt) : at::empty({r.count}, opt);
-    return THPVariable_Wrap(t.as_strided(r.size, r.stride));
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
-    return nullptr;
-  }
+  const Rows r(x, d, (int64_t)c10::elementSize(type));
+  const auto opt = x.options().dtype(type).requires_grad(false);
+  const at::Tensor t = zero ? at::zeros({r.count}, opt) : at::empty({r.count}, opt);
+  return THPVariable_Wrap(t.as_strided(r.size, r.stride));
+  END_HANDLE_TH_ERRORS
 }
 
 // New zero tensors like each of a tuple of token tensors of one type (None gives
 // None), in one allocation with one fill.
 PyObject* zeros_like_tokens(PyObject*, PyObject* arg) {
+  HANDLE_TH_ERRORS
   if (!PyTuple_Check(arg)) {
     PyErr_SetString(PyExc_TypeError, "zeros_like_tokens((x, ...))");
     return nullptr;
   }
   const Py_ssize_t n = PyTuple_GET_SIZE(arg);
-  try {
-    std::vector<Rows> rows;
-    const at::Tensor* first = nullptr;
-    int64_t total = 0;
-    for (Py_ssize_t i = 0; i < n; ++i) {
-      PyObject* o = PyTuple_GET_ITEM(arg, i);
-      if (o == Py_None) continue;
-      if (!THPVariable_Check(o) || THPVariable_Unpack(o).dim() != 4) {
-        PyErr_SetString(PyExc_ValueError, "tokens are [B,H,T,d]");
-        return nullptr;
-      }
-      const at::Tensor& x = THPVariable_Unpack(o);
-      if (!first) first = &x;
-      rows.emplace_back(x, x.size(3), (int64_t)x.element_size());
-      total += rows.back().count;
+  std::vector<Rows> rows;
+  const at::Tensor* first = nullptr;
+  int64_t total = 0;
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    PyObject* o = PyTuple_GET_ITEM(arg, i);
+    if (o == Py_None) continue;
+    if (!THPVariable_Check(o) || THPVariable_Unpack(o).dim() != 4) {
+      PyErr_SetString(PyExc_ValueError, "tokens are [B,H,T,d]");
+      return nullptr;
     }
-    PyObject* out = PyTuple_New(n);
-    if (!out) return nullptr;
-    at::Tensor all;
-    if (first) all = at::zeros({total}, first->options().requires_grad(false));
-    int64_t at_ = 0;
-    size_t k = 0;
-    for (Py_ssize_t i = 0; i < n; ++i) {
-      if (PyTuple_GET_ITEM(arg, i) == Py_None) {
-        Py_INCREF(Py_None);
-        PyTuple_SET_ITEM(out, i, Py_None);
-        continue;
-      }
-      PyTuple_SET_ITEM(out, i, THPVariable_Wrap(all.as_strided(rows[k].size, rows[k].stride, at_)));
-      at_ += rows[k++].count;
-    }
-    return out;
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
-    return nullptr;
+    const at::Tensor& x = THPVariable_Unpack(o);
+    if (!first) first = &x;
+    rows.emplace_back(x, x.size(3), (int64_t)x.element_size());
+    total += rows.back().count;
   }
+  THPObjectPtr out(PyTuple_New(n));
+  if (!out) return nullptr;
+  at::Tensor all;
+  if (first) all = at::zeros({total}, first->options().requires_grad(false));
+  int64_t at_ = 0;
+  size_t k = 0;
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    if (PyTuple_GET_ITEM(arg, i) == Py_None) {
+      Py_INCREF(Py_None);
+      PyTuple_SET_ITEM(out.get(), i, Py_None);
+      continue;
+    }
+    PyTuple_SET_ITEM(out.get(), i, THPVariable_Wrap(all.as_strided(rows[k].size, rows[k].stride, at_)));
+    at_ += rows[k++].count;
+  }
+  return out.release();
+  END_HANDLE_TH_ERRORS
 }
 
 PyMethodDef methods[] = {
