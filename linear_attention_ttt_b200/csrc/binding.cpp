@@ -82,6 +82,10 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
       PyErr_Format(PyExc_ValueError, "%s: tensors have to be strided, of at most 4 dimensions", name);
       return nullptr;
     }
+    if (v.is_neg()) {  // its memory holds the values with the other sign
+      PyErr_Format(PyExc_ValueError, "%s: argument %zd is a negated view: resolve_neg() first", name, i);
+      return nullptr;
+    }
     ttt_tensor& d = desc[i];
     switch (v.scalar_type()) {
       case at::kFloat: d.dtype = TTT_F32; break;

@@ -52,3 +52,26 @@ def test_tokens_of_ragged_sizes_raise():
     t = torch.nested.nested_tensor([torch.zeros(2, 3, 8), torch.zeros(1, 3, 8)])
     with pytest.raises(RuntimeError):
         ops._like_tokens(t, 8, torch.float32)
+
+
+NEGATED = """
+import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
+from linear_attention_ttt_b200 import ops
+with FakeTensorMode():
+    x, w = torch.empty(1, 1, 4, 8, device="cuda"), torch.empty(8, device="cuda")
+    n = torch.empty(1, 1, 4, 8, 1, dtype=torch.complex64, device="cuda").conj().imag[..., 0]
+    assert n.is_neg()
+    for t in ((n, None, w, x, None, None), (x, None, w, n, None, None)):
+        try:
+            ops._block_call("rms_norm_fwd", t, 3, 1e-6)
+        except ValueError as e:
+            print("refused", e)
+"""
+
+
+def test_a_negated_view_is_refused():
+    """The imaginary part of a conjugate is a view of memory that holds its values with the
+    other sign."""
+    r = run(NEGATED)
+    assert r.returncode == 0 and r.stdout.count("refused") == 2, (r.stdout, r.stderr[-500:])
