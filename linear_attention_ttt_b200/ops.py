@@ -335,15 +335,16 @@ def _on_stream(op):
     """With a stream given, the call and the outputs it makes belong to that stream: memory
     that the current stream still uses is not handed to another one."""
     @functools.wraps(op)
-    def call(x, *args, stream=None, **kwargs):
+    def call(*args, stream=None, **kwargs):
         if stream is None:
-            return op(x, *args, **kwargs)
+            return op(*args, **kwargs)
         if not hasattr(stream, "cuda_stream"):
             handle = int(stream)
-            stream = (torch.cuda.ExternalStream(handle, device=x.device) if handle
-                      else torch.cuda.default_stream(x.device))
+            device = next(t.device for t in (*args, *kwargs.values()) if torch.is_tensor(t))
+            stream = (torch.cuda.ExternalStream(handle, device=device) if handle
+                      else torch.cuda.default_stream(device))
         with torch.cuda.stream(stream):
-            return op(x, *args, **kwargs)
+            return op(*args, **kwargs)
     return call
 
 

@@ -1,5 +1,7 @@
 """The Python half of the recurrent block's calls, without a GPU: what reaches the native
 binding, and what comes back from it."""
+import contextlib
+import inspect
 import os
 import subprocess
 import sys
@@ -75,3 +77,56 @@ def test_a_negated_view_is_refused():
     other sign."""
     r = run(NEGATED)
     assert r.returncode == 0 and r.stdout.count("refused") == 2, (r.stdout, r.stderr[-500:])
+
+
+# ---- arguments by name ----------------------------------------------------------------------
+
+def arguments(T=4, B=2, H=2, d=8, N=4, K=4):
+    """op -> its required arguments by name."""
+    x, s = torch.zeros(B, H, T, d), torch.zeros(B, H, 1, d)
+    bc, bc1 = torch.zeros(B, 1, T, N), torch.zeros(B, 1, 1, N)
+    A, w = torch.zeros(H, d, N), torch.zeros(H, d, K)
+    return dict(rms_norm_fwd=dict(x=x, weight=x[0, 0, 0]), rms_norm_bwd=dict(h=x, weight=x[0, 0, 0], dy=x),
+                causal_conv_fwd=dict(x=x, weight=w), causal_conv_bwd=dict(x=x, weight=w, dy=x),
+                causal_conv_step=dict(x=s, state=torch.zeros(B, H, K - 1, d), weight=w),
+                selective_scan_fwd=dict(x=x, dt=x, A=A, Bm=bc, Cm=bc),
+                selective_scan_bwd=dict(x=x, dt=x, A=A, Bm=bc, Cm=bc, dy=x),
+                selective_scan_step=dict(x=s, dt=s, A=A, Bm=bc1, Cm=bc1, state=torch.zeros(B, H, d, N)))
+
+
+@pytest.fixture
+def reached(monkeypatch):
+    """The calls that reach the library, in place of making them."""
+    got = []
+    monkeypatch.setattr(ops, "_block_call", lambda name, tensors, split, scalar: got.append((name, tensors)))
+    return got
+
+
+@pytest.mark.parametrize("name", arguments())
+def test_arguments_may_be_named(name, reached):
+    op, kw = getattr(ops, name), arguments()[name]
+    required = [k for k, p in inspect.signature(op).parameters.items() if p.default is p.empty]
+    assert required == list(kw)
+    op(*kw.values())
+    op(**kw)
+    op(**dict(reversed(kw.items())))
+    assert [r[0] for r in reached] == [name] * 3
+    for _, tensors in reached[1:]:
+        assert [t.data_ptr() for t in tensors if any(t is v for v in kw.values())] == \
+               [t.data_ptr() for t in reached[0][1] if any(t is v for v in kw.values())]
+    with pytest.raises(TypeError):
+        op(**kw, no_such_argument=1)
+    with pytest.raises(TypeError):
+        op(**{("x" if k == "h" else "h" if k == "x" else k): v for k, v in kw.items()})
+
+
+@pytest.mark.parametrize("name", arguments())
+def test_a_stream_and_named_arguments(name, reached, monkeypatch):
+    used = []
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: used.append(s) or contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device: ("default", device))
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device: (handle, device))
+    cpu = torch.device("cpu")
+    for handle in (0, 7):
+        getattr(ops, name)(**arguments()[name], stream=handle)
+    assert used == [("default", cpu), (7, cpu)] and len(reached) == 2
