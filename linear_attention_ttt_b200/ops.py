@@ -338,11 +338,13 @@ def _on_stream(op):
     def call(*args, stream=None, **kwargs):
         if stream is None:
             return op(*args, **kwargs)
+        device = next(t.device for t in (*args, *kwargs.values()) if torch.is_tensor(t))
         if not hasattr(stream, "cuda_stream"):
             handle = int(stream)
-            device = next(t.device for t in (*args, *kwargs.values()) if torch.is_tensor(t))
             stream = (torch.cuda.ExternalStream(handle, device=device) if handle
                       else torch.cuda.default_stream(device))
+        elif stream.device != device:
+            raise ValueError(f"{op.__name__}: a stream of {stream.device} for tensors on {device}")
         with torch.cuda.stream(stream):
             return op(*args, **kwargs)
     return call

@@ -130,3 +130,14 @@ def test_a_stream_and_named_arguments(name, reached, monkeypatch):
     for handle in (0, 7):
         getattr(ops, name)(**arguments()[name], stream=handle)
     assert used == [("default", cpu), (7, cpu)] and len(reached) == 2
+
+
+@pytest.mark.parametrize("name", arguments())
+def test_a_stream_of_another_device_is_refused(name, reached, monkeypatch):
+    """The call would run on the tensors' device, on a stream that is not the one given."""
+    class Stream:
+        cuda_stream, device = 7, torch.device("cuda", 1)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    with pytest.raises(ValueError, match="stream"):
+        getattr(ops, name)(**arguments()[name], stream=Stream())
+    assert not reached
