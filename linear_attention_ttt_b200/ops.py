@@ -318,17 +318,20 @@ def lact_swiglu_window_fwd(q, k, v, eta, W1, W2, W3, chunk: int, update_rule: in
 # Every function here also takes stream= (a torch stream or a handle): the call and
 # its outputs then belong to that stream instead of the current one.
 
-_ADDRESS = {}  # of the loaded library's functions, by name; and the native binding's
+_ADDRESS = {}   # of the loaded library's functions, by name
+_NATIVE = None  # the native half, csrc/binding.cpp
 
 
-def _load_binding():
-    try:
-        from . import _binding
-    except ImportError as e:
-        raise OSError(f"{_PKG}/_binding.so is missing or does not load: run "
-                      f"`python -m linear_attention_ttt_b200.build`") from e
-    for f in (_binding.call, _binding.like_tokens, _binding.zeros_like_tokens):
-        _ADDRESS[f.__name__] = f
+def _native():
+    global _NATIVE
+    if _NATIVE is None:
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise OSError(f"{_PKG}/_binding.so is missing or does not load: run "
+                          f"`python -m linear_attention_ttt_b200.build`") from e
+        _NATIVE = _binding  # whole at once: another thread may be making its first call
+    return _NATIVE
 
 
 def _on_stream(op):
@@ -357,10 +360,9 @@ def _block_call(name, tensors, split, scalar):
     csrc/binding.cpp does the marshalling."""
     address = _ADDRESS.get(name)
     if address is None:
-        _load_binding()
         address = ctypes.cast(getattr(load(), name), ctypes.c_void_p).value
         _ADDRESS[name] = address
-    code = _ADDRESS["call"](address, tensors, split, scalar, None, name)
+    code = _native().call(address, tensors, split, scalar, None, name)
     if code != 0:
         raise TTTError(code, name)
 
@@ -368,9 +370,7 @@ def _block_call(name, tensors, split, scalar):
 def _like_tokens(x, d=None, dtype=None, zero=False):
     """A new token tensor [B,H,T,d] with x's order of storage (heads before or behind
     tokens) and rows of a multiple of 16 bytes."""
-    if not _ADDRESS:
-        _load_binding()
-    return _ADDRESS["like_tokens"](x, x.shape[3] if d is None else d, dtype or x.dtype, zero)
+    return _native().like_tokens(x, x.shape[3] if d is None else d, dtype or x.dtype, zero)
 
 
 def _conv_state(x, S, K):
@@ -482,9 +482,7 @@ def selective_scan_bwd(x, dt, A, Bm, Cm, dy, D=None, z=None, dt_bias=None, softp
     if cu_seqlens is None:
         dx, ddt, dz, dBm, dCm = (None if t is None else _like_tokens(t) for t in like)
     else:  # rows behind the last sequence stay zero
-        if not _ADDRESS:
-            _load_binding()
-        dx, ddt, dz, dBm, dCm = _ADDRESS["zeros_like_tokens"](like)
+        dx, ddt, dz, dBm, dCm = _native().zeros_like_tokens(like)
     dA = torch.empty(A.shape, **f32)
     dD = None if D is None else torch.empty(D.shape, **f32)
     dbias = None if dt_bias is None else torch.empty(dt_bias.shape, **f32)

@@ -141,3 +141,44 @@ def test_a_stream_of_another_device_is_refused(name, reached, monkeypatch):
     with pytest.raises(ValueError, match="stream"):
         getattr(ops, name)(**arguments()[name], stream=Stream())
     assert not reached
+
+
+# ---- first calls ------------------------------------------------------------------------------
+
+FIRST_CALLS = """
+import threading, time, torch
+import linear_attention_ttt_b200 as package
+from linear_attention_ttt_b200 import _binding as real, ops
+
+class Slow:  # a function of the native half that takes its time to say its name
+    def __init__(self, f):
+        self.f = f
+    @property
+    def __name__(self):
+        time.sleep(0.05)
+        return self.f.__name__
+    def __call__(self, *args):
+        return self.f(*args)
+
+class Module:
+    call, like_tokens, zeros_like_tokens = Slow(real.call), Slow(real.like_tokens), Slow(real.zeros_like_tokens)
+
+package._binding = Module
+x, failed = torch.zeros(1, 1, 4, 8), []
+
+def first(i):
+    time.sleep(0.02 * i)
+    try:
+        ops._like_tokens(x)
+    except Exception as e:
+        failed.append(repr(e))
+
+threads = [threading.Thread(target=first, args=(i,)) for i in range(10)]
+[t.start() for t in threads], [t.join() for t in threads]
+assert not failed, failed
+"""
+
+
+def test_first_calls_of_two_threads():
+    r = run(FIRST_CALLS)
+    assert r.returncode == 0, r.stderr[-500:]
