@@ -50,27 +50,44 @@ def _headers():
     return glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(ROOT, "include", "*.h"))
 
 
+def binding_key() -> str:
+    """What _binding.so is compiled against: torch, its C++ ABI and Python's."""
+    import sysconfig
+
+    import torch
+    return (f"torch {torch.__version__} {torch.version.git_version} "
+            f"cxx11abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)} python {sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
 def build_binding(force: bool = False) -> str:
-    """_binding.so (see csrc/binding.cpp). Only torch's headers and libraries are used."""
+    """_binding.so (see csrc/binding.cpp). Only torch's headers and libraries are used. It is
+    built again when its source or what it is compiled against has changed."""
     newest = max(os.path.getmtime(f) for f in (BINDING_SRC, os.path.join(ROOT, "include", "ttt.h")))
-    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
+    key, stamp = binding_key(), os.path.join(BUILD, "binding.key")
+    if (not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest
+            and os.path.exists(stamp) and open(stamp).read() == key):
         return BINDING
     import sysconfig
 
     import torch
+    os.makedirs(BUILD, exist_ok=True)
+    if os.path.exists(stamp):
+        os.remove(stamp)
     base = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     inc = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
     lib = os.path.join(base, "lib")
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DTTT_BUILT_FOR="{key}"',
            *(f"-I{i}" for i in inc), BINDING_SRC, "-o", BINDING, f"-L{lib}", f"-Wl,-rpath,{lib}",
            "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError("g++ failed on binding.cpp")
+    with open(stamp, "w") as f:
+        f.write(key)
     return BINDING
 
 

@@ -330,6 +330,10 @@ def _native():
         except ImportError as e:
             raise OSError(f"{_PKG}/_binding.so is missing or does not load: run "
                           f"`python -m linear_attention_ttt_b200.build`") from e
+        from .build import binding_key
+        if _binding.built_for != binding_key():
+            raise OSError(f"{_PKG}/_binding.so was built for {_binding.built_for}, not for "
+                          f"{binding_key()}: run `python -m linear_attention_ttt_b200.build`")
         _NATIVE = _binding  # whole at once: another thread may be making its first call
     return _NATIVE
 

@@ -161,6 +161,7 @@ class Slow:  # a function of the native half that takes its time to say its name
         return self.f(*args)
 
 class Module:
+    built_for = real.built_for
     call, like_tokens, zeros_like_tokens = Slow(real.call), Slow(real.like_tokens), Slow(real.zeros_like_tokens)
 
 package._binding = Module
@@ -182,3 +183,42 @@ assert not failed, failed
 def test_first_calls_of_two_threads():
     r = run(FIRST_CALLS)
     assert r.returncode == 0, r.stderr[-500:]
+
+
+# ---- what the native half is built against ------------------------------------------------------
+
+def test_the_binding_is_built_again_for_another_torch(tmp_path, monkeypatch):
+    monkeypatch.setattr(B, "BUILD", str(tmp_path / "objects"))
+    monkeypatch.setattr(B, "BINDING", str(tmp_path / "_binding.so"))
+    compiled = []
+
+    def compile_it(cmd, **_):
+        compiled.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+    monkeypatch.setattr(B.subprocess, "run", compile_it)
+    B.build_binding()
+    B.build_binding()
+    assert len(compiled) == 1
+    monkeypatch.setattr(torch, "__version__", "0.0.0")
+    B.build_binding()
+    B.build_binding()
+    assert len(compiled) == 2 and any("0.0.0" in c for c in compiled[1])
+    os.remove(tmp_path / "_binding.so")
+    B.build_binding()
+    assert len(compiled) == 3
+    B.build_binding(force=True)
+    assert len(compiled) == 4
+    monkeypatch.setattr(B.subprocess, "run", lambda cmd, **_: subprocess.CompletedProcess(cmd, 1, "", ""))
+    with pytest.raises(RuntimeError):
+        B.build_binding(force=True)
+    monkeypatch.setattr(B.subprocess, "run", compile_it)
+    B.build_binding()  # what a failed build left behind is not taken for whole
+    assert len(compiled) == 5
+
+
+def test_a_binding_built_for_another_torch_is_refused(monkeypatch):
+    monkeypatch.setattr(ops, "_NATIVE", None)
+    monkeypatch.setattr(torch, "__version__", "0.0.0")
+    with pytest.raises(OSError, match="0.0.0"):
+        ops._like_tokens(torch.zeros(1, 1, 4, 8))
