@@ -418,8 +418,9 @@ ttt_status lact_swiglu_window_fwd(const ttt_tensor* q, const ttt_tensor* k, cons
  *  eps          finite, >= 0 (a row of zeros with eps = 0 gives zeros)
  *  out          [B,H,T,d] of x's type, or TTT_E4M3: then per token
  *               scale = max_d |out| / 448 and the stored 8-bit values are
- *               out / scale rounded to the nearest (ties to even); a token
- *               of zeros has scale 0
+ *               the fp32 quotients out / scale rounded to the nearest (ties
+ *               to even, at most 448), out being the fp32 value; a token of
+ *               zeros has scale 0
  *  scale        [B,H,T] fp32, any strides; required for a TTT_E4M3 out and
  *               NULL otherwise
  *  residual_out NULL or [B,H,T,d] of x's type: s (requires residual)

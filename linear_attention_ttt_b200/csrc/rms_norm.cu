@@ -7,7 +7,7 @@
 // warp up to 256 vectors (128 in the backward pass), and to a block of its own
 // above that.
 //
-// B4 T4096 d2048 bf16: forward with residual and 8-bit output 42 us (36 at the
+// B4 T4096 d2048 bf16: forward with residual and 8-bit output 43 us (36 at the
 // measured copy rate), backward 64 us (41) with the ordered sum of
 // dweight's shares; 16 heads of 64, B8 T2048: 20 us (10), waiting on its loads
 // with 5 blocks an SM.
@@ -256,21 +256,26 @@ __device__ __forceinline__ void norm_rows(const NormArgs& a, int lanes, float* r
     if (k >= n) break;
     const float scale = top[k] / 448.f;
     if (lane == 0) a.scale[at.b * a.sc_sb + at.h * a.sc_sh + (t0 + k) * a.sc_st] = scale;
-    // the quotient by the reciprocal is at most an fp32 step off, well within
-    // e4m3's; tiny scales have none and keep the division
+    // The fp32 quotient, as a division rounds it: s / scale by the reciprocal is an
+    // fp32 step off at times, and next to the middle between two 8-bit values that
+    // step decides; the remainder (exact in an fma) puts it right. Scales whose
+    // remainders would leave fp32's range keep the division.
     const float inv = 1.f / scale;
-    const bool tiny = scale < 1e-36f;
+    const bool divide = !(scale >= 1e-28f && scale < INFINITY);
     uint8_t* o = static_cast<uint8_t*>(a.out.p) + at.b * a.out.sb + at.h * a.out.sh + (t0 + k) * a.out.st;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = (i * lanes + lane) * V;
       float y[8];
-      if (tiny) {
+      if (divide) {
 #pragma unroll
         for (int j = 0; j < V; ++j) y[j] = scale == 0.f ? s[k][i][j] : s[k][i][j] / scale;
       } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j) y[j] = s[k][i][j] * inv;
+        for (int j = 0; j < V; j += 2) {
+          const f2 v = mk2(s[k][i][j], s[k][i][j + 1]), q = mul2(v, mk2(inv, inv));
+          un2(fma2(fma2(q, mk2(-scale, -scale), v), mk2(inv, inv), q), y[j], y[j + 1]);
+        }
       }
       store_e4m3<V>(o + c, kWhole ? V : a.d - c, kWhole || a.wide, y);
     }
@@ -434,7 +439,7 @@ int bwd_blocks(const NormBwdArgs& a) {
 // weights are found once, and four loads are in flight.
 constexpr int kShortRows = 4;
 // A warp a row, without barriers, up to 256 vectors: B4 T4096 d2048 with 8-bit
-// output takes 42 us (5.6 TB/s), a block of 128 threads a row 59 us. The backward pass has
+// output takes 43 us (5.4 TB/s), a block of 128 threads a row 59 us. The backward pass has
 // no registers for that beside its share of dweight.
 constexpr int kFwdVpt = 8;
 
