@@ -92,9 +92,18 @@ __device__ __forceinline__ RowAt row_at(int64_t r, int H, int T) {
 }
 
 // (mean + eps)^(-1/2); a row of zeros with eps = 0 has nothing to scale.
-__device__ __forceinline__ float inv_rms(float sumsq, int d, float eps) {
-  const float m = sumsq / (float)d + eps;
-  return m > 0.f || m != m ? rsqrtf(m) : 0.f;
+__device__ __forceinline__ float inv_rms(float m) { return m > 0.f || m != m ? rsqrtf(m) : 0.f; }
+
+// Whether a row's mean square (with eps) overflowed, or is so small that squares
+// may have been lost: below 2^-90 they come near fp32's smallest number.
+__device__ __forceinline__ bool lost_squares(float m) { return !(m >= 0x1p-90f && m < INFINITY); }
+// The power of two that brings such a row's largest magnitude, or the root of eps,
+// near 1; 1 for a row that has none (infinities, NaN).
+__device__ __forceinline__ float row_scale(float top, float eps) {
+  if (!(top < INFINITY)) return 1.f;
+  auto exponent = [](float x) { return (int)(__float_as_uint(x) >> 23) - 127; };
+  const int k = max(exponent(top), eps > 0.f ? exponent(eps) / 2 : -126);
+  return __uint_as_float((uint32_t)(127 - min(max(k, -126), 126)) << 23);
 }
 
 // V quotients as 8-bit values, n of them to memory.
@@ -219,13 +228,47 @@ __device__ __forceinline__ void norm_rows(const NormArgs& a, int lanes, float* r
       }
   }
   row_reduce<false>(sum, lanes, red);
+  float m[R];  // mean square and eps
+  bool lost = false;
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    m[k] = sum[k] / (float)a.d + a.eps;
+    lost |= lost_squares(m[k]);
+  }
+  if (__any_sync(0xffffffffu, lost)) {  // rare; a row's threads agree
+    float top[R], by[R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      top[k] = 0.f;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) top[k] = join<true>(top[k], fabsf(s[k][i][j]));
+    }
+    row_reduce<true>(top, lanes, red);
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      by[k] = lost_squares(m[k]) ? row_scale(top[k], a.eps) : 1.f;
+      sum[k] = 0.f;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          s[k][i][j] *= by[k];
+          sum[k] = fmaf(s[k][i][j], s[k][i][j], sum[k]);
+        }
+    }
+    row_reduce<false>(sum, lanes, red);
+#pragma unroll
+    for (int k = 0; k < R; ++k) m[k] = sum[k] / (float)a.d + a.eps * by[k] * by[k];
+  }
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     float f[V];
     weights<kWhole, V>(w, (i * lanes + lane) * V, a.d, f);
 #pragma unroll
     for (int k = 0; k < R; ++k) {
-      const float rs = inv_rms(sum[k], a.d, a.eps);
+      const float rs = inv_rms(m[k]);
 #pragma unroll
       for (int j = 0; j < V; ++j) s[k][i][j] = s[k][i][j] * rs * f[j];
     }
@@ -363,8 +406,32 @@ __device__ __forceinline__ void norm_back(const NormBwdArgs& a, int lanes, int64
       }
     }
     row_reduce<false>(sums, lanes, red);
-    const float rs = inv_rms(sums[0], a.d, a.eps);
-    const float m = sums[1] / (float)a.d * rs * rs;
+    float ms = sums[0] / (float)a.d + a.eps, by = 1.f;  // mean square; what the row is multiplied with
+    if (__any_sync(0xffffffffu, lost_squares(ms))) {  // rare; a row's threads agree
+      float top[1] = {0.f};
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) top[0] = join<true>(top[0], fabsf(h[i][j]));
+      row_reduce<true>(top, lanes, red);
+      if (lost_squares(ms)) by = row_scale(top[0], a.eps);
+      sums[0] = sums[1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        float(&f)[V] = w[kAhead ? i : 0];
+        if (!kAhead) weights<kWhole, V>(wp, (i * lanes + lane) * V, a.d, f);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          h[i][j] *= by;
+          sums[0] = fmaf(h[i][j], h[i][j], sums[0]);
+          sums[1] = fmaf(g[i][j] * f[j], h[i][j], sums[1]);
+        }
+      }
+      row_reduce<false>(sums, lanes, red);
+      ms = sums[0] / (float)a.d + a.eps * by * by;
+    }
+    const float rn = inv_rms(ms), rs = rn * by;  // of the row in registers, of h
+    const float m = sums[1] / (float)a.d * rn * rn;
     if (!live) continue;  // the block's last turn
     T* op = static_cast<T*>(a.dh.p) + at.b * a.dh.sb + at.h * a.dh.sh + at.t * a.dh.st;
 #pragma unroll
@@ -376,7 +443,7 @@ __device__ __forceinline__ void norm_back(const NormBwdArgs& a, int lanes, int64
       unpack<T>(res[i], o);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        dw[i][j] = fmaf(g[i][j], h[i][j] * rs, dw[i][j]);
+        dw[i][j] = fmaf(g[i][j], h[i][j] * rn, dw[i][j]);
         o[j] = fmaf(rs, fmaf(g[i][j], f[j], -h[i][j] * m), a.dres.p ? o[j] : 0.f);
       }
       write_row<kWhole, T, V>(op + c, a.d - c, a.wide, o);

@@ -1,10 +1,12 @@
-"""RMS norm on the GPU where a rounding decides: 8-bit values next to the middle between two."""
+"""RMS norm on the GPU where a rounding decides (8-bit values next to the middle between two) and
+where squares leave fp32's range."""
 import numpy as np
 import pytest
 import torch
 
 from linear_attention_ttt_b200 import ops
-from tests.test_parity_block_gpu import BF16, F32, clean
+from oracle import block_oracle as O
+from tests.test_parity_block_gpu import BF16, F32, clean, close, gen, num, tokens
 
 pytestmark = pytest.mark.gpu
 
@@ -70,4 +72,74 @@ def test_8_bit_values_of_small_and_infinite_rows():
     assert torch.equal(s.cpu()[0, :, 0], torch.from_numpy(scale[:, 0]))
     got = q.float().cpu()[0, :, 0]
     assert torch.equal(torch.isnan(got), torch.isnan(want)) and torch.equal(got.nan_to_num(1), want.nan_to_num(1))
+    clean()
+
+
+# ---- rows whose squares fp32 does not hold ------------------------------------------------------
+
+SIZES = [-140, -126, -100, -75, -64, -55, -45, -20, 0, 50, 58, 62, 64, 90, 120]  # powers of two
+
+
+def sized_rows(g, d, dtype):
+    """A token of every size, beside one another: rows of both kinds share a warp."""
+    x = tokens(g, 2, 2, len(SIZES), d, dtype)
+    return x.mul_(torch.tensor([2.0 ** e for e in SIZES]).cuda().to(dtype)[:, None])
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-36, 1e-28, 1e-6, 1e30])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [7, 64, 256, 1024, 2048, 2056, 9000])
+def test_rows_of_every_size(d, dtype, eps):
+    """x / rms(x) does not depend on x's size, as long as x is representable. The bounds are
+    those of rows of an ordinary size: a power of two in front changes no rounding."""
+    g = gen(d)
+    x = sized_rows(g, d, dtype)
+    w = (1 + 0.1 * torch.randn(2, d, generator=g)).cuda()
+    want = O.rms_norm(num(x), num(w)[:, None], eps)
+    y, _, _ = ops.rms_norm_fwd(x, w, eps)
+    close(y, want, np.abs(want), 8 + d / 16, "y")
+    q, s, _ = ops.rms_norm_fwd(x, w, eps, quant=True)
+    top = np.abs(want).max(-1)
+    close(s, top / 448, top / 448, 8 + d / 16, "scale")
+    # the largest row's size bounds e4m3's own errors, the scale's and the value's
+    off = np.abs(num(q) * num(s)[..., None] - want) / np.maximum(top, 1e-30)[..., None]
+    assert (off <= 2.0 ** -4 + (8 + d / 16) * 3 * 2.0 ** -21 + 1e-9).all()
+    clean()
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-28, 1e-6])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [7, 64, 256, 1024, 2056, 9000])
+def test_gradients_of_rows_of_every_size(d, dtype, eps):
+    g = gen(d + 1)
+    h = sized_rows(g, d, dtype)[:, :, 1:]  # not the denormal ones
+    dy = tokens(g, 2, 2, len(SIZES) - 1, d, dtype, "htd")
+    dy.mul_(torch.tensor([2.0 ** (e / 2) for e in SIZES[1:]]).cuda().to(dtype)[:, None])
+    for w in ((1 + 0.1 * torch.randn(2, d, generator=g)).cuda(), (1 + 0.1 * torch.randn(d, generator=g)).cuda()):
+        wn = num(w)[:, None] if w.dim() == 2 else num(w)
+        dh, dw = ops.rms_norm_bwd(h, w, dy, eps)
+        want, rows = O.rms_norm_bwd(num(h), wn, num(dy), eps)
+        hn, dn = np.abs(num(h)), np.abs(num(dy) * wn)
+        r = 1 / np.sqrt((hn * hn).mean(-1, keepdims=True) + eps)
+        mag = r * (dn + hn * r * (dn * hn * r).mean(-1, keepdims=True))
+        close(dh, want, mag, 12 + d / 8, "dh")
+        axes = (0, 2) if w.dim() == 2 else (0, 1, 2)
+        close(dw, rows.sum(axes), np.abs(rows).sum(axes), 12 + d / 16 + 4 * len(SIZES), "dw")
+    clean()
+
+
+def test_infinite_and_empty_rows_among_sized_ones():
+    x = sized_rows(gen(1), 64, F32)
+    x[0, 0, 3] = 0
+    x[0, 1, 4, 7] = float("inf")
+    x[1, 0, 5, 9] = float("nan")
+    y, _, _ = ops.rms_norm_fwd(x, torch.ones(64).cuda(), 0.0)
+    assert (y[0, 0, 3] == 0).all()
+    assert torch.isnan(y[0, 1, 4, 7]) and (y[0, 1, 4, :7] == 0).all()      # a finite value over an infinite one
+    assert torch.isnan(y[1, 0, 5]).all()
+    x[0, 1, 4], x[1, 0, 5] = 0, 0
+    rest, _, _ = ops.rms_norm_fwd(x, torch.ones(64).cuda(), 0.0)
+    keep = torch.ones(2, 2, len(SIZES), dtype=torch.bool).cuda()
+    keep[0, 1, 4] = keep[1, 0, 5] = False
+    assert torch.equal(y[keep], rest[keep])
     clean()
