@@ -518,7 +518,8 @@ ttt_status selective_scan_fwd(const ttt_tensor* x, const ttt_tensor* dt, const t
  *  dA [H,d,N] fp32; dBm, dCm [B,G,T,N] of x's type, summed over the channels
  *  that share them; dD, ddt_bias [H,d] fp32 (each required iff its input is
  *  given); dh0 NULL or as h0 (requires h0)
- * Workspace: at most 16 bytes x B*H*T*ceil(N/16) x d rounded up to 64.
+ * Workspace: at most 17 bytes x B*H x (T rounded up to 32) x ceil(N/16) x
+ * (d rounded up to 64).
  */
 ttt_status selective_scan_bwd(const ttt_tensor* x, const ttt_tensor* dt, const ttt_tensor* A,
                               const ttt_tensor* Bm, const ttt_tensor* Cm, const ttt_tensor* D,
