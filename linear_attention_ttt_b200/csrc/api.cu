@@ -1034,7 +1034,7 @@ ttt_status rms_norm_fwd(const ttt_tensor* x, const ttt_tensor* residual,
   a.x = view(x);
   a.r = view_or_null(residual);
   a.w = ptr<const float>(weight);
-  a.wide = a.wide && aligned16(a.w) && n.d % 4 == 0;
+  a.wide = a.wide && aligned16(a.w);
   a.eps = eps;
   a.out = rows_view(out);
   a.rout = rows_view(residual_out);
@@ -1068,7 +1068,7 @@ ttt_status rms_norm_bwd(const ttt_tensor* h, const ttt_tensor* weight, const ttt
   a.dy = view(dy);
   a.dres = view_or_null(dres);
   a.w = ptr<const float>(weight);
-  a.wide = a.wide && aligned16(a.w) && n.d % 4 == 0;
+  a.wide = a.wide && aligned16(a.w);
   a.eps = eps;
   a.dh = view_mut(dh);
   a.dw = ptr(dweight);

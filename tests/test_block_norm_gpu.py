@@ -143,3 +143,35 @@ def test_infinite_and_empty_rows_among_sized_ones():
     keep[0, 1, 4] = keep[1, 0, 5] = False
     assert torch.equal(y[keep], rest[keep])
     clean()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [2, 9, 63, 1023, 2049, 4099, 8195, 16383])
+def test_aligned_rows_of_any_length(d, dtype):
+    """Rows that 4 does not divide move 16 bytes at a time but for their last elements: NaN lies
+    behind every row, in the inputs and in what an output's row has behind its end."""
+    g = gen(d)
+    B, H, T = 1, 2, 5
+    x, r, dy = (tokens(g, B, H, T, d, dtype, o) for o in ("thd", "htd", "thd"))
+    w = (1 + 0.1 * torch.randn(H, d, generator=g)).cuda()
+    wn, sn = num(w)[:, None], num(x) + num(r)
+    want = O.rms_norm(sn, wn, 1e-5)
+    pad = -(-d // 16) * 16
+    for quant in (False, True):
+        out = torch.full((B, H, T, pad), 3.0, device="cuda").to(torch.float8_e4m3fn if quant else dtype)
+        got, s, h = ops.rms_norm_fwd(x, w, 1e-5, residual=r, quant=quant, out=out[..., :d])
+        assert (out[..., d:].float() == 3).all()
+        close(h, sn, np.abs(num(x)) + np.abs(num(r)), 1, "sum")
+        if not quant:
+            close(got, want, np.abs(want), 8 + d / 16, "y")
+        else:
+            top, scale = np.abs(want).max(-1)[..., None], num(s)[..., None]
+            off = np.abs(num(got) * scale - want)
+            assert (off <= np.maximum(np.abs(want) * 2.0 ** -4, scale * 2.0 ** -10) + (8 + d / 16) * 3 * 2.0 ** -21 * top).all()
+    dh, dw = ops.rms_norm_bwd(x, w, dy, 1e-5)
+    want, rows = O.rms_norm_bwd(num(x), wn, num(dy), 1e-5)
+    hn, dn = np.abs(num(x)), np.abs(num(dy) * wn)
+    rs = 1 / np.sqrt((hn * hn).mean(-1, keepdims=True) + 1e-5)
+    close(dh, want, rs * (dn + hn * rs * (dn * hn * rs).mean(-1, keepdims=True)), 12 + d / 8, "dh")
+    close(dw, rows.sum((0, 2)), np.abs(rows).sum((0, 2)), 12 + d / 16 + B * T, "dw")
+    clean()
