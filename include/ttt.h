@@ -385,6 +385,14 @@ ttt_status lact_swiglu_window_fwd(const ttt_tensor* q, const ttt_tensor* k, cons
  * their element, and rows may start anywhere. Where all token rows of a call
  * are 16-byte aligned they move 16 bytes at a time, else one by one.
  * Arithmetic, sums and states are fp32; a 16-bit output is rounded once.
+ * Exponentials, reciprocals, silu and its derivative come from the
+ * special-function unit: 2^-22 relative beside the rounding of an exponent
+ * (2^-24 of its size), and 0 where a result would be denormal, so that silu is
+ * 0 below about -87.
+ *
+ * Sizes: B*H and S*H up to 2^24, T up to 2^30, d up to 2^20, B*H*ceil(d/32) up
+ * to 2^24, B*H*T up to 2^40, and 65535 rows in a single-token call;
+ * TTT_ERR_UNSUPPORTED beyond.
  *
  * Packed sequences: with cu_seqlens (TTT_I32, contiguous, [S+1], on the
  * device) B is 1 and sequence i is the tokens cu_seqlens[i] ..
@@ -497,6 +505,10 @@ ttt_status causal_conv_step(const ttt_tensor* x, const ttt_tensor* state, const 
  *  h0      NULL (zero) or [S,H,d,N] fp32 contiguous; cu_seqlens as above
  *  softplus 0 or 1
  *  h_final NULL or [S,H,d,N] fp32 contiguous: the state after the last token
+ * Long sequences are cut into chunks, whose decays exp(A sum D_t) join them:
+ * a state that grows (A D_t > 0) by more than fp32's range, e^88, within a
+ * chunk may come out as infinite or NaN, as may its gradients, where token by
+ * token it would not.
  */
 ttt_status selective_scan_fwd(const ttt_tensor* x, const ttt_tensor* dt, const ttt_tensor* A,
                               const ttt_tensor* Bm, const ttt_tensor* Cm, const ttt_tensor* D,

@@ -1,7 +1,7 @@
 // Native half of the Python binding for the recurrent block's entry points
 // (include/ttt.h): fills the ttt_tensor descriptors from torch tensors and
 // calls the C function, about 1 us instead of the 15 us that building a dozen
-// descriptors in Python takes. A single-token step's kernel runs 3 to 6 us.
+// descriptors in Python takes. A single-token call is 7 to 9 us in all.
 //
 // call(function, tensors, split, scalar, stream, name) -> status. `function` is the
 // C function's address (from the loaded library), `tensors` a tuple of tensors

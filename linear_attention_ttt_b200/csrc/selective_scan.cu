@@ -11,9 +11,9 @@
 // What bounds it: one exponential and four fp32 operations per (channel,
 // state, token), and four special functions per element beside them. The
 // special-function unit gives 16 a clock and SM: at N = 16 that is 3.5 times the
-// memory traffic's time. B16 T1024 d4096 takes 482 us, 290 of them the unit's own
+// memory traffic's time. B16 T1024 d4096 takes 483 us, 290 of them the unit's own
 // (60 % busy); B4 T4096 d4096, with two warps a scheduler and nothing to hide
-// their latencies behind, 637 (50 %).
+// their latencies behind, 648 (50 %).
 //
 // The raw rows of a part arrive by asynchronous copies while the part before is
 // scanned; a token's decays are computed while the token before is; the sums
@@ -336,7 +336,7 @@ __global__ void copy_empty_kernel(Seqs q, int T, int64_t n, const float* src, fl
 // them of four channels: places and slots are found once for 16 states. What a
 // channel needs once (its step size, the gate) one of its lanes computes for
 // the others. The states are read and written once, in 16-byte pieces:
-// 64 sequences, d4096 N16 bf16, take 9.2 us a call (5.5 at the measured copy
+// 64 sequences, d4096 N16 bf16, take 9.3 us a call (5.5 at the measured copy
 // rate), waiting on their loads.
 constexpr int kStepThreads = 128, kStepCh = 4;
 
