@@ -64,9 +64,10 @@ def build_binding(force: bool = False) -> str:
     built again when its source or what it is compiled against has changed."""
     newest = max(os.path.getmtime(f) for f in (BINDING_SRC, os.path.join(ROOT, "include", "ttt.h")))
     key, stamp = binding_key(), os.path.join(BUILD, "binding.key")
-    if (not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest
-            and os.path.exists(stamp) and open(stamp).read() == key):
-        return BINDING
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest and os.path.exists(stamp):
+        with open(stamp) as f:
+            if f.read() == key:
+                return BINDING
     import sysconfig
 
     import torch

@@ -345,7 +345,9 @@ def _on_stream(op):
     def call(*args, stream=None, **kwargs):
         if stream is None:
             return op(*args, **kwargs)
-        device = next(t.device for t in (*args, *kwargs.values()) if torch.is_tensor(t))
+        device = next((t.device for t in (*args, *kwargs.values()) if torch.is_tensor(t)), None)
+        if device is None:
+            return op(*args, **kwargs)  # says what is missing
         if not hasattr(stream, "cuda_stream"):
             handle = int(stream)
             stream = (torch.cuda.ExternalStream(handle, device=device) if handle

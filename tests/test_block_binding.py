@@ -143,6 +143,13 @@ def test_a_stream_of_another_device_is_refused(name, reached, monkeypatch):
     assert not reached
 
 
+@pytest.mark.parametrize("name", arguments())
+def test_a_stream_and_no_tensor(name, reached):
+    with pytest.raises(TypeError):
+        getattr(ops, name)(stream=7)
+    assert not reached
+
+
 # ---- first calls ------------------------------------------------------------------------------
 
 FIRST_CALLS = """
