@@ -506,8 +506,9 @@ int bwd_blocks(const NormBwdArgs& a) {
 // weights are found once, and four loads are in flight.
 constexpr int kShortRows = 4;
 // A warp a row, without barriers, up to 256 vectors: B4 T4096 d2048 with 8-bit
-// output takes 43 us (5.4 TB/s), a block of 128 threads a row 59 us. The backward pass has
-// no registers for that beside its share of dweight.
+// output takes 43 us (5.4 TB/s), a block of 128 threads a row 59 us. Wider rows do not fit
+// a warp's registers and take a block each: as many elements in rows of 4096 68 us, in rows
+// of 8192 100 us. The backward pass has no registers for it beside its share of dweight.
 constexpr int kFwdVpt = 8;
 
 template <typename T>
